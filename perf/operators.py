@@ -232,7 +232,7 @@ def prepare(case, seed):
         s |= _paged(case, g, lens)
         counts = [max(1, int(n * case["part"])) for n in lens]
         first = [int((n - c) * 0.37) if i % 2 else n - c for i, (n, c) in enumerate(zip(lens, counts))]
-        s["first"], s["cu"], s["max_n"], s["max_len"] = _i32(first), _i32(_cu(counts)), max(counts), max(lens)
+        s["first"], s["cu"], s["max_len"] = _i32(first), _i32(_cu(counts)), max(lens)
         s["out"] = [torch.empty(sum(counts), case["hkv"], D, dtype=DTYPES[case["dtype"]], device="cuda")
                     for _ in range(2)]
     if own:
@@ -284,8 +284,7 @@ def _own_append(s):
 def _own_read(s):
     import kv_cache_quantization_x128_gb300 as kv
 
-    kv.kvarn_read_tokens(s["cache"], s["ws"], s["tables"], s["lens"], s["cu"], s["max_n"], *s["out"], s["meta"],
-                         first=s["first"])
+    kv.kvarn_read_tokens(s["cache"], s["ws"], s["tables"], s["lens"], s["cu"], *s["out"], s["meta"], first=s["first"])
     return s["out"]
 
 
