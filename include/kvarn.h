@@ -139,6 +139,7 @@ typedef enum {
 #define KVARN_FLAG_BAD_BLOCK 0x2u      /* block index outside [0, num_blocks): skipped */
 #define KVARN_FLAG_BAD_LENGTH 0x4u     /* seq_len > max_blocks_per_seq*128: clipped   */
 #define KVARN_FLAG_WAIT_TIMEOUT 0x8u   /* a bounded wait on a copy gave up            */
+#define KVARN_FLAG_BAD_INDEX 0x10u     /* an index of a new token is outside its chunk */
 
 typedef struct {
   int32_t num_kv_heads;       /* Hkv >= 1                                         */
@@ -153,6 +154,22 @@ typedef struct {
   int32_t max_blocks_per_seq; /* row length of block_tables                       */
   int32_t layout;             /* 0, or KVARN_LAYOUT_LEAN with k4v2 (preset k4v2l) */
 } kvarn_meta;
+
+/* Element types of model rows (kvarn_qk_norm_rope's inputs, kvarn_read_tokens' outputs). */
+#define KVARN_F16 0
+#define KVARN_BF16 1
+#define KVARN_F32 2
+
+/* kvarn_qk_norm_rope's rows, rotation and norm. */
+typedef struct {
+  int32_t dtype;        /* KVARN_F16, KVARN_BF16 or KVARN_F32: q, k, v and the weights */
+  int32_t rotary_dim;   /* rotated channels of a head, the first ones: 16, 32, 64, 128 */
+  int32_t interleaved;  /* 0: pairs (i, i + rotary_dim/2); 1: pairs (2i, 2i + 1)       */
+  float norm_eps;       /* added to the mean square, in (0, 1)                         */
+  int64_t q_stride;     /* elements between tokens' rows; whole multiples of 16 bytes  */
+  int64_t k_stride;
+  int64_t v_stride;
+} kvarn_rope;
 
 /* Bytes of one (block, kv-head) record of the default preset k4v2: 14336. */
 KVARN_API size_t kvarn_record_bytes(void);
@@ -323,6 +340,76 @@ KVARN_API kvarn_status kvarn_prefill_attention(const uint16_t* q, const uint16_t
                                      int32_t max_chunk, const int32_t* block_tables, const uint8_t* cache,
                                      const uint16_t* workspace, uint16_t* out, const kvarn_meta* meta,
                                      void* stream);
+
+/*
+ * Norm and rotation of a model's projected rows: what a step runs before
+ * kvarn_append_* and the attention calls, in one launch. Per token and head of q and k:
+ *   x <- x / sqrt(mean(x^2) + norm_eps) * weight     (skipped where the weight is NULL)
+ *   (a, b) <- (a cos t - b sin t, b cos t + a sin t), t = positions[token] * inv_freq[i],
+ * for pair i of the first rotary_dim channels (skipped where inv_freq is NULL); v is
+ * converted only. fp32 arithmetic, angles exact at any position, one rounding to fp16.
+ * No counterpart on the pages, whose engine does this before its cache write.
+ *   q, k, v       rows of rope->dtype: token t's heads are at q + t * q_stride, head h
+ *                 at + 128 h (so slices of one fused projection work). v may be NULL,
+ *                 v_out is not used then.
+ *   q_weight, k_weight  rope->dtype [128] or NULL.
+ *   inv_freq      float [rotary_dim / 2] or NULL: radians a position.
+ *   positions     int32 [n_tokens] (may be NULL where inv_freq is).
+ *   n_tokens      0 .. 2^31 - 1.
+ *   q_out, k_out, v_out  fp16 [n_tokens][heads][128]. They may be the inputs themselves
+ *                 (fp16, contiguous rows); otherwise they must not overlap them.
+ */
+KVARN_API kvarn_status kvarn_qk_norm_rope(const void* q, const void* k, const void* v, const kvarn_rope* rope,
+                                          const void* q_weight, const void* k_weight, const float* inv_freq,
+                                          const int32_t* positions, int64_t n_tokens, uint16_t* q_out,
+                                          uint16_t* k_out, uint16_t* v_out, const kvarn_meta* meta, void* stream);
+
+/*
+ * Append of several tokens a sequence, e.g. the drafted tokens that a verify step
+ * accepted, or the rest of a prompt behind its whole tiles: kvarn_append_decode for
+ * n(s) = 0..128 tokens of sequence s at once, in one launch. The i-th goes to workspace
+ * slot (L + i) % 128, L = seq_lens[s]; a tile that is completed is quantized into block
+ * block_tables[s][L / 128], the tokens behind it begin the next one.
+ *   k_new, v_new  fp16 [n_tokens][num_kv_heads][128]; sequence s's rows are cu_tokens[s]
+ *                 .. cu_tokens[s+1]-1 (int32 [n_seqs + 1], non-decreasing).
+ *   accepted      int32 [n_seqs][max_accept]: the rows to append, counted from
+ *                 cu_tokens[s], in sequence order; an index outside the sequence's rows
+ *                 leaves its slot as it was and raises KVARN_FLAG_BAD_INDEX. NULL: all
+ *                 rows of the sequence, in order (n_accepted must be NULL too).
+ *   n_accepted    int32 [n_seqs]: n(s).
+ *                 A sequence with n(s) outside 0..min(max_accept, 128) appends nothing
+ *                 and raises KVARN_FLAG_BAD_LENGTH; one with a negative length appends
+ *                 nothing and keeps its seq_lens_out.
+ *   max_accept    row length of accepted, >= 0.
+ *   seq_lens_out  int32 [n_seqs] or NULL: receives L + n(s). Must not alias seq_lens.
+ * A completed tile whose block does not exist is dropped and flagged, as in
+ * kvarn_append_decode. k_new and v_new must not overlap the workspace.
+ */
+KVARN_API kvarn_status kvarn_append_tokens(const uint16_t* k_new, const uint16_t* v_new, const int32_t* cu_tokens,
+                                           int64_t n_tokens, const int32_t* accepted, const int32_t* n_accepted,
+                                           int32_t max_accept, const int32_t* seq_lens, int32_t* seq_lens_out,
+                                           const int32_t* block_tables, int32_t n_seqs, uint16_t* workspace,
+                                           uint8_t* cache, const kvarn_meta* meta, void* stream);
+
+/*
+ * Cached tokens back as plain rows: tokens first[s] .. first[s] + n - 1 of sequence s, n =
+ * cu_tokens[s+1] - cu_tokens[s], into rows cu_tokens[s] .. of k_out and v_out (to hand
+ * a sequence to another engine, to keep a prefix elsewhere, to check a cache). A packed
+ * token is H (r c (code s + z)) in fp32, rounded once to `dtype`; a token of the partial
+ * last tile is the workspace's. One launch, no scratch.
+ *   first         int32 [n_seqs] or NULL: 0.
+ *   cu_tokens     int32 [n_seqs + 1], non-decreasing.
+ *   n_tokens      rows of k_out and v_out (0 .. 2^31 - 1); rows behind it are not written.
+ *   dtype         KVARN_F16, KVARN_BF16 or KVARN_F32.
+ *   k_out, v_out  [n_tokens][num_kv_heads][128] of dtype. Rows of tokens that are not
+ *                 there (outside 0..seq_lens[s]-1, or in the partial tile with workspace
+ *                 NULL: KVARN_FLAG_BAD_LENGTH; in a block outside [0, num_blocks):
+ *                 KVARN_FLAG_BAD_BLOCK) and of no sequence stay as they were.
+ */
+KVARN_API kvarn_status kvarn_read_tokens(const uint8_t* cache, const uint16_t* workspace, const int32_t* block_tables,
+                                         const int32_t* seq_lens, const int32_t* first, const int32_t* cu_tokens,
+                                         int32_t n_seqs, int64_t n_tokens, int32_t dtype, void* k_out, void* v_out,
+                                         const kvarn_meta* meta, void* stream);
 
 /*
  * Self-test of the give-up path of the library's bounded waits (failure

@@ -19,7 +19,8 @@ HEAD_DIM = 128
 BLOCK_SIZE = 128
 
 KVARN_OK, KVARN_EINVAL, KVARN_EUNSUPPORTED, KVARN_EALIGN, KVARN_ESCRATCH, KVARN_ECUDA = range(6)
-FLAG_BAD_SLOTS, FLAG_BAD_BLOCK, FLAG_BAD_LENGTH, FLAG_WAIT_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+FLAG_BAD_SLOTS, FLAG_BAD_BLOCK, FLAG_BAD_LENGTH, FLAG_WAIT_TIMEOUT, FLAG_BAD_INDEX = 0x1, 0x2, 0x4, 0x8, 0x10
+KVARN_F16, KVARN_BF16, KVARN_F32 = range(3)
 KVARN_WAIT_MBARRIER, KVARN_WAIT_GRID = 0, 1
 
 # exported entry points and their C signatures (include/kvarn.h)
@@ -48,6 +49,11 @@ _SIGS = {
                                                ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                                ctypes.c_void_p]),
+    "kvarn_qk_norm_rope": (ctypes.c_int, [ctypes.c_void_p] * 8 + [ctypes.c_int64] + [ctypes.c_void_p] * 5),
+    "kvarn_append_tokens": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_int64] + [ctypes.c_void_p] * 2
+                            + [ctypes.c_int32] + [ctypes.c_void_p] * 3 + [ctypes.c_int32] + [ctypes.c_void_p] * 4),
+    "kvarn_read_tokens": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32]
+                          + [ctypes.c_void_p] * 4),
     "kvarn_check_bounded_waits": (ctypes.c_int, [ctypes.c_int32, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_size_t,
                                                  ctypes.c_void_p]),
     "kvarn_device_flags": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), ctypes.c_void_p]),
@@ -76,6 +82,13 @@ class KvarnMeta(ctypes.Structure):
         ("max_blocks_per_seq", ctypes.c_int32),
         ("layout", ctypes.c_int32),
     ]
+
+
+class KvarnRope(ctypes.Structure):
+    """Mirror of ``kvarn_rope``."""
+    _fields_ = [("dtype", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("norm_eps", ctypes.c_float), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
 
 
 # bit widths (keys, values) and metadata layout of the presets; k4v2 is
@@ -242,6 +255,109 @@ def kvarn_prefill_attention(q, k_new, v_new, cu_tokens, seq_lens, max_chunk: int
                                         _ptr(block_tables, "block_tables", torch.int32),
                                         _ptr(cache, "cache", torch.uint8), _ptr(workspace, "workspace", torch.float16),
                                         _ptr(out, "out", torch.float16), ctypes.byref(meta), _stream(stream)))
+
+
+def _dtype_code(t, name):
+    import torch
+    code = {torch.float16: KVARN_F16, torch.bfloat16: KVARN_BF16, torch.float32: KVARN_F32}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be torch.float16, torch.bfloat16 or torch.float32, got {t.dtype}")
+    return code
+
+
+def _device_call(lead, tensors, stream, call):
+    """call(stream handle) with `lead`'s device current: the calls below launch on the
+    device of their tensors, on its current stream unless one is given."""
+    import torch
+    if not lead.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    dev = lead.device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors are on {dev} and on {t.device}")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"tensors are on {dev}, the stream is on {stream.device}")
+    if dev.index == torch.cuda.current_device():
+        _check(call(ctypes.c_void_p((stream or torch.cuda.current_stream(dev)).cuda_stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(call(ctypes.c_void_p((stream or torch.cuda.current_stream(dev)).cuda_stream)))
+
+
+def _heads(t, name, n, heads, dtype):
+    """Row stride of a [n, heads, 128] tensor whose rows are contiguous inside."""
+    if t.dim() != 3 or tuple(t.shape) != (n, heads, HEAD_DIM):
+        raise ValueError(f"{name} must be [{n}, {heads}, {HEAD_DIM}], got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != HEAD_DIM):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    return t.stride(0)
+
+
+def kvarn_qk_norm_rope(q, k, v, positions, q_out, k_out, v_out, meta: KvarnMeta, q_weight=None, k_weight=None,
+                       norm_eps: float = 1e-6, inv_freq=None, interleaved: bool = False, stream=None):
+    """Per-head norm and rotation of projected rows. q [n, Hq, 128], k and v [n, Hkv, 128]
+    in fp16, bf16 or fp32, rows at any stride (slices of a fused projection); weights
+    [128] of the same type or None (no norm); positions int32 [n]; inv_freq float32
+    [rotary_dim / 2] or None (no rotation); outputs fp16, contiguous. v and v_out may be None."""
+    import torch
+    n, hq, hkv = int(q.shape[0]), meta.num_q_heads, meta.num_kv_heads
+    f16 = torch.float16
+    rope = KvarnRope(_dtype_code(q, "q"), HEAD_DIM if inv_freq is None else 2 * inv_freq.numel(), int(bool(interleaved)),
+                     norm_eps, _heads(q, "q", n, hq, q.dtype), _heads(k, "k", n, hkv, q.dtype),
+                     0 if v is None else _heads(v, "v", n, hkv, q.dtype))
+    args = (q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(), ctypes.byref(rope),
+            _ptr(q_weight, "q_weight", q.dtype, HEAD_DIM), _ptr(k_weight, "k_weight", q.dtype, HEAD_DIM),
+            _ptr(inv_freq, "inv_freq", torch.float32),
+            _ptr(positions, "positions", torch.int32, n), n, _ptr(q_out, "q_out", f16, n * hq * HEAD_DIM),
+            _ptr(k_out, "k_out", f16, n * hkv * HEAD_DIM),
+            None if v is None else _ptr(v_out, "v_out", f16, n * hkv * HEAD_DIM), ctypes.byref(meta))
+    _device_call(q, (k, v, positions, q_out, k_out, v_out, q_weight, k_weight, inv_freq), stream,
+                 lambda st: _lib.kvarn_qk_norm_rope(*args, st))
+
+
+def kvarn_append_tokens(k_new, v_new, cu_tokens, seq_lens, seq_lens_out, block_tables, workspace, cache, meta: KvarnMeta,
+                        accepted=None, n_accepted=None, stream=None):
+    """Several tokens a sequence into the cache. k_new, v_new: fp16 [n_tokens, Hkv, 128],
+    sequence s's rows cu_tokens[s] .. cu_tokens[s + 1] - 1 (int32 [n_seqs + 1]); accepted:
+    int32 [n_seqs, max_accept] rows counted from cu_tokens[s] with n_accepted int32
+    [n_seqs], or both None: all rows, in order; seq_lens / seq_lens_out: int32 [n_seqs]."""
+    import torch
+    n, n_seqs, f16, i32 = int(k_new.shape[0]), int(seq_lens.shape[0]), torch.float16, torch.int32
+    rows = n * meta.num_kv_heads * HEAD_DIM
+    width = 0
+    if accepted is not None:
+        if accepted.dim() != 2 or accepted.shape[0] != n_seqs:
+            raise ValueError(f"accepted must be [{n_seqs}, max_accept], got {list(accepted.shape)}")
+        width = int(accepted.shape[1])
+    args = (_ptr(k_new, "k_new", f16, rows), _ptr(v_new, "v_new", f16, rows),
+            _ptr(cu_tokens, "cu_tokens", i32, n_seqs + 1), n, _ptr(accepted, "accepted", i32),
+            _ptr(n_accepted, "n_accepted", i32, n_seqs), width, _ptr(seq_lens, "seq_lens", i32, n_seqs),
+            _ptr(seq_lens_out, "seq_lens_out", i32, n_seqs),
+            _ptr(block_tables, "block_tables", i32, n_seqs * meta.max_blocks_per_seq), n_seqs,
+            _ptr(workspace, "workspace", f16, n_seqs * meta.num_kv_heads * 32768), _ptr(cache, "cache", torch.uint8),
+            ctypes.byref(meta))
+    _device_call(seq_lens, (k_new, v_new, cu_tokens, accepted, n_accepted, seq_lens_out, block_tables, workspace, cache),
+                 stream, lambda st: _lib.kvarn_append_tokens(*args, st))
+
+
+def kvarn_read_tokens(cache, workspace, block_tables, seq_lens, cu_tokens, k_out, v_out, meta: KvarnMeta, first=None,
+                      stream=None):
+    """Cached tokens first[s] (None: 0) .. first[s] + n - 1 of sequence s, n =
+    cu_tokens[s + 1] - cu_tokens[s], as rows cu_tokens[s] .. of k_out and v_out
+    [n_tokens, Hkv, 128] (fp16, bf16 or fp32)."""
+    import torch
+    n, n_seqs, i32 = int(k_out.shape[0]), int(seq_lens.shape[0]), torch.int32
+    rows = n * meta.num_kv_heads * HEAD_DIM
+    args = (_ptr(cache, "cache", torch.uint8),
+            _ptr(workspace, "workspace", torch.float16, n_seqs * meta.num_kv_heads * 32768),
+            _ptr(block_tables, "block_tables", i32, n_seqs * meta.max_blocks_per_seq),
+            _ptr(seq_lens, "seq_lens", i32, n_seqs), _ptr(first, "first", i32, n_seqs),
+            _ptr(cu_tokens, "cu_tokens", i32, n_seqs + 1), n_seqs, n, _dtype_code(k_out, "k_out"),
+            _ptr(k_out, "k_out", None, rows), _ptr(v_out, "v_out", k_out.dtype, rows), ctypes.byref(meta))
+    _device_call(k_out, (v_out, cache, workspace, block_tables, seq_lens, first, cu_tokens), stream,
+                 lambda st: _lib.kvarn_read_tokens(*args, st))
 
 
 def kvarn_check_bounded_waits(which: int, limit_us: int, scratch=None, stream=None):

@@ -253,6 +253,129 @@ kvarn_status kvarn_prefill_attention(const uint16_t* q, const uint16_t* k_new, c
                      "kvarn_prefill_attention");
 }
 
+kvarn_status kvarn_qk_norm_rope(const void* q, const void* k, const void* v, const kvarn_rope* rope,
+                                const void* q_weight, const void* k_weight, const float* inv_freq,
+                                const int32_t* positions, int64_t n_tokens, uint16_t* q_out, uint16_t* k_out,
+                                uint16_t* v_out, const kvarn_meta* meta, void* stream) {
+  g_err[0] = 0;
+  KV_TRY(check_meta(meta));
+  if (rope == nullptr) return fail(KVARN_EINVAL, "rope is NULL");
+  if (rope->dtype != KVARN_F16 && rope->dtype != KVARN_BF16 && rope->dtype != KVARN_F32)
+    return fail(KVARN_EUNSUPPORTED, "dtype must be KVARN_F16, KVARN_BF16 or KVARN_F32 (got %lld)", (long long)rope->dtype);
+  if (rope->rotary_dim != 16 && rope->rotary_dim != 32 && rope->rotary_dim != 64 && rope->rotary_dim != 128)
+    return fail(KVARN_EUNSUPPORTED, "rotary_dim must be 16, 32, 64 or 128 (got %lld)", (long long)rope->rotary_dim);
+  if (rope->interleaved != 0 && rope->interleaved != 1)
+    return fail(KVARN_EINVAL, "interleaved must be 0 or 1 (got %lld)", (long long)rope->interleaved);
+  if (!(rope->norm_eps > 0.0f) || !(rope->norm_eps < 1.0f)) return fail(KVARN_EINVAL, "norm_eps must be in (0, 1)");
+  if (n_tokens < 0 || n_tokens > INT32_MAX)
+    return fail(KVARN_EINVAL, "n_tokens must be in 0..2^31 - 1 (got %lld)", (long long)n_tokens);
+  const int64_t piece = rope->dtype == KVARN_F32 ? 4 : 8;   // elements of 16 bytes
+  const int64_t strides[3] = {rope->q_stride, rope->k_stride, rope->v_stride};
+  const int64_t widths[3] = {static_cast<int64_t>(meta->num_q_heads) * KVARN_HEAD_DIM,
+                             static_cast<int64_t>(meta->num_kv_heads) * KVARN_HEAD_DIM,
+                             static_cast<int64_t>(meta->num_kv_heads) * KVARN_HEAD_DIM};
+  for (int i = 0; i < (v != nullptr ? 3 : 2); ++i) {
+    if (n_tokens > 1 && strides[i] < widths[i])
+      return fail(KVARN_EINVAL, "the row stride of %c is smaller than a row (%lld)", "qkv"[i], (long long)strides[i]);
+    if (strides[i] % piece != 0)
+      return fail(KVARN_EALIGN, "the row stride of %c must be a multiple of 16 bytes (%lld elements)", "qkv"[i],
+                  (long long)strides[i]);
+  }
+  if (n_tokens == 0) return KVARN_OK;
+  KV_TRY(need_ptr(q, "q"));
+  KV_TRY(need_ptr(k, "k"));
+  KV_TRY(need_ptr(q_out, "q_out"));
+  KV_TRY(need_ptr(k_out, "k_out"));
+  if (v != nullptr) {
+    KV_TRY(need_ptr(v, "v"));
+    KV_TRY(need_ptr(v_out, "v_out"));
+  }
+  if (q_weight != nullptr) KV_TRY(need_ptr(q_weight, "q_weight"));
+  if (k_weight != nullptr) KV_TRY(need_ptr(k_weight, "k_weight"));
+  if (inv_freq != nullptr) {
+    KV_TRY(need_ptr(inv_freq, "inv_freq"));
+    KV_TRY(need_ptr(positions, "positions"));
+  }
+  return cuda_status(kvarn::launch_rope(q, k, v, rope, q_weight, k_weight, inv_freq, positions, n_tokens,
+                                        meta->num_q_heads, meta->num_kv_heads, q_out, k_out, v_out,
+                                        static_cast<cudaStream_t>(stream)),
+                     "kvarn_qk_norm_rope");
+}
+
+kvarn_status kvarn_append_tokens(const uint16_t* k_new, const uint16_t* v_new, const int32_t* cu_tokens,
+                                 int64_t n_tokens, const int32_t* accepted, const int32_t* n_accepted,
+                                 int32_t max_accept, const int32_t* seq_lens, int32_t* seq_lens_out,
+                                 const int32_t* block_tables, int32_t n_seqs, uint16_t* workspace, uint8_t* cache,
+                                 const kvarn_meta* meta, void* stream) {
+  g_err[0] = 0;
+  KV_TRY(check_meta(meta));
+  if (n_seqs < 0) return fail(KVARN_EINVAL, "n_seqs must be >= 0 (got %lld)", (long long)n_seqs);
+  if (static_cast<int64_t>(n_seqs) * meta->num_kv_heads > INT32_MAX / (2 * KVARN_BLOCK_SIZE))
+    return fail(KVARN_EINVAL, "n_seqs * num_kv_heads must be below 2^23 (got %lld)",
+                (long long)n_seqs * meta->num_kv_heads);
+  if (n_tokens < 0 || n_tokens > INT32_MAX)
+    return fail(KVARN_EINVAL, "n_tokens must be in 0..2^31 - 1 (got %lld)", (long long)n_tokens);
+  if (max_accept < 0) return fail(KVARN_EINVAL, "max_accept must be >= 0 (got %lld)", (long long)max_accept);
+  if ((accepted == nullptr) != (n_accepted == nullptr))
+    return fail(KVARN_EINVAL, "accepted and n_accepted must be given together");
+  if (n_seqs == 0) return KVARN_OK;
+  if (n_tokens > 0) {
+    KV_TRY(need_ptr(k_new, "k_new"));
+    KV_TRY(need_ptr(v_new, "v_new"));
+  }
+  KV_TRY(need_ptr(cu_tokens, "cu_tokens"));
+  if (accepted != nullptr) {
+    KV_TRY(need_ptr(accepted, "accepted"));
+    KV_TRY(need_ptr(n_accepted, "n_accepted"));
+  }
+  KV_TRY(need_ptr(seq_lens, "seq_lens"));
+  if (seq_lens_out != nullptr) KV_TRY(need_ptr(seq_lens_out, "seq_lens_out"));
+  if (seq_lens_out == seq_lens) return fail(KVARN_EINVAL, "seq_lens_out must not alias seq_lens");
+  KV_TRY(need_ptr(block_tables, "block_tables"));
+  KV_TRY(need_ptr(workspace, "workspace"));
+  KV_TRY(need_ptr(cache, "cache"));
+  if (meta->max_blocks_per_seq < 1) return fail(KVARN_EINVAL, "max_blocks_per_seq must be >= 1");
+  unsigned* fl = nullptr;
+  KV_TRY(flags_ptr(&fl));
+  return cuda_status(kvarn::launch_append_tokens(k_new, v_new, cu_tokens, n_tokens, accepted, n_accepted, max_accept,
+                                                 seq_lens, seq_lens_out, block_tables, n_seqs, meta->num_kv_heads,
+                                                 meta->max_blocks_per_seq, meta->num_blocks, workspace, cache,
+                                                 meta->k_bits, meta->v_bits, meta->layout == KVARN_LAYOUT_LEAN,
+                                                 meta->n_iters, meta->eps, fl, static_cast<cudaStream_t>(stream)),
+                     "kvarn_append_tokens");
+}
+
+kvarn_status kvarn_read_tokens(const uint8_t* cache, const uint16_t* workspace, const int32_t* block_tables,
+                               const int32_t* seq_lens, const int32_t* first, const int32_t* cu_tokens,
+                               int32_t n_seqs, int64_t n_tokens, int32_t dtype, void* k_out, void* v_out,
+                               const kvarn_meta* meta, void* stream) {
+  g_err[0] = 0;
+  KV_TRY(check_meta(meta));
+  if (dtype != KVARN_F16 && dtype != KVARN_BF16 && dtype != KVARN_F32)
+    return fail(KVARN_EUNSUPPORTED, "dtype must be KVARN_F16, KVARN_BF16 or KVARN_F32 (got %lld)", (long long)dtype);
+  if (n_seqs < 0) return fail(KVARN_EINVAL, "n_seqs must be >= 0 (got %lld)", (long long)n_seqs);
+  if (n_tokens < 0 || n_tokens > INT32_MAX)
+    return fail(KVARN_EINVAL, "n_tokens must be in 0..2^31 - 1 (got %lld)", (long long)n_tokens);
+  if (n_seqs == 0 || n_tokens == 0) return KVARN_OK;
+  KV_TRY(need_ptr(seq_lens, "seq_lens"));
+  if (first != nullptr) KV_TRY(need_ptr(first, "first"));
+  KV_TRY(need_ptr(cu_tokens, "cu_tokens"));
+  KV_TRY(need_ptr(k_out, "k_out"));
+  KV_TRY(need_ptr(v_out, "v_out"));
+  if (meta->max_blocks_per_seq > 0) {
+    KV_TRY(need_ptr(cache, "cache"));
+    KV_TRY(need_ptr(block_tables, "block_tables"));
+  }
+  if (workspace != nullptr) KV_TRY(need_ptr(workspace, "workspace"));
+  unsigned* fl = nullptr;
+  KV_TRY(flags_ptr(&fl));
+  return cuda_status(kvarn::launch_read(cache, workspace, block_tables, seq_lens, first, cu_tokens, n_seqs, n_tokens,
+                                        meta->num_kv_heads, meta->max_blocks_per_seq, meta->num_blocks, meta->k_bits,
+                                        meta->v_bits, meta->layout == KVARN_LAYOUT_LEAN, dtype, k_out, v_out, fl,
+                                        static_cast<cudaStream_t>(stream)),
+                     "kvarn_read_tokens");
+}
+
 kvarn_status kvarn_check_bounded_waits(int32_t which, uint32_t limit_us, void* scratch, size_t scratch_bytes,
                                        void* stream) {
   g_err[0] = 0;

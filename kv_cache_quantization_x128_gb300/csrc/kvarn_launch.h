@@ -51,6 +51,22 @@ cudaError_t launch_serve_step(const uint16_t* q, const uint16_t* k_new, const ui
                               uint16_t* ws, uint8_t* cache, int n_seqs, int hkv, int group, int max_blocks,
                               int64_t num_blocks, int k_bits, int v_bits, bool lean, int n_iters, float eps,
                               uint16_t* out, void* scratch, unsigned* flags, cudaStream_t stream);
+cudaError_t launch_append_tokens(const uint16_t* k_new, const uint16_t* v_new, const int32_t* cu_tokens,
+                                 int64_t n_tokens, const int32_t* accepted, const int32_t* n_accepted, int max_accept,
+                                 const int32_t* seq_lens, int32_t* seq_lens_out, const int32_t* block_tables,
+                                 int n_seqs, int hkv, int max_blocks, int64_t num_blocks, uint16_t* ws, uint8_t* cache,
+                                 int k_bits, int v_bits, bool lean, int n_iters, float eps, unsigned* flags,
+                                 cudaStream_t stream);
+
+cudaError_t launch_read(const uint8_t* cache, const uint16_t* ws, const int32_t* block_tables, const int32_t* seq_lens,
+                        const int32_t* first, const int32_t* cu_tokens, int n_seqs, int64_t n_tokens, int hkv,
+                        int max_blocks, int64_t num_blocks, int k_bits, int v_bits, bool lean, int dtype, void* k,
+                        void* v, unsigned* flags, cudaStream_t stream);
+
+cudaError_t launch_rope(const void* q, const void* k, const void* v, const kvarn_rope* r, const void* qw,
+                        const void* kw, const float* inv_freq, const int32_t* positions, int64_t n, int hq, int hkv,
+                        uint16_t* qo, uint16_t* ko, uint16_t* vo, cudaStream_t stream);
+
 // Device scratch of launch_decode: tile prefix per sequence + partial records, and
 // at its end kServeBarrierBytes for the serving step's grid barrier words.
 constexpr size_t kServeBarrierBytes = 256;

@@ -103,6 +103,7 @@ struct PrefillSource {
   int64_t num_blocks;
 
   static constexpr bool kSparse = false;   // every item has a tile
+  static constexpr bool kTail = false;
   __device__ int scatter_all(int, uint8_t*) const { return 0; }
   // every item has a tile: the block's next one
   __device__ int64_t next_item(int64_t w, int) const { return w + gridDim.x; }
@@ -134,7 +135,11 @@ struct PrefillSource {
   }
 };
 
-struct AppendSource {
+// kMulti: each sequence appends count(s) tokens of its part of k_new and v_new (0..128:
+// at most one tile completes) instead of one. The tokens behind a completed tile are the
+// next tile's first; they are written to the workspace once the tile's copy has landed.
+template <bool kMulti>
+struct AppendSourceT {
   CUtensorMap map;              // workspace as [n_seqs * hkv * 2 * 128 rows][128 channels] fp16
   const uint16_t* k_new;        // [n_seqs][hkv][128] fp16: the token appended to each sequence
   const uint16_t* v_new;
@@ -148,11 +153,61 @@ struct AppendSource {
   int max_blocks;
   int64_t num_blocks;
   int ranked;                   // the completing items are handed out by rank (see kRankItems)
+  // kMulti only
+  const int32_t* cu_tokens;     // [n_seqs + 1]: sequence s's rows of k_new and v_new
+  const int32_t* accepted;      // [n_seqs][max_accept] rows inside them, or NULL: all, in order
+  const int32_t* n_accepted;    // [n_seqs]
+  int max_accept;
+  int64_t n_tokens;             // rows of k_new and v_new
+  unsigned* flags;
 
   static constexpr bool kSparse = true;    // only items whose sequence completes a tile
+  static constexpr bool kTail = kMulti;    // tokens to write behind a completed tile
   __device__ bool needs_load(int64_t w) const {
-    const int L = seq_lens[hd.div(w)];
-    return L >= 0 && (L % kB) == kB - 1;
+    const uint32_t s = hd.div(w);
+    const int L = seq_lens[s];
+    if constexpr (kMulti) {
+      return L >= 0 && (L % kB) + count(s) >= kB;
+    } else {
+      return L >= 0 && (L % kB) == kB - 1;
+    }
+  }
+  // Tokens that sequence s appends (none where the given number is not in its range).
+  __device__ int given(uint32_t s) const {
+    return accepted != nullptr ? n_accepted[s] : cu_tokens[s + 1] - cu_tokens[s];
+  }
+  __device__ int count(uint32_t s) const {
+    const int n = given(s);
+    return n < 0 || n > kB || (accepted != nullptr && n > max_accept) ? 0 : n;
+  }
+  // Row of k_new and v_new of the i-th token that sequence s appends (-1: none such).
+  __device__ int64_t row_of(uint32_t s, int i) const {
+    const int64_t c0 = cu_tokens[s], c1 = cu_tokens[s + 1];
+    const int64_t j = accepted != nullptr ? accepted[static_cast<int64_t>(s) * max_accept + i] : i;
+    return j < 0 || c0 < 0 || c0 + j >= c1 || c1 > n_tokens ? -1 : c0 + j;
+  }
+  // Thread t of nt copies its 16-byte pieces of tokens [i0, i1) of item w, tensor g; slot 0
+  // of the workspace tile holds token i_slot0.
+  __device__ void copy_rows(int64_t w, int g, int t, int nt, int i0, int i1, int i_slot0) const {
+    const uint32_t s = hd.div(w);
+    const uint32_t h = static_cast<uint32_t>(w) - s * hkv;
+    for (int i = i0 + (t >> 4); i < i1; i += nt >> 4) {
+      const int64_t r = row_of(s, i);
+      if (r < 0) {
+        raise_flag(flags, KVARN_FLAG_BAD_INDEX);
+        continue;
+      }
+      const uint16_t* src = (g ? v_new : k_new) + (r * hkv + h) * kD + (t & 15) * 8;
+      uint16_t* dst = ws + ((static_cast<int64_t>(w) * 2 + g) * kB + (i - i_slot0)) * kD + (t & 15) * 8;
+      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+    }
+  }
+  // The tokens behind the completed tile of item w, whose tile of tensor g has landed in
+  // shared memory (the group's 256 threads).
+  __device__ void write_tail(int64_t w, int g, int gt) const {
+    const uint32_t s = hd.div(w);
+    const int split = kB - seq_lens[s] % kB;
+    copy_rows(w, g, gt, kGroupThreads, split, count(s), split);
   }
   __device__ void coords(int64_t w, int g, int& x, int& y) const {
     x = 0;
@@ -167,6 +222,16 @@ struct AppendSource {
     const uint32_t h = static_cast<uint32_t>(w) - s * hkv;
     const int L = seq_lens[s];
     if (L < 0) return;
+    if constexpr (kMulti) {
+      const int n = count(s);
+      copy_rows(w, g, t, 16, 0, min(n, kB - L % kB), -(L % kB));
+      if (g == 0 && h == 0 && t == 0) {
+        if (n != given(s)) raise_flag(flags, KVARN_FLAG_BAD_LENGTH);
+        if (seq_lens_out != nullptr) seq_lens_out[s] = L + n;
+      }
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      return;
+    }
     const uint16_t* src = (g ? v_new : k_new) + static_cast<int64_t>(w) * kD + t * 8;
     uint16_t* dst = ws + ((static_cast<int64_t>(w) * 2 + g) * kB + L % kB) * kD + t * 8;
     *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
@@ -277,7 +342,10 @@ struct AppendSource {
 };
 
 __device__ __forceinline__ const CUtensorMap* tensor_map(const PrefillSource& s, int g) { return &s.map[g]; }
-__device__ __forceinline__ const CUtensorMap* tensor_map(const AppendSource& s, int) { return &s.map; }
+template <bool kMulti>
+__device__ __forceinline__ const CUtensorMap* tensor_map(const AppendSourceT<kMulti>& s, int) {
+  return &s.map;
+}
 
 // Thread gt == 0 of group g starts the two TMA copies (64 channels each) of item
 // w's tile into `dst`, completing on `bar`.
@@ -342,11 +410,17 @@ __global__ void __maxnreg__(128)
   constexpr int kTmaThread = 64, kStoreThread = 32;
   uint8_t* tiles = smem + kOffIn + grp * 2 * kTileOp;   // this group's [buf]
 
+  uint8_t* rank = smem + S::kOffRank;
+  int n_mine = 0;
+  if constexpr (Src::kTail) {
+    // most steps complete no tile: a block without one is done once its rows are written
+    n_mine = src.scatter_all(tid, rank);
+    if (src.first_item(tid & 31, rank, n_mine) >= src.n_items) return;
+  }
   fill_hadamard_sw128(smem + kOffH, tid, kThreads);   // the +-1 Hadamard operand
   // appended tokens into the workspace (the block's items), ordered before any tile
   // copy by the barrier below
-  uint8_t* rank = smem + S::kOffRank;
-  const int n_mine = src.scatter_all(tid, rank);
+  if constexpr (!Src::kTail) n_mine = src.scatter_all(tid, rank);
   if (tid == 0) {
     for (int b = 0; b < 6; ++b) mbar_init(&mma_bar[b], 1);
     fence_mbar_init();
@@ -405,6 +479,9 @@ __global__ void __maxnreg__(128)
         load_parity ^= 1u << buf;
         pend &= ~(1u << buf);
       }
+    }
+    if constexpr (Src::kTail) {
+      if (ok) src.write_tail(item, grp, gt);   // the tile has been read: its rows may be overwritten
     }
     // the item's Hadamard products first, so the next item's bookkeeping below
     // (slot loads, the next tile copy) runs under them
@@ -617,7 +694,7 @@ cudaError_t launch_append(const uint16_t* k_new, const uint16_t* v_new, const in
                           int n_iters, float eps, unsigned* flags, cudaStream_t stream) {
   if (n_seqs <= 0) return cudaSuccess;
   if (static_cast<int64_t>(n_seqs) * hkv * 2 * kB > INT32_MAX) return cudaErrorInvalidValue;
-  AppendSource src{};
+  AppendSourceT<false> src{};
   const cudaError_t err = tile_map(&src.map, ws, kD, static_cast<uint64_t>(n_seqs) * hkv * 2 * kB);
   if (err != cudaSuccess) return err;
   src.k_new = k_new;
@@ -631,6 +708,39 @@ cudaError_t launch_append(const uint16_t* k_new, const uint16_t* v_new, const in
   src.hd = make_item_div(static_cast<uint32_t>(hkv));
   src.max_blocks = max_blocks;
   src.num_blocks = num_blocks;
+  const int64_t grid = std::min<int64_t>(sm_count(), src.n_items);
+  src.ranked = src.n_items <= kRankItems && (src.n_items + grid - 1) / grid <= kRankList;
+  return launch_quantize(src, cache, k_bits, v_bits, lean, n_iters, eps, flags, stream, 0);
+}
+
+cudaError_t launch_append_tokens(const uint16_t* k_new, const uint16_t* v_new, const int32_t* cu_tokens,
+                                 int64_t n_tokens, const int32_t* accepted, const int32_t* n_accepted, int max_accept,
+                                 const int32_t* seq_lens, int32_t* seq_lens_out, const int32_t* block_tables,
+                                 int n_seqs, int hkv, int max_blocks, int64_t num_blocks, uint16_t* ws, uint8_t* cache,
+                                 int k_bits, int v_bits, bool lean, int n_iters, float eps, unsigned* flags,
+                                 cudaStream_t stream) {
+  if (n_seqs <= 0) return cudaSuccess;
+  if (static_cast<int64_t>(n_seqs) * hkv * 2 * kB > INT32_MAX) return cudaErrorInvalidValue;
+  AppendSourceT<true> src{};
+  const cudaError_t err = tile_map(&src.map, ws, kD, static_cast<uint64_t>(n_seqs) * hkv * 2 * kB);
+  if (err != cudaSuccess) return err;
+  src.k_new = k_new;
+  src.v_new = v_new;
+  src.ws = ws;
+  src.seq_lens_out = seq_lens_out;
+  src.seq_lens = seq_lens;
+  src.block_tables = block_tables;
+  src.n_items = static_cast<int64_t>(n_seqs) * hkv;
+  src.hkv = hkv;
+  src.hd = make_item_div(static_cast<uint32_t>(hkv));
+  src.max_blocks = max_blocks;
+  src.num_blocks = num_blocks;
+  src.cu_tokens = cu_tokens;
+  src.accepted = accepted;
+  src.n_accepted = n_accepted;
+  src.max_accept = max_accept;
+  src.n_tokens = n_tokens;
+  src.flags = flags;
   const int64_t grid = std::min<int64_t>(sm_count(), src.n_items);
   src.ranked = src.n_items <= kRankItems && (src.n_items + grid - 1) / grid <= kRankList;
   return launch_quantize(src, cache, k_bits, v_bits, lean, n_iters, eps, flags, stream, 0);
