@@ -171,6 +171,16 @@ typedef struct {
   int64_t v_stride;
 } kvarn_rope;
 
+/* How kvarn_tree_attention turns q.k into a score. */
+typedef struct {
+  float scale;          /* factor of q.k; 0: 1/sqrt(128)                               */
+  float softcap;        /* > 0: scaled score x -> softcap * tanh(x / softcap); 0: none */
+  int32_t window;       /* W > 0: only keys whose position is > query's - W; 0: all    */
+  int32_t reserved;     /* 0 */
+  const float* slopes;  /* device float [num_q_heads] or NULL: -slope * (position of the
+                           query - position of the key) is added (after the cap)       */
+} kvarn_score;
+
 /* Bytes of one (block, kv-head) record of the default preset k4v2: 14336. */
 KVARN_API size_t kvarn_record_bytes(void);
 
@@ -363,6 +373,51 @@ KVARN_API kvarn_status kvarn_qk_norm_rope(const void* q, const void* k, const vo
                                           const void* q_weight, const void* k_weight, const float* inv_freq,
                                           const int32_t* positions, int64_t n_tokens, uint16_t* q_out,
                                           uint16_t* k_out, uint16_t* v_out, const kvarn_meta* meta, void* stream);
+
+/* The most new tokens of a sequence in one kvarn_tree_attention call. */
+#define KVARN_MAX_TREE 64
+
+/* Bytes of device scratch kvarn_tree_attention needs; 0 if an argument is invalid. */
+KVARN_API size_t kvarn_tree_scratch_bytes(const kvarn_meta* meta, int32_t n_seqs, int32_t max_tree);
+
+/*
+ * Attention of drafted tokens over the quantized cache (the verify step of speculative
+ * decoding; a reading of this library, the pages are silent on it). Each sequence s has
+ * L0 = seq_lens[s] cached tokens (floor(L0/128) packed tiles, then L0 % 128 workspace
+ * tokens) and new tokens cu_tokens[s] .. cu_tokens[s+1]-1, up to 64 of them. A new token
+ * attends the cached tokens and those new tokens of its sequence whose bits its word of
+ * tree_mask has: bit j is the sequence's j-th new token. Its own bit is not implied, and
+ * a token that attends nothing gets zeros. Nothing is written to the cache: append the
+ * accepted tokens with kvarn_append_tokens. The context is split over the GPU and
+ * merged, as in kvarn_decode_attention.
+ *   q, out        fp16 [n_tokens][num_q_heads][128].
+ *   k_new, v_new  fp16 [n_tokens][num_kv_heads][128].
+ *   tree_mask     uint64 [n_tokens], or NULL: a chain (each token attends those before
+ *                 it and itself).
+ *   positions     int32 [n_tokens], the new tokens' positions, used by score->window and
+ *                 score->slopes only (NULL without them); the cached tokens' are 0..L0-1.
+ *   cu_tokens     int32 [n_seqs + 1], non-decreasing, cu_tokens[0] >= 0; tokens outside
+ *                 every sequence keep their out rows.
+ *   n_tokens      rows of q, k_new, v_new and out, below 2^31 / num_q_heads. A sequence
+ *                 with a row outside 0..n_tokens-1 is not computed (KVARN_FLAG_BAD_LENGTH).
+ *   n_seqs        0..65535. max_tree: 1..64, an upper bound of a sequence's new tokens;
+ *                 of a longer sequence the tokens behind it are neither attended nor
+ *                 computed, and KVARN_FLAG_BAD_LENGTH is raised.
+ *   workspace     fp16 workspace or NULL (then L0 % 128 tokens are not attended and
+ *                 KVARN_FLAG_BAD_LENGTH is raised).
+ *   score         NULL: q.k / sqrt(128) as it is.
+ *   scratch       device buffer of >= kvarn_tree_scratch_bytes(meta, n_seqs, max_tree);
+ *                 calls that overlap on the GPU must not share it.
+ * Packed tiles in a block outside [0, num_blocks) are not attended (KVARN_FLAG_BAD_BLOCK),
+ * nor are those behind max_blocks_per_seq (KVARN_FLAG_BAD_LENGTH).
+ */
+KVARN_API kvarn_status kvarn_tree_attention(const uint16_t* q, const uint16_t* k_new, const uint16_t* v_new,
+                                            const uint64_t* tree_mask, const int32_t* positions,
+                                            const int32_t* cu_tokens, const int32_t* seq_lens, int32_t n_seqs,
+                                            int64_t n_tokens, int32_t max_tree, const int32_t* block_tables,
+                                            const uint8_t* cache, const uint16_t* workspace,
+                                            const kvarn_score* score, uint16_t* out, void* scratch,
+                                            size_t scratch_bytes, const kvarn_meta* meta, void* stream);
 
 /*
  * Append of several tokens a sequence, e.g. the drafted tokens that a verify step

@@ -21,6 +21,7 @@ BLOCK_SIZE = 128
 KVARN_OK, KVARN_EINVAL, KVARN_EUNSUPPORTED, KVARN_EALIGN, KVARN_ESCRATCH, KVARN_ECUDA = range(6)
 FLAG_BAD_SLOTS, FLAG_BAD_BLOCK, FLAG_BAD_LENGTH, FLAG_WAIT_TIMEOUT, FLAG_BAD_INDEX = 0x1, 0x2, 0x4, 0x8, 0x10
 KVARN_F16, KVARN_BF16, KVARN_F32 = range(3)
+KVARN_MAX_TREE = 64
 KVARN_WAIT_MBARRIER, KVARN_WAIT_GRID = 0, 1
 
 # exported entry points and their C signatures (include/kvarn.h)
@@ -50,6 +51,9 @@ _SIGS = {
                                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                                ctypes.c_void_p]),
     "kvarn_qk_norm_rope": (ctypes.c_int, [ctypes.c_void_p] * 8 + [ctypes.c_int64] + [ctypes.c_void_p] * 5),
+    "kvarn_tree_scratch_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32]),
+    "kvarn_tree_attention": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32]
+                             + [ctypes.c_void_p] * 6 + [ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
     "kvarn_append_tokens": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_int64] + [ctypes.c_void_p] * 2
                             + [ctypes.c_int32] + [ctypes.c_void_p] * 3 + [ctypes.c_int32] + [ctypes.c_void_p] * 4),
     "kvarn_read_tokens": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32]
@@ -89,6 +93,12 @@ class KvarnRope(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
                 ("norm_eps", ctypes.c_float), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
                 ("v_stride", ctypes.c_int64)]
+
+
+class KvarnScore(ctypes.Structure):
+    """Mirror of ``kvarn_score``."""
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("slopes", ctypes.c_void_p)]
 
 
 # bit widths (keys, values) and metadata layout of the presets; k4v2 is
@@ -315,6 +325,38 @@ def kvarn_qk_norm_rope(q, k, v, positions, q_out, k_out, v_out, meta: KvarnMeta,
             None if v is None else _ptr(v_out, "v_out", f16, n * hkv * HEAD_DIM), ctypes.byref(meta))
     _device_call(q, (k, v, positions, q_out, k_out, v_out, q_weight, k_weight, inv_freq), stream,
                  lambda st: _lib.kvarn_qk_norm_rope(*args, st))
+
+
+def tree_scratch_bytes(meta: KvarnMeta, n_seqs: int, max_tree: int) -> int:
+    return int(_lib.kvarn_tree_scratch_bytes(ctypes.byref(meta), n_seqs, max_tree))
+
+
+def kvarn_tree_attention(q, k_new, v_new, tree_mask, cu_tokens, seq_lens, max_tree: int, block_tables, cache, workspace,
+                         out, scratch, meta: KvarnMeta, positions=None, scale: float = 0.0, softcap: float = 0.0,
+                         window: int = 0, slopes=None, stream=None):
+    """Drafted tokens over the quantized cache. q, out: fp16 [n_tokens, Hq, 128]; k_new,
+    v_new: fp16 [n_tokens, Hkv, 128]; tree_mask: int64 (or uint64) [n_tokens], bit j = the
+    sequence's j-th new token is attended, None = a chain; cu_tokens: int32 [n_seqs + 1];
+    seq_lens: int32 [n_seqs], cached tokens; max_tree: at least every sequence's new tokens
+    (<= 64); scratch: at least tree_scratch_bytes(meta, n_seqs, max_tree) bytes. Scores:
+    scale (0: 1/sqrt(128)), softcap, window and slopes (float32 [Hq]), the last two over
+    positions (int32 [n_tokens])."""
+    import torch
+    n, n_seqs, f16, i32 = int(q.shape[0]), int(seq_lens.shape[0]), torch.float16, torch.int32
+    if tree_mask is not None and tree_mask.dtype not in (torch.int64, torch.uint64):
+        raise ValueError(f"tree_mask must be 64-bit integers, got {tree_mask.dtype}")
+    rows = n * meta.num_kv_heads * HEAD_DIM
+    score = KvarnScore(scale, softcap, window, 0, _ptr(slopes, "slopes", torch.float32, meta.num_q_heads))
+    args = (_ptr(q, "q", f16, n * meta.num_q_heads * HEAD_DIM), _ptr(k_new, "k_new", f16, rows),
+            _ptr(v_new, "v_new", f16, rows), _ptr(tree_mask, "tree_mask", None, n),
+            _ptr(positions, "positions", i32, n), _ptr(cu_tokens, "cu_tokens", i32, n_seqs + 1),
+            _ptr(seq_lens, "seq_lens", i32, n_seqs), n_seqs, n, int(max_tree),
+            _ptr(block_tables, "block_tables", i32, n_seqs * meta.max_blocks_per_seq),
+            _ptr(cache, "cache", torch.uint8), _ptr(workspace, "workspace", f16, n_seqs * meta.num_kv_heads * 32768),
+            ctypes.byref(score), _ptr(out, "out", f16, n * meta.num_q_heads * HEAD_DIM), _ptr(scratch, "scratch"),
+            0 if scratch is None else scratch.numel() * scratch.element_size(), ctypes.byref(meta))
+    _device_call(q, (k_new, v_new, tree_mask, positions, cu_tokens, seq_lens, block_tables, cache, workspace, out,
+                     scratch, slopes), stream, lambda st: _lib.kvarn_tree_attention(*args, st))
 
 
 def kvarn_append_tokens(k_new, v_new, cu_tokens, seq_lens, seq_lens_out, block_tables, workspace, cache, meta: KvarnMeta,

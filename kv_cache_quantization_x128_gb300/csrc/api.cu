@@ -302,6 +302,61 @@ kvarn_status kvarn_qk_norm_rope(const void* q, const void* k, const void* v, con
                      "kvarn_qk_norm_rope");
 }
 
+size_t kvarn_tree_scratch_bytes(const kvarn_meta* meta, int32_t n_seqs, int32_t max_tree) {
+  if (check_meta(meta) != KVARN_OK || n_seqs < 0 || n_seqs > 65535 || max_tree < 1 || max_tree > KVARN_MAX_TREE) return 0;
+  return kvarn::tree_scratch_bytes(n_seqs, meta->num_kv_heads, meta->num_q_heads / meta->num_kv_heads, max_tree);
+}
+
+kvarn_status kvarn_tree_attention(const uint16_t* q, const uint16_t* k_new, const uint16_t* v_new,
+                                  const uint64_t* tree_mask, const int32_t* positions, const int32_t* cu_tokens,
+                                  const int32_t* seq_lens, int32_t n_seqs, int64_t n_tokens, int32_t max_tree,
+                                  const int32_t* block_tables, const uint8_t* cache, const uint16_t* workspace,
+                                  const kvarn_score* score, uint16_t* out, void* scratch, size_t scratch_bytes,
+                                  const kvarn_meta* meta, void* stream) {
+  g_err[0] = 0;
+  KV_TRY(check_meta(meta));
+  if (n_seqs < 0 || n_seqs > 65535) return fail(KVARN_EINVAL, "n_seqs must be in 0..65535 (got %lld)", (long long)n_seqs);
+  if (n_tokens < 0 || n_tokens > INT32_MAX / meta->num_q_heads)
+    return fail(KVARN_EINVAL, "n_tokens must be in 0..2^31 / num_q_heads (got %lld)", (long long)n_tokens);
+  if (max_tree < 1 || max_tree > KVARN_MAX_TREE)
+    return fail(KVARN_EUNSUPPORTED, "max_tree must be in 1..64 (got %lld)", (long long)max_tree);
+  kvarn_score sc = {};
+  if (score != nullptr) sc = *score;
+  if (!(sc.scale >= 0.0f) || !(sc.scale <= 3.0e38f)) return fail(KVARN_EINVAL, "score scale must be finite and >= 0");
+  if (!(sc.softcap >= 0.0f) || !(sc.softcap <= 3.0e38f)) return fail(KVARN_EINVAL, "softcap must be finite and >= 0");
+  if (sc.window < 0) return fail(KVARN_EINVAL, "window must be >= 0 (got %lld)", (long long)sc.window);
+  if (sc.reserved != 0) return fail(KVARN_EINVAL, "score reserved must be 0");
+  if (sc.scale == 0.0f) sc.scale = 0.088388347648318440f;
+  if (n_seqs == 0 || n_tokens == 0) return KVARN_OK;
+  KV_TRY(need_ptr(q, "q"));
+  KV_TRY(need_ptr(k_new, "k_new"));
+  KV_TRY(need_ptr(v_new, "v_new"));
+  if (tree_mask != nullptr) KV_TRY(need_ptr(tree_mask, "tree_mask"));
+  if (sc.slopes != nullptr) KV_TRY(need_ptr(sc.slopes, "slopes"));
+  if (sc.slopes != nullptr || sc.window > 0 || positions != nullptr) KV_TRY(need_ptr(positions, "positions"));
+  KV_TRY(need_ptr(cu_tokens, "cu_tokens"));
+  KV_TRY(need_ptr(seq_lens, "seq_lens"));
+  KV_TRY(need_ptr(out, "out"));
+  if (meta->max_blocks_per_seq > 0) {
+    KV_TRY(need_ptr(cache, "cache"));
+    KV_TRY(need_ptr(block_tables, "block_tables"));
+  }
+  if (workspace != nullptr) KV_TRY(need_ptr(workspace, "workspace"));
+  const int group = meta->num_q_heads / meta->num_kv_heads;
+  const size_t need = kvarn::tree_scratch_bytes(n_seqs, meta->num_kv_heads, group, max_tree);
+  KV_TRY(need_ptr(scratch, "scratch"));
+  if (scratch_bytes < need)
+    return fail(KVARN_ESCRATCH, "scratch too small: need %lld bytes", static_cast<long long>(need));
+  unsigned* fl = nullptr;
+  KV_TRY(flags_ptr(&fl));
+  return cuda_status(kvarn::launch_tree(q, k_new, v_new, tree_mask, positions, cu_tokens, seq_lens, n_seqs, n_tokens,
+                                        max_tree, block_tables, cache, workspace, meta->num_kv_heads, group,
+                                        meta->max_blocks_per_seq, meta->num_blocks, meta->k_bits, meta->v_bits,
+                                        meta->layout == KVARN_LAYOUT_LEAN, sc, out, scratch, fl,
+                                        static_cast<cudaStream_t>(stream)),
+                     "kvarn_tree_attention");
+}
+
 kvarn_status kvarn_append_tokens(const uint16_t* k_new, const uint16_t* v_new, const int32_t* cu_tokens,
                                  int64_t n_tokens, const int32_t* accepted, const int32_t* n_accepted,
                                  int32_t max_accept, const int32_t* seq_lens, int32_t* seq_lens_out,

@@ -67,6 +67,14 @@ cudaError_t launch_rope(const void* q, const void* k, const void* v, const kvarn
                         const void* kw, const float* inv_freq, const int32_t* positions, int64_t n, int hq, int hkv,
                         uint16_t* qo, uint16_t* ko, uint16_t* vo, cudaStream_t stream);
 
+cudaError_t launch_tree(const uint16_t* q, const uint16_t* k_new, const uint16_t* v_new, const uint64_t* tree_mask,
+                        const int32_t* positions, const int32_t* cu_tokens, const int32_t* seq_lens, int n_seqs,
+                        int64_t n_tokens, int max_tree, const int32_t* block_tables, const uint8_t* cache,
+                        const uint16_t* ws, int hkv, int group, int max_blocks, int64_t num_blocks, int k_bits,
+                        int v_bits, bool lean, const kvarn_score& score, uint16_t* out, void* scratch, unsigned* flags,
+                        cudaStream_t stream);
+size_t tree_scratch_bytes(int n_seqs, int hkv, int group, int max_tree);
+
 // Device scratch of launch_decode: tile prefix per sequence + partial records, and
 // at its end kServeBarrierBytes for the serving step's grid barrier words.
 constexpr size_t kServeBarrierBytes = 256;

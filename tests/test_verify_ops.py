@@ -139,6 +139,39 @@ def test_rope_refuses_pointers_and_sizes(kv):
     assert f(None, None, None, r, None, None, None, None, 0, None, None, None, m, None) == 0
 
 
+def _tree(kv, m, score=None, n=4, tokens=8, max_tree=4, short=0, **ptr):
+    p = dict(q=A, k=A, v=A, mask=A, pos=A, cu=A, lens=A, bt=A, cache=A, ws=A, out=A, scratch=A) | ptr
+    need = kv.tree_scratch_bytes(m, max(n, 0), max_tree) if 1 <= max_tree <= 64 else 1 << 20
+    return kv._lib.kvarn_tree_attention(p["q"], p["k"], p["v"], p["mask"], p["pos"], p["cu"], p["lens"], n, tokens,
+                                        max_tree, p["bt"], p["cache"], p["ws"],
+                                        None if score is None else ctypes.byref(score), p["out"], p["scratch"],
+                                        need - short, ctypes.byref(m), None)
+
+
+def test_tree_refusals(kv):
+    m = kv.make_meta(8, 64, 16, max_blocks_per_seq=4)
+    S = kv.KvarnScore
+    assert ctypes.sizeof(S) == 24 and S.slopes.offset == 16
+    assert kv.tree_scratch_bytes(m, 4, 8) > 0
+    assert kv.tree_scratch_bytes(m, 4, 0) == kv.tree_scratch_bytes(m, 4, 65) == kv.tree_scratch_bytes(m, -1, 4) == 0
+    assert _tree(kv, m, max_tree=0) == 2 and _tree(kv, m, max_tree=65) == 2
+    assert _tree(kv, m, n=-1) == 1 and _tree(kv, m, n=65536) == 1
+    assert _tree(kv, m, tokens=-1) == 1 and _tree(kv, m, tokens=1 << 26) == 1
+    assert _tree(kv, m, short=1) == 4 and _tree(kv, m, scratch=None) == 1 and _tree(kv, m, scratch=MIS) == 3
+    for name in ("q", "k", "v", "cu", "lens", "bt", "cache", "out"):
+        assert _tree(kv, m, **{name: None}) == 1, name
+        assert _tree(kv, m, **{name: MIS}) == 3, name
+    for name in ("mask", "pos", "ws"):
+        assert _tree(kv, m, **{name: MIS}) == 3, name
+    assert _tree(kv, m, S(0, 0, 5, 0, None), pos=None) == 1              # a window needs positions
+    assert _tree(kv, m, S(0, 0, 0, 0, 0x10000), pos=None) == 1           # so do slopes
+    assert _tree(kv, m, S(0, 0, 0, 0, 0x10008)) == 3
+    for bad in (S(-1.0, 0, 0, 0, None), S(float("nan"), 0, 0, 0, None), S(float("inf"), 0, 0, 0, None),
+                S(0, -1.0, 0, 0, None), S(0, float("inf"), 0, 0, None), S(0, 0, -1, 0, None), S(0, 0, 0, 1, None)):
+        assert _tree(kv, m, bad) == 1
+    assert _tree(kv, m, n=0) == 0 and _tree(kv, m, tokens=0) == 0
+
+
 def test_append_tokens_refusals(kv):
     m = kv.make_meta(8, 64, 16, max_blocks_per_seq=4)
     f, r = kv._lib.kvarn_append_tokens, ctypes.byref(m)
