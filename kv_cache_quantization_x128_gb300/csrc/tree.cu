@@ -1,11 +1,52 @@
 // Attention of drafted tokens over the packed cache, the workspace and the drafted
-// tokens themselves: one block per (new token, kv-head, sequence), 128 threads, fp32.
-#include "kvarn_common.cuh"
+// tokens themselves (KVarN README, "How KVarN works": the scales are re-applied on read,
+// the orthonormal rotation keeps attention scores, the output is un-rotated).
+//
+// The rows of a (sequence, kv-head) are its drafted tokens times the group's q-heads
+// (row = token * group + head), cut into units of up to kR rows. A unit's items are its
+// packed tiles and then its fresh tiles (up to 128 tokens each: the workspace tokens
+// followed by the drafted ones). The flattened items are cut into one contiguous range
+// per team (stream-K), so a few long sequences fill the GPU and ragged batches balance.
+//   tree_scan_kernel   prefix of items per sequence, first tile inside the window
+//   tree_split_kernel  one persistent CTA per SM, two teams of 8 warps; a team leaving a
+//                      unit writes a partial record
+//   tree_merge_kernel  a warp per output row joins the records
+//
+// Per item and team, all products with M = 128 on the 5th-generation tensor core, tokens
+// (then channels) as TMEM lanes, A in TMEM, B in shared memory:
+//   keys    thread (lane = token, half = channels 64 half ..) turns codes into fp16 in TMEM;
+//           q' = q_r r^K s^K 2^e as fp16 hi + lo rows, beta = sum_i q_r,i r_i z_i
+//   QK^T    S[token][row] = codes . q'           (8 K steps, hi and lo)
+//           x = c^K_t (S + beta) in the log2 domain, cap, bias, masks
+//   values  thread (lane = channel) turns codes into fp16 in TMEM (under QK^T)
+//   PV      O[channel][row] = codes . p',  p' = p c^V s^V 2^e as fp16 hi + lo
+//           acc += r^V_channel (O + gamma), gamma = sum_t p c^V z^V
+// The hi + lo pairs carry q' and p' to ~22 bits: rounded once to fp16, scores of keys with
+// outlier channels are off by some 1e-3 and so are the outputs. The tensor core drops
+// subnormal fp16 operands, hence the powers of two.
+// The running max is lazy: a tile rescales only when a score exceeds it by more than
+// kTau, so that most tiles need no reduction over tokens (lanes); p stays <= 2^kTau.
+// Before fresh tiles, or before a record is written, the accumulator of the packed part is
+// rotated back by one more product, with the +-1 Hadamard matrix as A.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "decode_tc.cuh"
 #include "kvarn_launch.h"
-#include "kvarn_unpack.cuh"
 
 namespace kvarn {
 namespace {
+
+constexpr int kTreeTeams = 2;
+constexpr int kTreeTeamThreads = 256;
+constexpr int kTreeThreads = kTreeTeams * kTreeTeamThreads;   // 128 registers each
+constexpr int kTreeIssuer = 224;       // the thread of a team (first of its last warp) that issues its UMMAs
+constexpr int kTreeStages = 2;
+constexpr int kTreeMaxCtas = 160;      // sizes the scratch
+constexpr uint32_t kTrAK = 0, kTrAV = 64, kTrS = 128, kTrO = 192, kTrCols = 256;   // TMEM columns of a team
+constexpr float kTau = 8.0f;
+constexpr float kNoMax = -1.0e30f;     // running max of a record whose row saw no key
 
 struct TreeArgs {
   const uint16_t *q, *k_new, *v_new;
@@ -16,192 +57,1063 @@ struct TreeArgs {
   const float* slopes;
   uint16_t* out;
   unsigned* flags;
+  int64_t* prefix;       // [n_seqs + 1] items of the sequences before
+  int32_t* first;        // [n_seqs] first packed tile that a window leaves
+  float* part;           // partial records
   int64_t num_blocks, n_tokens;
   int n_seqs, max_tree, hkv, group, max_blocks, window;
-  float scale, softcap;
+  int n_teams, max_units;   // teams; units of a (sequence, kv-head) at most
+  float scale, softcap;     // scale includes log2(e) where no cap is set
 };
 
-struct TreeSmem {
-  float q[8][128], qr[8][128], p[8][128], red[8][4];
-  float2 ab[128];
-  float rv[128];
-  float rows[128][129];
+// Row count and layout of a record: acc [R][128], then (max, sum) [R].
+__host__ __device__ constexpr int tree_rec_floats(int r) { return r * 130; }
+
+__device__ __forceinline__ void tree_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void tree_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Sizes of sequence s.
+struct TreeSeq {
+  int nt;       // drafted tokens that are computed (0: none, nothing to do)
+  int full;     // packed tiles [first, full)
+  int ws;       // workspace tokens
+  int units;    // of a kv-head
+  int fresh;    // fresh tiles
 };
-
-// Score of (query at pq, key at pk).
-__device__ __forceinline__ float tree_score(const TreeArgs& a, float x, float slope, int pq, int pk) {
-  x *= a.scale;
-  if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
-  if (a.slopes != nullptr) x -= slope * static_cast<float>(pq - pk);
-  if (a.window > 0 && static_cast<int64_t>(pq) - pk >= a.window) x = -INFINITY;
-  return x;
+template <int R>
+__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int s, bool report) {
+  TreeSeq q{};
+  const int64_t c0 = a.cu[s];
+  const int64_t n = a.cu[s + 1] - c0;
+  const int len = max(a.seq_lens[s], 0);
+  unsigned bad = 0;
+  q.nt = static_cast<int>(max(min(n, static_cast<int64_t>(a.max_tree)), static_cast<int64_t>(0)));
+  if (n > a.max_tree) bad = KVARN_FLAG_BAD_LENGTH;
+  if (q.nt > 0 && (c0 < 0 || c0 + q.nt > a.n_tokens)) {
+    q.nt = 0;
+    bad = KVARN_FLAG_BAD_LENGTH;
+  }
+  q.full = min(len / kB, a.max_blocks);
+  q.ws = len % kB;
+  if (q.nt > 0 && (len / kB > a.max_blocks || (q.ws > 0 && a.ws == nullptr))) bad = KVARN_FLAG_BAD_LENGTH;
+  if (a.ws == nullptr) q.ws = 0;
+  q.units = (q.nt * a.group + R - 1) / R;
+  q.fresh = (q.ws + q.nt + kB - 1) / kB;
+  if (report && bad) raise_flag(a.flags, bad);
+  return q;
 }
 
-// One block of up to 128 keys: thread t's key row dots are sc[g] (-inf: none); V rows in
-// sm.rows. Updates the running max, sum and the thread's channel of acc.
-__device__ __forceinline__ void tree_step(TreeSmem& sm, int t, float (&sc)[8], float (&m)[8], float (&l)[8],
-                                          float (&acc)[8], float (&other)[8]) {
-  const int w = t >> 5;
+// ------------------------------------------------------------------ scan
+template <int R>
+__global__ void __launch_bounds__(1024) tree_scan_kernel(const TreeArgs a) {
+  tree_dep_launch();
+  __shared__ int64_t warp_sums[32];
+  const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+  const int per = (a.n_seqs + 1023) / 1024;
+  const int s0 = min(t * per, a.n_seqs), s1 = min(s0 + per, a.n_seqs);
+  int64_t sum = 0;
+  for (int s = s0; s < s1; ++s) {
+    const TreeSeq q = tree_seq<R>(a, s, true);
+    int first = 0;
+    if (a.window > 0 && q.nt > 0) {   // tiles that no drafted token's window reaches are left out
+      int64_t pmin = INT32_MAX;
+      for (int i = 0; i < q.nt; ++i) pmin = min(pmin, static_cast<int64_t>(a.positions[a.cu[s] + i]));
+      const int64_t lo = max(pmin - a.window + 1, static_cast<int64_t>(0)) / kB;
+      first = static_cast<int>(min(lo, static_cast<int64_t>(q.full)));
+    }
+    a.first[s] = first;
+    const int64_t items = static_cast<int64_t>(a.hkv) * q.units * (q.full - first + q.fresh);
+    a.prefix[s] = items;              // turned into the prefix below
+    sum += items;
+  }
+  int64_t incl = sum;
 #pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    float v = sc[g];
-    for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if ((t & 31) == 0) sm.red[g][w] = v;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_sums[w] = incl;
+  __syncthreads();
+  if (w == 0) {
+    int64_t v = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    warp_sums[lane] = v;
   }
   __syncthreads();
-#pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    const float mt = fmaxf(fmaxf(sm.red[g][0], sm.red[g][1]), fmaxf(sm.red[g][2], sm.red[g][3]));
-    const float mn = fmaxf(m[g], mt);
-    const float corr = mn == -INFINITY ? 1.f : expf(m[g] - mn);
-    const float p = mn == -INFINITY ? 0.f : expf(sc[g] - mn);
-    m[g] = mn;
-    l[g] = l[g] * corr + p;
-    acc[g] *= corr;
-    other[g] *= corr;
-    sm.p[g][t] = p;
+  int64_t run = incl - sum + (w > 0 ? warp_sums[w - 1] : 0);
+  for (int s = s0; s < s1; ++s) {
+    const int64_t n = a.prefix[s];
+    a.prefix[s] = run;
+    run += n;
   }
-  __syncthreads();
-  for (int j = 0; j < 128; ++j) {
-    const float v = sm.rows[j][t];
-#pragma unroll
-    for (int g = 0; g < 8; ++g) acc[g] = fmaf(sm.p[g][j], v, acc[g]);
-  }
-  __syncthreads();
+  if (t == 1023) a.prefix[a.n_seqs] = warp_sums[31];
 }
 
-template <int KB, int VB, bool kLean>
-__global__ void __launch_bounds__(128) tree_kernel(const TreeArgs a) {
+// ------------------------------------------------------------------ cursor over items
+// Kept in shared memory: thread 0 of the team moves it, everyone reads what it needs.
+struct TreeCursor {
+  int s, h, u;           // sequence, kv-head, unit of it
+  int ti;                // item of the unit
+  int packed, items;     // packed tiles, all items of the unit
+  int units, nt, ws;     // units of a kv-head, drafted and workspace tokens
+  int first;             // first packed tile
+};
+template <int R>
+__device__ __forceinline__ void tree_enter(const TreeArgs& a, TreeCursor& c) {
+  const TreeSeq q = tree_seq<R>(a, c.s, false);
+  c.first = a.first[c.s];
+  c.packed = q.full - c.first;
+  c.items = c.packed + q.fresh;
+  c.units = q.units;
+  c.nt = q.nt;
+  c.ws = q.ws;
+}
+template <int R>
+__device__ __forceinline__ void tree_locate(const TreeArgs& a, int64_t g, TreeCursor& c) {
+  int lo = 0, hi = a.n_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.prefix[mid] <= g) lo = mid; else hi = mid - 1;
+  }
+  c.s = lo;
+  tree_enter<R>(a, c);
+  const int64_t off = g - a.prefix[lo];
+  const int64_t un = off / c.items;
+  c.ti = static_cast<int>(off - un * c.items);
+  c.h = static_cast<int>(un / c.units);
+  c.u = static_cast<int>(un - static_cast<int64_t>(c.h) * c.units);
+}
+// To the next unit's first item.
+template <int R>
+__device__ __forceinline__ void tree_next_unit(const TreeArgs& a, TreeCursor& c) {
+  c.ti = 0;
+  if (++c.u < c.units) return;
+  c.u = 0;
+  if (++c.h < a.hkv) return;
+  c.h = 0;
+  do {
+    ++c.s;
+    if (c.s >= a.n_seqs) return;
+  } while (a.prefix[c.s + 1] == a.prefix[c.s]);
+  tree_enter<R>(a, c);
+}
+
+// ------------------------------------------------------------------ shared memory of a team
+template <int KB, int VB, bool kLean, int R>
+struct TreeSm {
   using L = RecordLayout<KB, VB, kLean>;
-  extern __shared__ __align__(16) uint8_t raw[];
-  TreeSmem& sm = *reinterpret_cast<TreeSmem*>(raw);
-  const int t = threadIdx.x, h = blockIdx.y, s = blockIdx.z, p = blockIdx.x;
-  const int c0 = a.cu[s];
-  const int n = a.cu[s + 1] - c0;
-  if (n > a.max_tree && p == 0 && h == 0 && t == 0) raise_flag(a.flags, KVARN_FLAG_BAD_LENGTH);
-  const int nt = min(n, a.max_tree);
-  if (p >= nt) return;
-  if (c0 < 0 || static_cast<int64_t>(c0) + nt > a.n_tokens) {
-    if (t == 0) raise_flag(a.flags, KVARN_FLAG_BAD_LENGTH);
-    return;
-  }
-  const int64_t tok = c0 + p;
-  const int len = max(a.seq_lens[s], 0), full = min(len / kB, a.max_blocks);
-  if (len / kB > a.max_blocks && t == 0) raise_flag(a.flags, KVARN_FLAG_BAD_LENGTH);
-  const int pq = a.positions != nullptr ? a.positions[tok] : 0;
-  const int hq = a.hkv * a.group;
-  float slope[8], m[8], l[8], acc[8], accr[8];
+  static constexpr int kB0 = 0;                                  // B operand(s): 64 rows (hi; or hi and lo of 32)
+  static constexpr int kB1 = 16384;                              // lo rows (R = 64)
+  static constexpr int kQ = R == 64 ? 32768 : 16384;             // q_r scaled, [R][128] f32
+  static constexpr int kRec = kQ + R * 512;
+  static constexpr int kX = kRec + kTreeStages * ((L::kBytes + 15) / 16 * 16);
+  // small arrays at kX
+  static constexpr int kBeta = 0, kMax = 256, kGam = 512, kPos = 768, kSlope = 1024, kMask = 1280;
+  static constexpr int kPart = 1792;                             // [8 warps][32] f32
+  static constexpr int kCsMax = 2816, kBars = 2880;
+  static constexpr int kCur = 2944, kAhead = 2992;               // cursors: the team's, the copies'
+  static constexpr int kAheadN = 3040, kValid = 3048;            // items left to the copies; the stages' tiles are valid
+  static constexpr int kXBytes = 3056;
+  static constexpr int kTeam = (kX + kXBytes + 1023) / 1024 * 1024;
+  static constexpr int kSlot = kTreeTeams * kTeam;
+  static constexpr int kBytes = kSlot + 16;
+  static_assert(sizeof(TreeCursor) <= 48, "cursor");
+  static_assert(kBytes <= 232448, "tree shared memory");
+};
+constexpr int kTbRec = 0, kTbQkDone = 2, kTbPvDone = 3, kTbFin = 4;
+
+// Columns 16 ch .. 16 ch + 15 of this thread's R / 2 rows of a 64-column product. R = 64: rows
+// 32 half + 16 ch ..; R = 32: rows 16 half .., the sums of the hi columns (row) and the lo
+// columns (32 + row).
+template <int R>
+__device__ __forceinline__ void tree_read(uint32_t trow, int half, int ch, float (&v)[16]) {
+  if (R == 64) {
+    tc_ld16(trow + 32 * half + 16 * ch, v);
+  } else {
+    float lo[16];
+    tc_ld16(trow + 16 * half, v);
+    tc_ld16(trow + 32 + 16 * half, lo);
 #pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    const bool live = g < a.group;
-    slope[g] = a.slopes != nullptr && live ? a.slopes[h * a.group + g] : 0.f;
-    sm.q[g][t] = live ? h2f_bits(a.q[(tok * hq + h * a.group + g) * kD + t]) : 0.f;
-    m[g] = -INFINITY;
-    l[g] = acc[g] = accr[g] = 0.f;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    float x = 0.f;
-    for (int i = 0; i < 128; ++i) x += (__popc(i & t) & 1) ? -sm.q[g][i] : sm.q[g][i];
-    sm.qr[g][t] = x * kInvSqrt128;
-  }
-  __syncthreads();
-  float sc[8];
-  for (int ti = 0; ti < full; ++ti) {
-    const int64_t blk = a.block_tables[static_cast<int64_t>(s) * a.max_blocks + ti];
-    if (blk < 0 || blk >= a.num_blocks) {
-      if (t == 0) raise_flag(a.flags, KVARN_FLAG_BAD_BLOCK);
-      continue;
+    for (int i = 0; i < 16; i += 2) {
+      const float2 x = __fadd2_rn(make_float2(v[i], v[i + 1]), make_float2(lo[i], lo[i + 1]));
+      v[i] = x.x;
+      v[i + 1] = x.y;
     }
-    const uint8_t* rec = a.cache + (blk * a.hkv + h) * static_cast<int64_t>(L::kBytes);
-    const uint16_t* km = reinterpret_cast<const uint16_t*>(rec + L::kKMetaOff);
-    const uint16_t* vm = reinterpret_cast<const uint16_t*>(rec + L::kVMetaOff);
-    const float r = kLean ? 1.f : h2f_bits(km[L::kKr + t]);
-    const float s16 = r * h2f_bits(km[L::kKs + t]) * static_cast<float>(1 << KB);
-    sm.ab[t] = make_float2(s16, fmaf(r, h2f_bits(km[L::kKz + t]), -s16));
-    sm.rv[t] = h2f_bits(vm[L::kVr + t]);
-    __syncthreads();
-    float2 x[64];
-    read_keys<KB>(rec + L::kKCodeOff, sm.ab, t, x);
-    const float ck = h2f_bits(km[L::kKc + t]);
-#pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      float d = 0.f;
-#pragma unroll
-      for (int i = 0; i < 64; ++i) d += x[i].x * sm.qr[g][2 * i] + x[i].y * sm.qr[g][2 * i + 1];
-      sc[g] = tree_score(a, d * ck, slope[g], pq, ti * kB + t);
-    }
-    const float c = kLean ? 1.f : h2f_bits(vm[L::kVc + t]);
-    const float av = c * h2f_bits(vm[L::kVs + t]) * static_cast<float>(1 << VB);
-    read_values<VB>(rec + L::kVCodeOff, sm.rv, av, fmaf(c, h2f_bits(vm[L::kVz + t]), -av), t, x);
-#pragma unroll
-    for (int i = 0; i < 64; ++i) {
-      sm.rows[t][2 * i] = x[i].x;
-      sm.rows[t][2 * i + 1] = x[i].y;
-    }
-    tree_step(sm, t, sc, m, l, accr, acc);
-  }
-  // workspace, then new tokens
-  const uint64_t word = a.mask != nullptr ? a.mask[tok] : ~0ull >> (63 - p);
-  for (int part = 0; part < 2; ++part) {
-    const int cnt = part == 0 ? len % kB : nt;
-    if (cnt == 0) continue;
-    if (part == 0 && a.ws == nullptr) {
-      if (t == 0) raise_flag(a.flags, KVARN_FLAG_BAD_LENGTH);
-      continue;
-    }
-    const uint16_t* kr = part == 0 ? a.ws + (static_cast<int64_t>(s) * a.hkv + h) * 2 * kB * kD
-                                   : a.k_new + (static_cast<int64_t>(c0) * a.hkv + h) * kD;
-    const uint16_t* vr = part == 0 ? kr + kB * kD : a.v_new + (static_cast<int64_t>(c0) * a.hkv + h) * kD;
-    const int64_t stride = part == 0 ? kD : static_cast<int64_t>(a.hkv) * kD;
-    const bool live = t < cnt && (part == 0 || ((word >> (t & 63)) & 1));
-    const int pk = part == 0 ? len / kB * kB + t : (a.positions != nullptr && t < cnt ? a.positions[c0 + t] : 0);
-#pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      float d = 0.f;
-      if (t < cnt)
-        for (int i = 0; i < 128; ++i) d += h2f_bits(kr[t * stride + i]) * sm.q[g][i];
-      sc[g] = live ? tree_score(a, d, slope[g], pq, pk) : -INFINITY;
-    }
-    for (int j = 0; j < 128; ++j) sm.rows[j][t] = j < cnt ? h2f_bits(vr[j * stride + t]) : 0.f;
-    tree_step(sm, t, sc, m, l, acc, accr);
-  }
-  // rotate the packed part back, join, normalise
-  __syncthreads();
-#pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    sm.q[g][t] = accr[g];
-    sm.p[g][t] = l[g];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    if (g >= a.group) continue;
-    float x = 0.f, sum = 0.f;
-    for (int i = 0; i < 128; ++i) {
-      x += (__popc(i & t) & 1) ? -sm.q[g][i] : sm.q[g][i];
-      sum += sm.p[g][i];
-    }
-    const float y = sum > 0.f ? (x * kInvSqrt128 + acc[g]) / sum : 0.f;
-    a.out[(tok * hq + h * a.group + g) * kD + t] = f2h_bits(y);
   }
 }
 
-template <int KB, int VB, bool kLean>
+// Sum (or maximum) over the warp's 32 lanes of 16 values: lane l returns that of value l % 16.
+template <bool kMaxOp>
+__device__ __forceinline__ float tree_reduce(float (&g)[16], int lane) {
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float send = up ? g[i] : g[i + o], keep = up ? g[i + o] : g[i];
+      const float got = __shfl_xor_sync(0xffffffffu, send, o);
+      g[i] = kMaxOp ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  const float got = __shfl_xor_sync(0xffffffffu, g[0], 16);
+  return kMaxOp ? fmaxf(g[0], got) : g[0] + got;
+}
+
+// Byte offset of (row, channel) in a 64-row fp16 B operand, K = channels: 128-byte
+// swizzled K-major, halves of 64 channels 8192 bytes apart.
+__device__ __forceinline__ uint32_t tree_qo(int r, int ch) {
+  return static_cast<uint32_t>((ch >> 6) * 8192 + (r >> 3) * 1024 + (r & 7) * 128 +
+                               ((((ch & 63) >> 3) ^ (r & 7)) << 4));
+}
+// Byte offset of (8 rows from 8 c, token) in a 64-row fp16 B operand, K = tokens: 128-byte
+// swizzled with the rows contiguous (N-major), a token's 64 rows in 128 bytes.
+__device__ __forceinline__ uint32_t tree_po(int c, int tok) {
+  return static_cast<uint32_t>(tok * 128 + ((c ^ (tok & 7)) << 4));
+}
+
+// ------------------------------------------------------------------ operands
+// Keys: token t's codes of channels 64 half .. 64 half + 63 -> 32 TMEM columns.
+template <int KB>
+__device__ __forceinline__ void tree_keys(const uint8_t* codes, int t, int half, uint32_t taddr) {
+  uint32_t r[32];
+  if (KB == 4) {
+    const uint4* row = reinterpret_cast<const uint4*>(codes + t * 64);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint2 w2 = reinterpret_cast<const uint2*>(row + c)[half];   // words 2 half, 2 half + 1
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const uint32_t w = m ? w2.y : w2.x;
+        cvt4(w & 0x0F0F0F0Fu, r[16 * m + c], r[16 * m + 4 + c]);
+        cvt4((w >> 4) & 0x0F0F0F0Fu, r[16 * m + 8 + c], r[16 * m + 12 + c]);
+      }
+    }
+  } else {
+    // group g, word half: byte b = channel bits 4-5; crumbs 2 bit0 + bit3
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t x = *reinterpret_cast<const uint32_t*>(codes + t * 32 + c * 8 + half * 4);
+      uint32_t v0[4], v1[4];
+      cvt2(x & 0x33333333u, v0);
+      cvt2((x >> 2) & 0x33333333u, v1);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        r[8 * b + c] = v0[b];
+        r[8 * b + 4 + c] = v1[b];
+      }
+    }
+  }
+  tc_st32(taddr, r);
+}
+// Values: channel t's codes of tokens 64 half .. -> 32 TMEM columns.
+template <int VB>
+__device__ __forceinline__ void tree_values(const uint8_t* codes, int t, int half, uint32_t taddr) {
+  uint32_t r[32];
+  if (VB == 4) {
+    const uint4* row = reinterpret_cast<const uint4*>(codes + t * 64);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint2 w2 = reinterpret_cast<const uint2*>(row + c)[half];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const uint32_t w = m ? w2.y : w2.x;
+        cvt4(w & 0x0F0F0F0Fu, r[16 * m + c], r[16 * m + 4 + c]);
+        cvt4((w >> 4) & 0x0F0F0F0Fu, r[16 * m + 8 + c], r[16 * m + 12 + c]);
+      }
+    }
+  } else {
+    const uint8_t* base = codes + (t >> 4) * 512 + (t & 7) * 64 + ((t >> 3) & 1) * 8 + half * 4;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t x = *reinterpret_cast<const uint32_t*>(base + c * 16);
+      uint32_t v0[4], v1[4];
+      cvt2(x & 0x33333333u, v0);
+      cvt2((x >> 2) & 0x33333333u, v1);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        r[8 * b + c] = v0[b];
+        r[8 * b + 4 + c] = v1[b];
+      }
+    }
+  }
+  tc_st32(taddr, r);
+}
+
+// A team's work. Thread tt of 256: lane t = tt & 127 (token or channel), half = tt >> 7.
+template <int KB, int VB, bool kLean, int R, bool kMod>
+struct TreeTeam {
+  using L = RecordLayout<KB, VB, kLean>;
+  using S = TreeSm<KB, VB, kLean, R>;
+  static constexpr int CT = R / 2;               // rows (columns of the products) of a thread
+  static constexpr float kKF = KB == 4 ? 8.f : 2.f, kVF = VB == 4 ? 8.f : 2.f;   // codes were converted to code / kKF
+  static constexpr int kRecPitch = (L::kBytes + 15) / 16 * 16;
+  static constexpr int kLoRow = R == 64 ? 0 : 32;
+  const TreeArgs& a;
+  uint8_t* sm;
+  uint32_t tm, trow;                             // TMEM address of the team, of the thread's warp
+  int tt, t, half, lane, warp, bar_id;
+  float acc[CT], lsum[CT];
+  float qinv;                                    // 2^-e of the stored q_r
+  uint32_t qph, pph;
+  bool ok;
+  bool row_set;                                  // thread tt < R: row tt has seen a key
+  bool pending;                                  // some row of the unit has not (the team agrees)
+
+  __device__ TreeTeam(const TreeArgs& a_, uint8_t* sm_, uint32_t tm_, int team)
+      : a(a_), sm(sm_), tm(tm_), bar_id(1 + 3 * team), qinv(1.f), qph(0), pph(0), ok(true), row_set(false), pending(true) {
+    tt = static_cast<int>(threadIdx.x) - team * kTreeTeamThreads;
+    t = tt & 127;
+    half = tt >> 7;
+    lane = tt & 31;
+    warp = tt >> 5;
+    trow = tm + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+  }
+  __device__ float* beta() const { return reinterpret_cast<float*>(sm + S::kX + S::kBeta); }
+  __device__ float* mrow() const { return reinterpret_cast<float*>(sm + S::kX + S::kMax); }
+  __device__ float* gam() const { return reinterpret_cast<float*>(sm + S::kX + S::kGam); }
+  __device__ float* part() const { return reinterpret_cast<float*>(sm + S::kX + S::kPart); }
+  __device__ float* csmax() const { return reinterpret_cast<float*>(sm + S::kX + S::kCsMax); }
+  __device__ float* slope() const { return reinterpret_cast<float*>(sm + S::kX + S::kSlope); }
+  __device__ int32_t* pos() const { return reinterpret_cast<int32_t*>(sm + S::kX + S::kPos); }
+  __device__ uint64_t* mask() const { return reinterpret_cast<uint64_t*>(sm + S::kX + S::kMask); }
+  __device__ uint64_t* bars() const { return reinterpret_cast<uint64_t*>(sm + S::kX + S::kBars); }
+  __device__ TreeCursor& cur() const { return *reinterpret_cast<TreeCursor*>(sm + S::kX + S::kCur); }
+  __device__ TreeCursor& ahead() const { return *reinterpret_cast<TreeCursor*>(sm + S::kX + S::kAhead); }
+  __device__ int64_t& ahead_n() const { return *reinterpret_cast<int64_t*>(sm + S::kX + S::kAheadN); }
+  __device__ volatile uint32_t* valid_of() const { return reinterpret_cast<volatile uint32_t*>(sm + S::kX + S::kValid); }
+  __device__ void bar() { named_bar(bar_id, kTreeTeamThreads); }
+  __device__ uint8_t* b_lo() { return R == 64 ? sm + S::kB1 : sm + S::kB0; }   // where lo rows go
+
+  // The thread's operand writes are done; the issuer, once everyone's are, starts the product.
+  __device__ void product(bool pv) {
+    tc_operands_written();
+    const int id = bar_id + (pv ? 2 : 1);
+    if (warp != kTreeIssuer / 32) {
+      asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(kTreeTeamThreads) : "memory");
+      return;
+    }
+    named_bar(id, kTreeTeamThreads);
+    if (lane == 0) {
+      tc_fence_after();
+      constexpr uint32_t kIdQk = idesc_f16_f32(128, 64), kIdPv = kIdQk | (1u << 16);   // bit 16: B is N-major
+      constexpr int kParts = R / 32;             // operands of 64 rows: (hi and lo), or hi, lo
+      const uint32_t b = smem_u32(sm + S::kB0);
+#pragma unroll
+      for (int p = 0; p < kParts; ++p)
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          if (pv)
+            tc_umma_ts(tm + kTrO, tm + kTrAV + 8 * s, smem_desc_sw128(b + p * 16384 + s * 2048), kIdPv, p + s > 0);
+          else
+            tc_umma_ts(tm + kTrS, tm + kTrAK + 8 * s, smem_desc_sw128(b + p * 16384 + (s >> 2) * 8192 + (s & 3) * 32),
+                       kIdQk, p + s > 0);
+        }
+      umma_commit(&bars()[pv ? kTbPvDone : kTbQkDone]);
+    }
+    __syncwarp();
+  }
+
+  // Rows of the unit at the cursor: row tables, q_r scaled by a power of two in shared memory.
+  __device__ void enter() {
+    const TreeCursor& c = cur();
+    const int64_t c0 = a.cu[c.s];
+    const int hq = a.hkv * a.group, row0 = c.u * R, nt = c.nt, h = c.h;
+    if (tt < R) {
+      const int row = row0 + tt, p = row / a.group;
+      const bool live = p < nt;
+      mrow()[tt] = 0.f;
+      uint64_t w = 0;
+      if (live) w = a.mask != nullptr ? a.mask[c0 + p] : ~0ull >> (63 - p);
+      mask()[tt] = w;
+      if (kMod) {
+        pos()[tt] = live && a.positions != nullptr ? a.positions[c0 + p] : 0;
+        slope()[tt] = live && a.slopes != nullptr ? a.slopes[h * a.group + row % a.group] * kLog2e : 0.f;
+      }
+    }
+    const int jj = tt & 15, r0 = tt >> 4;
+    float m = 0.f;
+    float* qs = reinterpret_cast<float*>(sm + S::kQ);
+#pragma unroll
+    for (int k = 0; k < R / 16; ++k) {
+      const int r = r0 + 16 * k, row = row0 + r, p = row / a.group;
+      float x[8];
+      if (p < nt) {
+        const uint4 w = *reinterpret_cast<const uint4*>(a.q + ((c0 + p) * hq + h * a.group + row % a.group) * kD + 8 * jj);
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = h2pair(reinterpret_cast<const uint16_t*>(&ws[e]));
+          x[2 * e] = f.x;
+          x[2 * e + 1] = f.y;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+      }
+#pragma unroll
+      for (int bit = 1; bit < 8; bit <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if ((i & bit) == 0) {
+            const float u = x[i], v = x[i | bit];
+            x[i] = u + v;
+            x[i | bit] = u - v;
+          }
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) {
+        const bool up = (jj & o) != 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float other = __shfl_xor_sync(0xffffffffu, x[i], o);
+          x[i] = up ? (other - x[i]) : (x[i] + other);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+      float4* dst = reinterpret_cast<float4*>(qs + r * kD + 8 * jj);
+      dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+      dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+    if (lane == 0) part()[warp] = m;
+    bar();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, part()[i]);
+    const float2 sc = tc_pow2_scale(m, 12);        // the largest |q_r| into [2^12, 2^13)
+    qinv = sc.y;
+#pragma unroll
+    for (int k = 0; k < R / 16; ++k) {             // the thread's own elements
+      float4* p = reinterpret_cast<float4*>(qs + (r0 + 16 * k) * kD + 8 * jj);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float4 v = p[e];
+        p[e] = make_float4(v.x * sc.x, v.y * sc.x, v.z * sc.x, v.w * sc.x);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < CT; ++i) acc[i] = lsum[i] = 0.f;
+    row_set = false;
+    pending = true;
+    bar();                                          // part is used again
+  }
+
+  // q' rows and beta of a packed tile; returns 2^-k of the tile's scaling of r s.
+  __device__ float fold(const uint8_t* rec) {
+    const uint16_t* km = reinterpret_cast<const uint16_t*>(rec + L::kKMetaOff);
+    const int jj = tt & 15, r0 = tt >> 4;
+    const uint4 sv = *reinterpret_cast<const uint4*>(km + L::kKs + 8 * jj);
+    const uint4 zv = *reinterpret_cast<const uint4*>(km + L::kKz + 8 * jj);
+    uint4 rv = make_uint4(kH_One, kH_One, kH_One, kH_One);
+    if (!kLean) rv = *reinterpret_cast<const uint4*>(km + L::kKr + 8 * jj);
+    const uint32_t s4[4] = {sv.x, sv.y, sv.z, sv.w}, z4[4] = {zv.x, zv.y, zv.z, zv.w};
+    const uint32_t r4[4] = {rv.x, rv.y, rv.z, rv.w};
+    float2 rs[4], rz[4];
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      rs[e] = mul_h2(r4[e], s4[e]);
+      rz[e] = mul_h2(r4[e], z4[e]);
+      m = fmax3f(m, rs[e].x, rs[e].y);
+    }
+    // the scales are positive: their maximum over the tile's channels as integers
+    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+    const float2 sc = tc_pow2_scale(m, 0);          // the largest r s into [1, 2)
+    const float2 sc2 = make_float2(sc.x, sc.x);
+    const float zf = sc.x / kKF;                    // beta in the units of S
+    const float2 zf2 = make_float2(zf, zf);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      rs[e] = __fmul2_rn(rs[e], sc2);
+      rz[e] = __fmul2_rn(rz[e], zf2);
+    }
+    const float* qs = reinterpret_cast<const float*>(sm + S::kQ);
+    float b[R / 16];
+#pragma unroll
+    for (int k = 0; k < R / 16; ++k) {
+      const int r = r0 + 16 * k;
+      const float4* p = reinterpret_cast<const float4*>(qs + r * kD + 8 * jj);
+      const float4 u = p[0], v = p[1];
+      const float2 x[4] = {make_float2(u.x, u.y), make_float2(u.z, u.w), make_float2(v.x, v.y), make_float2(v.z, v.w)};
+      uint32_t hi[4], lo[4];
+      float2 b2 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        split2p(__fmul2_rn(x[e], rs[e]), hi[e], lo[e]);
+        b2 = __ffma2_rn(x[e], rz[e], b2);
+      }
+      b[k] = b2.x + b2.y;
+      *reinterpret_cast<uint4*>(sm + S::kB0 + tree_qo(r, 8 * jj)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(b_lo() + tree_qo(r + kLoRow, 8 * jj)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+#pragma unroll
+    for (int k = 0; k < R / 16; ++k) {
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) b[k] += __shfl_xor_sync(0xffffffffu, b[k], o);
+      if (jj == 0) beta()[r0 + 16 * k] = b[k];
+    }
+    return sc.y;
+  }
+
+  // Operands of fresh tokens [f0, f0 + 128) of the cursor's sequence: keys and values as
+  // they are, q as it is (hi rows; lo rows 0).
+  __device__ const uint16_t* fresh_row(int f, bool value) const {
+    const TreeCursor& c = cur();
+    if (f < c.ws) return a.ws + ((static_cast<int64_t>(c.s) * a.hkv + c.h) * 2 + (value ? 1 : 0)) * (kB * kD) + f * kD;
+    return (value ? a.v_new : a.k_new) + (static_cast<int64_t>(a.cu[c.s] + (f - c.ws)) * a.hkv + c.h) * kD;
+  }
+  __device__ void fresh_keys(int f0) {
+    const TreeCursor& c = cur();
+    const int f = f0 + t;
+    uint32_t r[32];
+    if (f < c.ws + c.nt) {
+      const uint4* src = reinterpret_cast<const uint4*>(fresh_row(f, false) + 64 * half);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4 v = src[i];
+        r[4 * i] = v.x; r[4 * i + 1] = v.y; r[4 * i + 2] = v.z; r[4 * i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) r[i] = 0;
+    }
+    tc_st32(trow + kTrAK + 32 * half, r);
+    const int64_t c0 = a.cu[c.s];
+    const int hq = a.hkv * a.group, jj = tt & 15, r0 = tt >> 4;
+#pragma unroll
+    for (int k = 0; k < R / 16; ++k) {
+      const int rr = r0 + 16 * k, row = c.u * R + rr, p = row / a.group;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (p < c.nt)
+        w = *reinterpret_cast<const uint4*>(a.q + ((c0 + p) * hq + c.h * a.group + row % a.group) * kD + 8 * jj);
+      *reinterpret_cast<uint4*>(sm + S::kB0 + tree_qo(rr, 8 * jj)) = w;
+      *reinterpret_cast<uint4*>(b_lo() + tree_qo(rr + kLoRow, 8 * jj)) = make_uint4(0, 0, 0, 0);
+    }
+    if (tt < R) beta()[tt] = 0.f;
+  }
+  __device__ void fresh_values(int f0) {
+    const TreeCursor& c = cur();
+    uint32_t r[32];
+    const int n = c.ws + c.nt;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int f = f0 + 64 * half + 2 * i;
+      const uint32_t x = f < n ? fresh_row(f, true)[t] : 0;
+      const uint32_t y = f + 1 < n ? fresh_row(f + 1, true)[t] : 0;
+      r[i] = x | (y << 16);
+    }
+    tc_st32(trow + kTrAV + 32 * half, r);
+  }
+
+  // Wait for a product; every thread of the team agrees on the outcome at the next barrier.
+  __device__ void wait_qk() {
+    ok = mbar_wait(&bars()[kTbQkDone], qph, a.flags) && ok;
+    qph ^= 1u;
+    tc_fence_after();
+  }
+  __device__ void wait_pv() {
+    ok = mbar_wait(&bars()[kTbPvDone], pph, a.flags) && ok;
+    pph ^= 1u;
+    tc_fence_after();
+  }
+
+  struct Keys {        // what the thread's token (lane) is in the current item
+    float f;           // factor of S
+    int pk;            // position
+    int chunk_i;       // index among the drafted tokens, or -1
+    bool key, fresh;
+  };
+  // Scores of 16 rows relative to their running max: x = f (S + beta) (then cap and bias) -
+  // max; masked keys -inf.
+  __device__ void scores(int ch, const Keys& k, float (&x)[16]) {
+    tree_read<R>(trow + kTrS, half, ch, x);
+    const float2 f2 = make_float2(k.f, k.f);
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int col = CT * half + 16 * ch + i;
+      const float4 b = *reinterpret_cast<const float4*>(beta() + col), m = *reinterpret_cast<const float4*>(mrow() + col);
+      float2 u = __fadd2_rn(make_float2(x[i], x[i + 1]), make_float2(b.x, b.y));
+      float2 v = __fadd2_rn(make_float2(x[i + 2], x[i + 3]), make_float2(b.z, b.w));
+      if (!kMod) {
+        u = __ffma2_rn(u, f2, make_float2(-m.x, -m.y));
+        v = __ffma2_rn(v, f2, make_float2(-m.z, -m.w));
+        x[i] = u.x; x[i + 1] = u.y; x[i + 2] = v.x; x[i + 3] = v.y;
+      } else {
+        const float s[4] = {u.x * k.f, u.y * k.f, v.x * k.f, v.y * k.f}, mm[4] = {m.x, m.y, m.z, m.w};
+        const int4 pq = *reinterpret_cast<const int4*>(pos() + col);
+        const float4 sl = *reinterpret_cast<const float4*>(slope() + col);
+        const int pp[4] = {pq.x, pq.y, pq.z, pq.w};
+        const float ss[4] = {sl.x, sl.y, sl.z, sl.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float y = s[e];
+          // cap tanh(z) = cap (1 - 2 / (1 + e^(2 z))), z = score / cap; y is z log2(e)
+          if (a.softcap > 0.f) y = a.softcap * kLog2e * (1.f - __fdividef(2.f, 1.f + ex2(2.f * y)));
+          const int64_t gap = static_cast<int64_t>(pp[e]) - k.pk;
+          y = fmaf(-ss[e], static_cast<float>(gap), y);
+          if (a.window > 0 && gap >= a.window) y = -INFINITY;
+          x[i + e] = y - mm[e];
+        }
+      }
+      if (k.fresh) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!(k.key && (k.chunk_i < 0 || ((mask()[col + e] >> k.chunk_i) & 1)))) x[i + e] = -INFINITY;
+      }
+    }
+  }
+
+  // Some score exceeds its row's running max by more than kTau, or a row has not seen a key
+  // yet: exact maxima of the tile, and everything moved to them.
+  __device__ void rescale(const Keys& k, bool valid) {
+#pragma unroll
+    for (int ch = 0; ch < CT / 16; ++ch) {
+      float x[16];
+      scores(ch, k, x);
+      float m = tree_reduce<true>(x, lane);
+      if (lane < 16) part()[warp * 32 + 16 * ch + lane] = valid ? m : -INFINITY;
+    }
+    bar();
+    if (tt < R) {                                   // row tt: its half's four warps
+      const float* p = part() + 4 * (tt / CT) * 32 + tt % CT;
+      float d = fmax3f(fmaxf(p[0], p[32]), p[64], p[96]);   // relative to the running max
+      if (row_set || d == -INFINITY) d = fmaxf(d, 0.f);     // a row's first max may be any
+      else row_set = true;
+      gam()[tt] = d;
+      mrow()[tt] += d;
+      const bool miss = __any_sync(0xffffffffu, !row_set);
+      if (lane == 0) csmax()[8 + warp] = miss ? 1.f : 0.f;
+    }
+    bar();
+    pending = csmax()[8] != 0.f || (R == 64 && csmax()[9] != 0.f);
+#pragma unroll
+    for (int i = 0; i < CT; i += 4) {
+      const float4 d = *reinterpret_cast<const float4*>(gam() + CT * half + i);
+      const float dd[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float corr = ex2(fminf(-dd[e], 0.f));         // (a row's first max: nothing to scale yet)
+        acc[i + e] *= corr;
+        lsum[i + e] *= corr;
+      }
+    }
+  }
+
+  // 16 rows' values of the thread's token into the B operand as hi and lo.
+  __device__ void store_p(int ch, const float2 (&pp)[8]) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split2p(pp[4 * c + e], hi[e], lo[e]);
+      const int cc = CT / 8 * half + 2 * ch + c;
+      *reinterpret_cast<uint4*>(sm + S::kB0 + tree_po(cc, t)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(b_lo() + tree_po(cc + kLoRow / 8, t)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+  }
+
+  // Second half of a sum over tokens: part (written per warp) -> gam()[row]. Ends with a barrier.
+  __device__ void join_rows() {
+    bar();
+    if (tt < R) {
+      const float* p = part() + 4 * (tt / CT) * 32 + tt % CT;
+      gam()[tt] = (p[0] + p[32]) + (p[64] + p[96]);
+    }
+    bar();
+  }
+  __device__ void sum_lsum() {
+#pragma unroll
+    for (int ch = 0; ch < CT / 16; ++ch) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = lsum[16 * ch + i];
+      const float m = tree_reduce<false>(v, lane);
+      if (lane < 16) part()[warp * 32 + 16 * ch + lane] = m;
+    }
+    join_rows();
+  }
+
+  // acc (rotated channels) -> H acc / sqrt(128), by one more product with A = H. Rows are
+  // divided by their sums on the way and scaled by a power of two, for the fp16 pairs.
+  __device__ bool unrotate() {
+    sum_lsum();
+    {
+      uint32_t hrow[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int j = 64 * half + 2 * i;
+        hrow[i] = 0x3C003C00u ^ ((__popc(t & j) & 1) ? 0x8000u : 0u) ^ ((__popc(t & (j + 1)) & 1) ? 0x80000000u : 0u);
+      }
+      tc_st32(trow + kTrAV + 32 * half, hrow);
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+      const float l = gam()[CT * half + i];
+      acc[i] = l > 0.f ? acc[i] / l : 0.f;
+      top = fmaxf(top, fabsf(acc[i]));
+    }
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    if (lane == 0) csmax()[warp] = top;
+    bar();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, csmax()[i]);
+    const float2 sc = tc_pow2_scale(top, 13);
+    const float2 sc2 = make_float2(sc.x, sc.x);
+#pragma unroll
+    for (int ch = 0; ch < CT / 16; ++ch) {
+      float2 pp[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) pp[i] = __fmul2_rn(make_float2(acc[16 * ch + 2 * i], acc[16 * ch + 2 * i + 1]), sc2);
+      store_p(ch, pp);
+    }
+    product(true);
+    wait_pv();
+#pragma unroll
+    for (int ch = 0; ch < CT / 16; ++ch) {
+      float v[16];
+      tree_read<R>(trow + kTrO, half, ch, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[16 * ch + i] = v[i] * (gam()[CT * half + 16 * ch + i] * (kInvSqrt128 * sc.y));
+    }
+    tc_fence_before();
+    return named_bar_and(bar_id, kTreeTeamThreads, ok);
+  }
+
+  __device__ void flush(int64_t rec_idx) {
+    sum_lsum();
+    float* out = a.part + rec_idx * tree_rec_floats(R);
+#pragma unroll
+    for (int i = 0; i < CT; ++i) out[(CT * half + i) * kD + t] = acc[i];
+    if (tt < R) *reinterpret_cast<float2*>(out + R * kD + 2 * tt) = make_float2(row_set ? mrow()[tt] : kNoMax, gam()[tt]);
+    bar();
+  }
+
+  // Thread 0: starts copies until `limit` packed tiles have been issued (of `issued` so far);
+  // a tile in a block that does not exist is flagged and marked.
+  __device__ uint32_t refill(uint32_t issued, uint32_t limit) {
+    TreeCursor& c = ahead();
+    int64_t left = ahead_n();
+    while (issued < limit && left > 0) {
+      if (c.ti >= c.packed) {                    // on to the next unit
+        left -= c.items - c.ti;
+        if (left > 0) tree_next_unit<R>(a, c);
+        continue;
+      }
+      const uint32_t stg = issued % kTreeStages;
+      uint64_t* rec_bar = &bars()[kTbRec + stg];
+      const int64_t blk = a.block_tables[static_cast<int64_t>(c.s) * a.max_blocks + c.first + c.ti];
+      if (blk < 0 || blk >= a.num_blocks) {
+        raise_flag(a.flags, KVARN_FLAG_BAD_BLOCK);
+        valid_of()[stg] = 0;
+        tc_arrive(rec_bar);
+      } else {
+        valid_of()[stg] = 1;
+        mbar_arrive_expect_tx(rec_bar, L::kBytes);
+        bulk_g2s(sm + S::kRec + stg * kRecPitch, a.cache + (blk * a.hkv + c.h) * static_cast<int64_t>(L::kBytes), L::kBytes,
+                 rec_bar);
+      }
+      ++c.ti;
+      ++issued;
+      --left;
+    }
+    ahead_n() = left;
+    return issued;
+  }
+
+  // One item: packed tile `ti` in stage used % kTreeStages, or the fresh tile at f0. False
+  // after a wait that timed out.
+  __device__ bool item(bool fresh, int ti, int f0, uint32_t used, uint32_t& issued) {
+    bool valid = true;
+    float cs = 1.f, cz = 0.f, rv = 1.f;
+    Keys key{0.f, 0, -1, true, fresh};
+    if (!fresh) {
+      const uint32_t stg = used % kTreeStages;
+      const uint8_t* rec = sm + S::kRec + stg * kRecPitch;
+      const uint16_t* km = reinterpret_cast<const uint16_t*>(rec + L::kKMetaOff);
+      const uint16_t* vm = reinterpret_cast<const uint16_t*>(rec + L::kVMetaOff);
+      ok = mbar_wait(&bars()[kTbRec + stg], (used / kTreeStages) & 1u, a.flags) && ok;
+      valid = valid_of()[stg] != 0;
+      const bool go = __all_sync(0xffffffffu, ok) && valid;
+      float kinv = 1.f;
+      if (go) {
+        tree_keys<KB>(rec + L::kKCodeOff, t, half, trow + kTrAK + 32 * half);
+        kinv = fold(rec);
+      }
+      product(false);
+      if (go) {
+        tree_values<VB>(rec + L::kVCodeOff, t, half, trow + kTrAV + 32 * half);
+        // S is in units of code / kKF, q 2^e, r s 2^k, and q_r lacks its 1 / sqrt(128)
+        key.f = h2f_bits(km[L::kKc + t]) * (a.scale * kInvSqrt128 * kKF * kinv * qinv);
+        const float cv = kLean ? 1.f : h2f_bits(vm[L::kVc + t]);
+        cs = cv * h2f_bits(vm[L::kVs + t]);
+        cz = cv * h2f_bits(vm[L::kVz + t]);
+        rv = h2f_bits(vm[L::kVr + t]);
+      }
+      const float cm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(cs)));
+      if (lane == 0) csmax()[warp] = cm;
+      key.pk = (cur().first + ti) * kB + t;
+    } else {
+      fresh_keys(f0);
+      product(false);
+      fresh_values(f0);
+      if (lane == 0) csmax()[warp] = 1.f;
+      const TreeCursor& c = cur();
+      const int ft = f0 + t;
+      key.f = a.scale;
+      key.key = ft < c.ws + c.nt;
+      if (key.key) key.chunk_i = max(ft - c.ws, -1);
+      key.pk = max(a.seq_lens[c.s], 0) / kB * kB + ft;
+      if (kMod && key.chunk_i >= 0 && a.positions != nullptr) key.pk = a.positions[a.cu[c.s] + key.chunk_i];
+    }
+    tc_operands_written();
+    ok = named_bar_and(bar_id, kTreeTeamThreads, ok);   // beta visible, the record read; every wait succeeded
+    if (!ok) return false;
+    if (tt == 0 && !fresh) issued = refill(issued, used + 1 + kTreeStages);
+
+    wait_qk();
+    float x[16];
+    float top = -INFINITY;
+#pragma unroll
+    for (int ch = 0; ch < CT / 16; ++ch) {
+      scores(ch, key, x);
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) top = fmax3f(top, x[i], x[i + 1]);
+    }
+    const float4 c4 = *reinterpret_cast<const float4*>(csmax());
+    // p' <= 2^kTau max(c s) 2^e < 2^14
+    const float2 psc = tc_pow2_scale(fmaxf(fmaxf(c4.x, c4.y), fmaxf(c4.z, c4.w)), 13 - static_cast<int>(kTau));
+    bool again = CT > 16;                  // the scores are not (all) at hand
+    if (tc_bar_or(bar_id, kTreeTeamThreads, (valid && top > kTau) || pending || !ok)) {
+      ok = named_bar_and(bar_id, kTreeTeamThreads, ok);
+      if (!ok) return false;
+      rescale(key, valid);
+      again = true;
+    }
+    if (valid) {
+      const float csq = cs * psc.x;
+      const float2 cs2 = make_float2(csq, csq), cz2 = make_float2(cz, cz);
+#pragma unroll
+      for (int ch = 0; ch < CT / 16; ++ch) {
+        if (again) scores(ch, key, x);
+        float2 pp[8];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const float2 p = make_float2(ex2(x[i]), ex2(x[i + 1]));
+          const float2 l = __fadd2_rn(make_float2(lsum[16 * ch + i], lsum[16 * ch + i + 1]), p);
+          lsum[16 * ch + i] = l.x;
+          lsum[16 * ch + i + 1] = l.y;
+          pp[i / 2] = __fmul2_rn(p, cs2);
+          const float2 z = __fmul2_rn(p, cz2);
+          x[i] = z.x;
+          x[i + 1] = z.y;
+        }
+        store_p(ch, pp);
+        if (!fresh) {                      // gamma, first half
+          const float m = tree_reduce<false>(x, lane);
+          if (lane < 16) part()[warp * 32 + 16 * ch + lane] = m;
+        }
+      }
+    }
+    product(true);
+    if (valid && !fresh) join_rows();      // gamma
+    wait_pv();
+    if (valid) {
+      const float of = (fresh ? 1.f : kVF) * psc.y;
+      const float2 of2 = make_float2(of, of), rv2 = make_float2(rv, rv);
+#pragma unroll
+      for (int ch = 0; ch < CT / 16; ++ch) {
+        float o[16];
+        tree_read<R>(trow + kTrO, half, ch, o);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (!fresh) w = *reinterpret_cast<const float4*>(gam() + CT * half + 16 * ch + i);
+          const int j = 16 * ch + i;
+          const float2 y = __ffma2_rn(rv2, __ffma2_rn(make_float2(o[i], o[i + 1]), of2, make_float2(w.x, w.y)),
+                                      make_float2(acc[j], acc[j + 1]));
+          const float2 z = __ffma2_rn(rv2, __ffma2_rn(make_float2(o[i + 2], o[i + 3]), of2, make_float2(w.z, w.w)),
+                                      make_float2(acc[j + 2], acc[j + 3]));
+          acc[j] = y.x; acc[j + 1] = y.y; acc[j + 2] = z.x; acc[j + 3] = z.y;
+        }
+      }
+    }
+    tc_fence_before();
+    return true;
+  }
+
+  // Items [gb, ge).
+  __device__ void run(int64_t gb, int64_t ge, int64_t team) {
+    if (gb >= ge) return;
+    uint32_t issued = 0, used = 0;             // packed tiles: copies started (thread 0), taken
+    if (tt == 0) {
+      TreeCursor c;
+      tree_locate<R>(a, gb, c);
+      cur() = c;
+      ahead() = c;
+      ahead_n() = ge - gb;
+      issued = refill(0, kTreeStages);
+    }
+    bar();
+    for (int64_t left = ge - gb; left > 0;) {  // a unit
+      const TreeCursor& c = cur();
+      int ti = c.ti;
+      const int packed = c.packed;
+      const int end = static_cast<int>(min(static_cast<int64_t>(c.items), ti + left));
+      left -= end - ti;
+      enter();
+      const int last = min(packed, end);
+      bool rotated = ti < last;                // acc will hold rotated channels
+      for (; ti < last && ok; ++ti, ++used) ok = item(false, ti, 0, used, issued) && ok;
+      if (!ok) break;
+      if (rotated && !unrotate()) break;
+      for (; ti < end && ok; ++ti) ok = item(true, 0, (ti - packed) * kB, used, issued) && ok;
+      if (!ok) break;
+      ok = named_bar_and(bar_id, kTreeTeamThreads, ok);
+      if (!ok) break;
+      flush(team + (static_cast<int64_t>(c.s) * a.hkv + c.h) * a.max_units + c.u);
+      if (tt == 0 && left > 0) tree_next_unit<R>(a, cur());
+      bar();
+    }
+    if (tt == 0)                               // after a timeout: copies still in flight
+      for (; used < issued; ++used) mbar_wait(&bars()[kTbRec + used % kTreeStages], (used / kTreeStages) & 1u, a.flags);
+  }
+
+  // Every product complete before TMEM is released.
+  __device__ void finish() {
+    if (tt == kTreeIssuer) {
+      umma_commit(&bars()[kTbFin]);
+      mbar_wait(&bars()[kTbFin], 0, a.flags);
+    }
+    __syncwarp();
+  }
+};
+
+template <int KB, int VB, bool kLean, int R, bool kMod>
+__global__ void __launch_bounds__(kTreeThreads, 1) tree_split_kernel(const __grid_constant__ TreeArgs a) {
+  using S = TreeSm<KB, VB, kLean, R>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  tree_dep_launch();
+  uint32_t* slot = reinterpret_cast<uint32_t*>(smem + S::kSlot);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int j = 0; j < kTreeTeams; ++j) {
+      uint64_t* bars = reinterpret_cast<uint64_t*>(smem + j * S::kTeam + S::kX + S::kBars);
+      for (int i = 0; i <= kTbFin; ++i) mbar_init(&bars[i], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 0) tmem_alloc(slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  tree_dep_wait();                               // the scan's prefix
+  const int j = warp >> 3;
+  const int64_t team = static_cast<int64_t>(blockIdx.x) * kTreeTeams + j;
+  const int64_t total = a.prefix[a.n_seqs];
+  TreeTeam<KB, VB, kLean, R, kMod> tm(a, smem + j * S::kTeam, tmem + j * kTrCols, j);
+  tm.run(team * total / a.n_teams, (team + 1) * total / a.n_teams, team);
+  tm.finish();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ merge
+// Block (token p, sequence s): warp w joins the records of q-heads w, w + 8, ...; lane l
+// holds channels 4l .. 4l + 3.
+template <int R>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
+  tree_dep_wait();
+  const int p = blockIdx.x, s = blockIdx.y, lane = threadIdx.x & 31;
+  const TreeSeq q = tree_seq<R>(a, s, false);
+  if (p >= q.nt) return;
+  const int hq = a.hkv * a.group;
+  const int64_t total = a.prefix[a.n_seqs];
+  const int64_t items = q.full - a.first[s] + q.fresh;
+  for (int m = threadIdx.x >> 5; m < hq; m += 8) {
+    const int h = m / a.group, row = p * a.group + m % a.group, u = row / R, r = row % R;
+    const int64_t g0 = a.prefix[s] + (static_cast<int64_t>(h) * q.units + u) * items, g1 = g0 + items - 1;
+    const int64_t unit = (static_cast<int64_t>(s) * a.hkv + h) * a.max_units + u;
+    float top = kNoMax, sum = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int64_t g = g0; g <= g1;) {
+      // team k owns items [k total / n, (k + 1) total / n): the one that has item g, then the one behind its last
+      const int64_t k = ((g + 1) * a.n_teams - 1) / total;
+      g = (k + 1) * total / a.n_teams;
+      const float* rec = a.part + (k + unit) * tree_rec_floats(R);
+      const float2 ml = *reinterpret_cast<const float2*>(rec + R * kD + 2 * r);
+      const float4 v = *reinterpret_cast<const float4*>(rec + r * kD + 4 * lane);
+      const float mn = fmaxf(top, ml.x);
+      const float c0 = ex2(top - mn), c1 = ex2(ml.x - mn);
+      top = mn;
+      sum = sum * c0 + ml.y * c1;
+      y.x = y.x * c0 + v.x * c1;
+      y.y = y.y * c0 + v.y * c1;
+      y.z = y.z * c0 + v.z * c1;
+      y.w = y.w * c0 + v.w * c1;
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const __half2 o0 = __floats2half2_rn(y.x * inv, y.y * inv), o1 = __floats2half2_rn(y.z * inv, y.w * inv);
+    *reinterpret_cast<uint2*>(a.out + ((static_cast<int64_t>(a.cu[s]) + p) * hq + m) * kD + 4 * lane) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&o0), *reinterpret_cast<const uint32_t*>(&o1));
+  }
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t tree_launch(void (*kernel)(KArgs...), dim3 grid, int block, size_t smem, bool after, cudaStream_t stream,
+                        const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int KB, int VB, bool kLean, int R, bool kMod>
 cudaError_t launch_tree_cfg(const TreeArgs& a, cudaStream_t stream) {
+  using S = TreeSm<KB, VB, kLean, R>;
   static std::atomic<unsigned long long> smem_set{0};
-  cudaError_t err = set_smem_once(tree_kernel<KB, VB, kLean>, sizeof(TreeSmem), smem_set);
-  if (err != cudaSuccess) return err;
-  tree_kernel<KB, VB, kLean><<<dim3(a.max_tree, a.hkv, a.n_seqs), 128, sizeof(TreeSmem), stream>>>(a);
-  return cudaGetLastError();
+  cudaError_t err = set_smem_once(tree_split_kernel<KB, VB, kLean, R, kMod>, S::kBytes, smem_set);
+  if (err == cudaSuccess) err = tree_launch(tree_scan_kernel<R>, dim3(1), 1024, 0, false, stream, a);
+  if (err == cudaSuccess)
+    err = tree_launch(tree_split_kernel<KB, VB, kLean, R, kMod>, dim3(a.n_teams / kTreeTeams), kTreeThreads, S::kBytes,
+                      true, stream, a);
+  if (err == cudaSuccess) err = tree_launch(tree_merge_kernel<R>, dim3(a.max_tree, a.n_seqs), 256, 0, true, stream, a);
+  return err;
+}
+
+template <int KB, int VB, bool kLean>
+cudaError_t launch_tree_preset(const TreeArgs& a, int rows, bool mod, cudaStream_t stream) {
+  if (rows == 64)
+    return mod ? launch_tree_cfg<KB, VB, kLean, 64, true>(a, stream) : launch_tree_cfg<KB, VB, kLean, 64, false>(a, stream);
+  return mod ? launch_tree_cfg<KB, VB, kLean, 32, true>(a, stream) : launch_tree_cfg<KB, VB, kLean, 32, false>(a, stream);
+}
+
+// Rows of a unit: 32 where the longest tree has no more (half the arithmetic of a tile), 64 otherwise.
+int tree_rows(int group, int max_tree) { return group * max_tree <= 32 ? 32 : 64; }
+
+size_t tree_head_bytes(int n_seqs) {   // prefix, first
+  return (static_cast<size_t>(n_seqs + 1) * 8 + static_cast<size_t>(n_seqs) * 4 + 255) / 256 * 256;
 }
 
 }  // namespace
 
 size_t tree_scratch_bytes(int n_seqs, int hkv, int group, int max_tree) {
-  (void)n_seqs; (void)hkv; (void)group; (void)max_tree;
-  return 256;
+  const int r = tree_rows(group, max_tree);
+  const size_t units = static_cast<size_t>(n_seqs) * hkv * ((group * max_tree + r - 1) / r);
+  return tree_head_bytes(n_seqs) + (units + kTreeTeams * kTreeMaxCtas) * tree_rec_floats(r) * sizeof(float);
 }
 
 cudaError_t launch_tree(const uint16_t* q, const uint16_t* k_new, const uint16_t* v_new, const uint64_t* tree_mask,
@@ -210,7 +1122,6 @@ cudaError_t launch_tree(const uint16_t* q, const uint16_t* k_new, const uint16_t
                         const uint16_t* ws, int hkv, int group, int max_blocks, int64_t num_blocks, int k_bits,
                         int v_bits, bool lean, const kvarn_score& score, uint16_t* out, void* scratch, unsigned* flags,
                         cudaStream_t stream) {
-  (void)scratch;
   TreeArgs a{};
   a.q = q; a.k_new = k_new; a.v_new = v_new;
   a.mask = tree_mask;
@@ -219,14 +1130,26 @@ cudaError_t launch_tree(const uint16_t* q, const uint16_t* k_new, const uint16_t
   a.slopes = score.slopes;
   a.out = out;
   a.flags = flags;
+  a.prefix = static_cast<int64_t*>(scratch);
+  a.first = reinterpret_cast<int32_t*>(a.prefix + n_seqs + 1);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + tree_head_bytes(n_seqs));
   a.num_blocks = num_blocks; a.n_tokens = n_tokens;
   a.n_seqs = n_seqs; a.max_tree = max_tree; a.hkv = hkv; a.group = group; a.max_blocks = max_blocks;
   a.window = score.window;
-  a.scale = score.scale; a.softcap = score.softcap;
+  a.softcap = score.softcap;
+  a.scale = score.softcap > 0.f ? score.scale / score.softcap * kLog2e : score.scale * kLog2e;
+  const int rows = tree_rows(group, max_tree);
+  a.max_units = (group * max_tree + rows - 1) / rows;
+  int dev = 0, sms = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (err != cudaSuccess) return err;
+  a.n_teams = kTreeTeams * std::max(1, std::min(sms, kTreeMaxCtas));
+  const bool mod = score.softcap > 0.f || score.window > 0 || score.slopes != nullptr;
   if (k_bits == 4 && v_bits == 2)
-    return lean ? launch_tree_cfg<4, 2, true>(a, stream) : launch_tree_cfg<4, 2, false>(a, stream);
-  if (k_bits == 4 && v_bits == 4 && !lean) return launch_tree_cfg<4, 4, false>(a, stream);
-  if (k_bits == 2 && v_bits == 2 && !lean) return launch_tree_cfg<2, 2, false>(a, stream);
+    return lean ? launch_tree_preset<4, 2, true>(a, rows, mod, stream) : launch_tree_preset<4, 2, false>(a, rows, mod, stream);
+  if (k_bits == 4 && v_bits == 4 && !lean) return launch_tree_preset<4, 4, false>(a, rows, mod, stream);
+  if (k_bits == 2 && v_bits == 2 && !lean) return launch_tree_preset<2, 2, false>(a, rows, mod, stream);
   return cudaErrorInvalidValue;
 }
 
