@@ -38,13 +38,18 @@
 namespace kvarn {
 namespace {
 
-constexpr int kTreeTeams = 2;
 constexpr int kTreeTeamThreads = 256;
-constexpr int kTreeThreads = kTreeTeams * kTreeTeamThreads;   // 128 registers each
-constexpr int kTreeIssuer = 224;       // the thread of a team (first of its last warp) that issues its UMMAs
+constexpr int kTreeIssuer = 7;         // the warp of a team that issues its UMMAs
 constexpr int kTreeStages = 2;
 constexpr int kTreeMaxCtas = 160;      // sizes the scratch
-constexpr uint32_t kTrAK = 0, kTrAV = 64, kTrS = 128, kTrO = 192, kTrCols = 256;   // TMEM columns of a team
+constexpr int kTreeMaxTeams = 3;
+// Units of 32 rows: three teams, 80 registers a thread, accumulators in registers. Units of 64
+// rows: two teams, 128 registers, accumulators in TMEM (32 of them a thread would spill).
+__host__ __device__ constexpr int tree_teams(int r) { return r == 32 ? 3 : 2; }
+// TMEM columns of a team: the key and value operands, S and O (O is written once S has been
+// read), and for 64 rows the accumulator.
+constexpr uint32_t kTrAK = 0, kTrAV = 64, kTrS = 128, kTrAcc = 192;
+__host__ __device__ constexpr uint32_t tree_cols(int r) { return r == 32 ? 160 : 256; }
 constexpr float kTau = 8.0f;
 constexpr float kNoMax = -1.0e30f;     // running max of a record whose row saw no key
 
@@ -206,45 +211,31 @@ __device__ __forceinline__ void tree_next_unit(const TreeArgs& a, TreeCursor& c)
 template <int KB, int VB, bool kLean, int R>
 struct TreeSm {
   using L = RecordLayout<KB, VB, kLean>;
-  static constexpr int kB0 = 0;                                  // B operand(s): 64 rows (hi; or hi and lo of 32)
-  static constexpr int kB1 = 16384;                              // lo rows (R = 64)
-  static constexpr int kQ = R == 64 ? 32768 : 16384;             // q_r scaled, [R][128] f32
+  static constexpr int kTeams = tree_teams(R);
+  static constexpr int kB0 = 0;                                  // B operand, hi rows (R = 32: and lo rows)
+  static constexpr int kExt = R == 64 ? 32768 : 16384;           // B of beta: [16][64 rows]
+  static constexpr int kQ = kExt + 2048;                         // q_r scaled, [R][128] f32
   static constexpr int kRec = kQ + R * 512;
-  static constexpr int kX = kRec + kTreeStages * ((L::kBytes + 15) / 16 * 16);
-  // small arrays at kX
-  static constexpr int kBeta = 0, kMax = 256, kGam = 512, kPos = 768, kSlope = 1024, kMask = 1280;
-  static constexpr int kPart = 1792;                             // [8 warps][32] f32
-  static constexpr int kCsMax = 2816, kBars = 2880;
-  static constexpr int kCur = 2944, kAhead = 2992;               // cursors: the team's, the copies'
-  static constexpr int kAheadN = 3040, kValid = 3048;            // items left to the copies; the stages' tiles are valid
-  static constexpr int kXBytes = 3056;
+  static constexpr int kRecPitch = (L::kBytes + 15) / 16 * 16;
+  static constexpr int kU = kRec + kTreeStages * kRecPitch;      // A of gamma: [128 tokens][8 x u]
+  static constexpr int kOne = kU + 2048;                         // A of beta: [16][8]
+  static constexpr int kAdd = kOne + 256;                        // [128] fp16: what the values' operand adds
+  static constexpr int kX = kAdd + 256;
+  // small arrays at kX, [R] each: negated maxima, sums, positions, slopes; mask words
+  static constexpr int kMax = 0, kGam = 4 * R, kPos = 8 * R, kSlope = 12 * R, kMask = 16 * R;
+  static constexpr int kPart = 24 * R;                           // [8 warps][R / 2] f32
+  static constexpr int kSmall = kPart + 16 * R;                  // 16 floats
+  static constexpr int kBars = kSmall + 64;
+  static constexpr int kCur = kBars + 48, kAhead = kCur + 48;    // cursors: the team's, the copies'
+  static constexpr int kAheadN = kAhead + 48, kValid = kAheadN + 8;   // items left to the copies; valid tiles in the stages
+  static constexpr int kXBytes = kValid + 8;
   static constexpr int kTeam = (kX + kXBytes + 1023) / 1024 * 1024;
-  static constexpr int kSlot = kTreeTeams * kTeam;
+  static constexpr int kSlot = kTeams * kTeam;
   static constexpr int kBytes = kSlot + 16;
-  static_assert(sizeof(TreeCursor) <= 48, "cursor");
   static_assert(kBytes <= 232448, "tree shared memory");
+  static_assert(sizeof(TreeCursor) <= 48, "cursor");
 };
 constexpr int kTbRec = 0, kTbQkDone = 2, kTbPvDone = 3, kTbFin = 4;
-
-// Columns 16 ch .. 16 ch + 15 of this thread's R / 2 rows of a 64-column product. R = 64: rows
-// 32 half + 16 ch ..; R = 32: rows 16 half .., the sums of the hi columns (row) and the lo
-// columns (32 + row).
-template <int R>
-__device__ __forceinline__ void tree_read(uint32_t trow, int half, int ch, float (&v)[16]) {
-  if (R == 64) {
-    tc_ld16(trow + 32 * half + 16 * ch, v);
-  } else {
-    float lo[16];
-    tc_ld16(trow + 16 * half, v);
-    tc_ld16(trow + 32 + 16 * half, lo);
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      const float2 x = __fadd2_rn(make_float2(v[i], v[i + 1]), make_float2(lo[i], lo[i + 1]));
-      v[i] = x.x;
-      v[i + 1] = x.y;
-    }
-  }
-}
 
 // Sum (or maximum) over the warp's 32 lanes of 16 values: lane l returns that of value l % 16.
 template <bool kMaxOp>
@@ -263,7 +254,7 @@ __device__ __forceinline__ float tree_reduce(float (&g)[16], int lane) {
   return kMaxOp ? fmaxf(g[0], got) : g[0] + got;
 }
 
-// Byte offset of (row, channel) in a 64-row fp16 B operand, K = channels: 128-byte
+// Byte offset of (row, K index) in a 64-row fp16 B operand, K = channels: 128-byte
 // swizzled K-major, halves of 64 channels 8192 bytes apart.
 __device__ __forceinline__ uint32_t tree_qo(int r, int ch) {
   return static_cast<uint32_t>((ch >> 6) * 8192 + (r >> 3) * 1024 + (r & 7) * 128 +
@@ -276,71 +267,122 @@ __device__ __forceinline__ uint32_t tree_po(int c, int tok) {
 }
 
 // ------------------------------------------------------------------ operands
-// Keys: token t's codes of channels 64 half .. 64 half + 63 -> 32 TMEM columns.
-template <int KB>
-__device__ __forceinline__ void tree_keys(const uint8_t* codes, int t, int half, uint32_t taddr) {
-  uint32_t r[32];
-  if (KB == 4) {
-    const uint4* row = reinterpret_cast<const uint4*>(codes + t * 64);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint2 w2 = reinterpret_cast<const uint2*>(row + c)[half];   // words 2 half, 2 half + 1
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const uint32_t w = m ? w2.y : w2.x;
-        cvt4(w & 0x0F0F0F0Fu, r[16 * m + c], r[16 * m + 4 + c]);
-        cvt4((w >> 4) & 0x0F0F0F0Fu, r[16 * m + 8 + c], r[16 * m + 12 + c]);
-      }
-    }
-  } else {
-    // group g, word half: byte b = channel bits 4-5; crumbs 2 bit0 + bit3
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t x = *reinterpret_cast<const uint32_t*>(codes + t * 32 + c * 8 + half * 4);
-      uint32_t v0[4], v1[4];
-      cvt2(x & 0x33333333u, v0);
-      cvt2((x >> 2) & 0x33333333u, v1);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        r[8 * b + c] = v0[b];
-        r[8 * b + 4 + c] = v1[b];
-      }
-    }
-  }
-  tc_st32(taddr, r);
+// A record's 16-byte parts (keys: of a token; 4-bit values: of a channel; 2-bit values: the
+// cells of a channel) hold the elements 16 j + 8 a + 2 c + e in part c. Half h of a team takes
+// parts 2h and 2h + 1, so the K index of such an operand is not the element's own but
+//   64 (c >> 1) + 8 j + 4 a + 2 (c & 1) + e,
+// and the other operand is laid out to match: q' by its writer, p' by the token that a lane
+// stands for (tree_token is the inverse for tokens).
+__device__ __forceinline__ int tree_token(int t) {
+  return (t & 3) | ((t >> 6) & 1) << 2 | ((t >> 2) & 1) << 3 | ((t >> 3) & 7) << 4;
 }
-// Values: channel t's codes of tokens 64 half .. -> 32 TMEM columns.
-template <int VB>
-__device__ __forceinline__ void tree_values(const uint8_t* codes, int t, int half, uint32_t taddr) {
-  uint32_t r[32];
-  if (VB == 4) {
-    const uint4* row = reinterpret_cast<const uint4*>(codes + t * 64);
+// Thread t of the warp: 16 consecutive columns of TMEM lane (base lane + t) from r.
+__device__ __forceinline__ void tree_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tree_add16(uint32_t (&r)[16], const uint16_t* add) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint2 w2 = reinterpret_cast<const uint2*>(row + c)[half];
+  for (int i = 0; i < 4; ++i) {
+    const uint4 v = reinterpret_cast<const uint4*>(add)[i];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const uint32_t w = m ? w2.y : w2.x;
-        cvt4(w & 0x0F0F0F0Fu, r[16 * m + c], r[16 * m + 4 + c]);
-        cvt4((w >> 4) & 0x0F0F0F0Fu, r[16 * m + 8 + c], r[16 * m + 12 + c]);
-      }
-    }
-  } else {
-    const uint8_t* base = codes + (t >> 4) * 512 + (t & 7) * 64 + ((t >> 3) & 1) * 8 + half * 4;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint32_t x = *reinterpret_cast<const uint32_t*>(base + c * 16);
-      uint32_t v0[4], v1[4];
-      cvt2(x & 0x33333333u, v0);
-      cvt2((x >> 2) & 0x33333333u, v1);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        r[8 * b + c] = v0[b];
-        r[8 * b + 4 + c] = v1[b];
-      }
+    for (int e = 0; e < 4; ++e) {
+      const __half2 x = __hadd2(*reinterpret_cast<const __half2*>(&r[4 * i + e]), *reinterpret_cast<const __half2*>(&w[e]));
+      r[4 * i + e] = *reinterpret_cast<const uint32_t*>(&x);
     }
   }
-  tc_st32(taddr, r);
+}
+// Rows of 64 bytes of 4-bit codes: row `row`'s parts 2 half, 2 half + 1 as fp16 code / 8
+// (+ add, by K element) to 32 TMEM columns. Lanes read their two parts in an order of their own, which leaves 2-way
+// bank conflicts of 4-way ones.
+template <bool kAdd>
+__device__ __forceinline__ void tree_codes4(const uint8_t* codes, int row, int half, const uint16_t* add, uint32_t taddr) {
+  const uint4* p = reinterpret_cast<const uint4*>(codes + row * 64) + 2 * half;
+  const bool swap = (row >> 1) & 1;
+  const uint4 x = p[swap ? 1 : 0], y = p[swap ? 0 : 1];
+  const uint32_t w[2][4] = {{swap ? y.x : x.x, swap ? y.y : x.y, swap ? y.z : x.z, swap ? y.w : x.w},
+                            {swap ? x.x : y.x, swap ? x.y : y.y, swap ? x.z : y.z, swap ? x.w : y.w}};
+#pragma unroll
+  for (int mm = 0; mm < 2; ++mm) {
+    uint32_t r[16];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const uint32_t u = w[c][2 * mm + m];
+        cvt4(u & 0x0F0F0F0Fu, r[8 * m + c], r[8 * m + 2 + c]);
+        cvt4((u >> 4) & 0x0F0F0F0Fu, r[8 * m + 4 + c], r[8 * m + 6 + c]);
+      }
+    if (kAdd) tree_add16(r, add + 32 * mm);
+    tree_st16(taddr + 16 * mm, r);
+  }
+}
+// 2-bit codes [part][word] as fp16 code / 2 (+ add) to 32 TMEM columns.
+template <bool kAdd>
+__device__ __forceinline__ void tree_codes2(const uint32_t (&w)[2][2], const uint16_t* add, uint32_t taddr) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    uint32_t r[16];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t v0[4], v1[4];
+      cvt2(w[c][u] & 0x33333333u, v0);
+      cvt2((w[c][u] >> 2) & 0x33333333u, v1);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        r[4 * b + c] = v0[b];
+        r[4 * b + 2 + c] = v1[b];
+      }
+    }
+    if (kAdd) tree_add16(r, add + 32 * u);
+    tree_st16(taddr + 16 * u, r);
+  }
+}
+// Keys of token `tok`.
+template <int KB>
+__device__ __forceinline__ void tree_keys(const uint8_t* codes, int tok, int half, uint32_t taddr) {
+  if (KB == 4) {
+    tree_codes4<false>(codes, tok, half, nullptr, taddr);
+  } else {
+    const uint4 v = reinterpret_cast<const uint4*>(codes + tok * 32)[half];
+    const uint32_t w[2][2] = {{v.x, v.y}, {v.z, v.w}};
+    tree_codes2<false>(w, nullptr, taddr);
+  }
+}
+// Values of channel t plus their token's `add` (by K element; sums exact in fp16).
+template <int VB>
+__device__ __forceinline__ void tree_values(const uint8_t* codes, int t, int half, const uint16_t* add, uint32_t taddr) {
+  if (VB == 4) {
+    tree_codes4<true>(codes, t, half, add + 64 * half, taddr);
+  } else {
+    const uint2* p = reinterpret_cast<const uint2*>(codes + (t >> 4) * 512 + (t & 7) * 64 + ((t >> 3) & 1) * 8 + half * 32);
+    const bool swap = (t >> 1) & 1;
+    const uint2 x = p[swap ? 2 : 0], y = p[swap ? 0 : 2];
+    const uint32_t w[2][2] = {{swap ? y.x : x.x, swap ? y.y : x.y}, {swap ? x.x : y.x, swap ? x.y : y.y}};
+    tree_codes2<true>(w, add + 64 * half, taddr);
+  }
+}
+
+// One lane of the (converged) warp. Chosen this way, rather than by its number, the compiler
+// keeps the operands of the UMMAs it issues in uniform registers: 16 of them (N = 64) take
+// 600 cycles from the first to the completion of the last, 1020 otherwise.
+__device__ __forceinline__ bool tree_elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+// An operand with its M (or N) elements contiguous, not swizzled, whose groups of 8 are all the
+// same 16 bytes a K element (stride 0): the operand's 128 rows are 8 that repeat.
+__device__ __forceinline__ uint64_t tree_desc_same(uint32_t saddr) {
+  uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(128u >> 4) << 16;    // leading byte offset: the next 8 K elements
+  d |= static_cast<uint64_t>(1) << 46;            // (stride byte offset 0; no swizzle)
+  return d;
 }
 
 // A team's work. Thread tt of 256: lane t = tt & 127 (token or channel), half = tt >> 7.
@@ -350,13 +392,19 @@ struct TreeTeam {
   using S = TreeSm<KB, VB, kLean, R>;
   static constexpr int CT = R / 2;               // rows (columns of the products) of a thread
   static constexpr float kKF = KB == 4 ? 8.f : 2.f, kVF = VB == 4 ? 8.f : 2.f;   // codes were converted to code / kKF
-  static constexpr int kRecPitch = (L::kBytes + 15) / 16 * 16;
-  static constexpr int kLoRow = R == 64 ? 0 : 32;
+  static constexpr float kMid = VB == 4 ? 7.5f : 1.5f;   // of the value codes
+  // gamma_row = sum_t p c z = sum_t p' u, u = z / s, is folded into PV: the value operand is
+  // code + u^, u^ the multiple of kUStep nearest to u (exact in fp16), and the rest u - u^ goes
+  // in as one more product, whose A has the same value in every channel's row. A token whose
+  // zero is more than kWide steps off the middle of the code range (a constant group, whose step
+  // has its least value) has u^ = -kMid and no rest there; its part is summed over the lanes.
+  static constexpr float kWide = VB == 4 ? 4.f : 1.f;
+  static constexpr float kUStep = VB == 4 ? 1.f / 128.f : 1.f / 256.f;
   const TreeArgs& a;
   uint8_t* sm;
   uint32_t tm, trow;                             // TMEM address of the team, of the thread's warp
   int tt, t, half, lane, warp, bar_id;
-  float acc[CT], lsum[CT];
+  float acc[R == 32 ? CT : 1], lsum[CT];
   float qinv;                                    // 2^-e of the stored q_r
   uint32_t qph, pph;
   bool ok;
@@ -364,19 +412,18 @@ struct TreeTeam {
   bool pending;                                  // some row of the unit has not (the team agrees)
 
   __device__ TreeTeam(const TreeArgs& a_, uint8_t* sm_, uint32_t tm_, int team)
-      : a(a_), sm(sm_), tm(tm_), bar_id(1 + 3 * team), qinv(1.f), qph(0), pph(0), ok(true), row_set(false), pending(true) {
+      : a(a_), sm(sm_), tm(tm_), bar_id(1 + 2 * team), qinv(1.f), qph(0), pph(0), ok(true), row_set(false), pending(true) {
     tt = static_cast<int>(threadIdx.x) - team * kTreeTeamThreads;
     t = tt & 127;
     half = tt >> 7;
     lane = tt & 31;
-    warp = tt >> 5;
+    warp = __shfl_sync(0xffffffffu, tt >> 5, 0);   // known to be the same for the warp
     trow = tm + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
   }
-  __device__ float* beta() const { return reinterpret_cast<float*>(sm + S::kX + S::kBeta); }
   __device__ float* mrow() const { return reinterpret_cast<float*>(sm + S::kX + S::kMax); }
   __device__ float* gam() const { return reinterpret_cast<float*>(sm + S::kX + S::kGam); }
   __device__ float* part() const { return reinterpret_cast<float*>(sm + S::kX + S::kPart); }
-  __device__ float* csmax() const { return reinterpret_cast<float*>(sm + S::kX + S::kCsMax); }
+  __device__ float* small() const { return reinterpret_cast<float*>(sm + S::kX + S::kSmall); }
   __device__ float* slope() const { return reinterpret_cast<float*>(sm + S::kX + S::kSlope); }
   __device__ int32_t* pos() const { return reinterpret_cast<int32_t*>(sm + S::kX + S::kPos); }
   __device__ uint64_t* mask() const { return reinterpret_cast<uint64_t*>(sm + S::kX + S::kMask); }
@@ -386,36 +433,88 @@ struct TreeTeam {
   __device__ int64_t& ahead_n() const { return *reinterpret_cast<int64_t*>(sm + S::kX + S::kAheadN); }
   __device__ volatile uint32_t* valid_of() const { return reinterpret_cast<volatile uint32_t*>(sm + S::kX + S::kValid); }
   __device__ void bar() { named_bar(bar_id, kTreeTeamThreads); }
-  __device__ uint8_t* b_lo() { return R == 64 ? sm + S::kB1 : sm + S::kB0; }   // where lo rows go
+  static __device__ uint32_t tree_qo_lo(int r, int k) { return R == 64 ? 16384 + tree_qo(r, k) : tree_qo(r + 32, k); }
 
-  // The thread's operand writes are done; the issuer, once everyone's are, starts the product.
-  __device__ void product(bool pv) {
+  // The thread's operand writes are done; once everyone's are, the issuer starts the product.
+  // QK^T: the whole team meets (what it wrote for the values is visible then).
+  __device__ void product_qk(bool fresh) {
     tc_operands_written();
-    const int id = bar_id + (pv ? 2 : 1);
-    if (warp != kTreeIssuer / 32) {
-      asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(kTreeTeamThreads) : "memory");
-      return;
-    }
-    named_bar(id, kTreeTeamThreads);
-    if (lane == 0) {
+    bar();
+    if (warp != kTreeIssuer) return;
+    if (tree_elect()) {
       tc_fence_after();
-      constexpr uint32_t kIdQk = idesc_f16_f32(128, 64), kIdPv = kIdQk | (1u << 16);   // bit 16: B is N-major
-      constexpr int kParts = R / 32;             // operands of 64 rows: (hi and lo), or hi, lo
-      const uint32_t b = smem_u32(sm + S::kB0);
+      // bit 15: A, bit 16: B with M or N contiguous
+      constexpr uint32_t kId = idesc_f16_f32(128, R), kIdSame = kId | (1u << 15) | (1u << 16);
+      const uint64_t d = smem_desc_sw128(smem_u32(sm + S::kB0));
 #pragma unroll
-      for (int p = 0; p < kParts; ++p)
+      for (int s = 0; s < 8; ++s)
+        tc_umma_ts(tm + kTrS, tm + kTrAK + 8 * s, d + (((s >> 2) * 8192 + (s & 3) * 32) >> 4), kId, s > 0);
+      if (!fresh) {                              // (fresh: q is exact in fp16)
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          if (pv)
-            tc_umma_ts(tm + kTrO, tm + kTrAV + 8 * s, smem_desc_sw128(b + p * 16384 + s * 2048), kIdPv, p + s > 0);
-          else
-            tc_umma_ts(tm + kTrS, tm + kTrAK + 8 * s, smem_desc_sw128(b + p * 16384 + (s >> 2) * 8192 + (s & 3) * 32),
-                       kIdQk, p + s > 0);
-        }
-      umma_commit(&bars()[pv ? kTbPvDone : kTbQkDone]);
+        for (int s = 0; s < 8; ++s)
+          tc_umma_ts(tm + kTrS, tm + kTrAK + 8 * s,
+                     d + (((R == 64 ? 16384 : 4096) + (s >> 2) * 8192 + (s & 3) * 32) >> 4), kId, 1);
+        umma_f16(tm + kTrS, tree_desc_same(smem_u32(sm + S::kOne)), smem_desc_sw128(smem_u32(sm + S::kExt)), kIdSame, 1);
+      }
+      umma_commit(&bars()[kTbQkDone]);
     }
     __syncwarp();
   }
+  // PV: only the issuer waits.
+  __device__ void product_pv(bool gamma) {
+    tc_operands_written();
+    if (warp != kTreeIssuer) {
+      asm volatile("bar.arrive %0, %1;" ::"r"(bar_id + 1), "r"(kTreeTeamThreads) : "memory");
+      return;
+    }
+    named_bar(bar_id + 1, kTreeTeamThreads);
+    if (tree_elect()) {
+      tc_fence_after();
+      constexpr uint32_t kId = idesc_f16_f32(128, R) | (1u << 16), kIdSame = kId | (1u << 15);
+      const uint64_t d = smem_desc_sw128(smem_u32(sm + S::kB0));
+#pragma unroll
+      for (int p = 0; p < 2; ++p)                // lo rows: the next operand, or 64 bytes along a token's rows
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          tc_umma_ts(tm + kTrS, tm + kTrAV + 8 * s, d + ((p * (R == 64 ? 16384 : 64) + s * 2048) >> 4), kId, p + s > 0);
+      if (gamma) {
+        const uint64_t u = tree_desc_same(smem_u32(sm + S::kU));
+#pragma unroll
+        for (int s = 0; s < 8; ++s) umma_f16(tm + kTrS, u + ((s * 256) >> 4), d + ((s * 2048) >> 4), kIdSame, 1);
+      }
+      umma_commit(&bars()[kTbPvDone]);
+    }
+    __syncwarp();
+  }
+  // 16 of the thread's rows of S or O, and of the accumulator.
+  __device__ void read16(int ch, float (&v)[16]) { tc_ld16(trow + kTrS + CT * half + 16 * ch, v); }
+  __device__ void get_acc(int ch, float (&v)[16]) {
+    if constexpr (R == 32) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = acc[i];
+    } else {
+      tc_ld16(trow + kTrAcc + CT * half + 16 * ch, v);
+    }
+  }
+  __device__ void put_acc(int ch, const float (&v)[16]) {
+    if constexpr (R == 32) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[i] = v[i];
+    } else {
+      tree_st16(trow + kTrAcc + CT * half + 16 * ch, reinterpret_cast<const uint32_t(&)[16]>(v));
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    }
+  }
+
+  // The constant operand of beta (64 at two K elements) and the zeros of its other one.
+  __device__ void init() {
+    for (int i = tt; i < 16; i += kTreeTeamThreads)
+      reinterpret_cast<uint4*>(sm + S::kOne)[i] =
+          i < 2 ? make_uint4(0x54005400u, 0x54005400u, 0x54005400u, 0x54005400u) : make_uint4(0, 0, 0, 0);
+    for (int i = tt; i < 128; i += kTreeTeamThreads) reinterpret_cast<uint4*>(sm + S::kExt)[i] = make_uint4(0, 0, 0, 0);
+  }
+
+  static __device__ int q_slot(int g) { return 16 * ((g >> 1) & 1) + 2 * (g >> 2) + (g & 1); }
 
   // Rows of the unit at the cursor: row tables, q_r scaled by a power of two in shared memory.
   __device__ void enter() {
@@ -474,9 +573,10 @@ struct TreeTeam {
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-      float4* dst = reinterpret_cast<float4*>(qs + r * kD + 8 * jj);
-      dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-      dst[1] = make_float4(x[4], x[5], x[6], x[7]);
+      // channels 4 G .. at 16-byte slot 16 e + j of the row (fold's thread j reads slots j, 16 + j)
+      float4* dst = reinterpret_cast<float4*>(qs + r * kD);
+      dst[q_slot(2 * jj)] = make_float4(x[0], x[1], x[2], x[3]);
+      dst[q_slot(2 * jj + 1)] = make_float4(x[4], x[5], x[6], x[7]);
     }
     m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
     if (lane == 0) part()[warp] = m;
@@ -487,43 +587,49 @@ struct TreeTeam {
     qinv = sc.y;
 #pragma unroll
     for (int k = 0; k < R / 16; ++k) {             // the thread's own elements
-      float4* p = reinterpret_cast<float4*>(qs + (r0 + 16 * k) * kD + 8 * jj);
+      float4* p = reinterpret_cast<float4*>(qs + (r0 + 16 * k) * kD);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float4 v = p[e];
-        p[e] = make_float4(v.x * sc.x, v.y * sc.x, v.z * sc.x, v.w * sc.x);
+        const int i = q_slot(2 * jj + e);
+        const float4 v = p[i];
+        p[i] = make_float4(v.x * sc.x, v.y * sc.x, v.z * sc.x, v.w * sc.x);
       }
     }
 #pragma unroll
-    for (int i = 0; i < CT; ++i) acc[i] = lsum[i] = 0.f;
+    for (int i = 0; i < CT; ++i) lsum[i] = 0.f;
+    const float zero[16] = {};
+#pragma unroll
+    for (int ch = 0; ch < CT / 16; ++ch) put_acc(ch, zero);
     row_set = false;
     pending = true;
     bar();                                          // part is used again
   }
 
-  // q' rows and beta of a packed tile; returns 2^-k of the tile's scaling of r s.
+  // q' rows and beta of a packed tile; returns 2^-k of the tile's scaling of r s. Thread j of a
+  // row's 16 takes channels ch .. ch + 3 and ch + 8 .. ch + 11, ch = 16 (j >> 1) + 4 (j & 1).
   __device__ float fold(const uint8_t* rec) {
     const uint16_t* km = reinterpret_cast<const uint16_t*>(rec + L::kKMetaOff);
-    const int jj = tt & 15, r0 = tt >> 4;
-    const uint4 sv = *reinterpret_cast<const uint4*>(km + L::kKs + 8 * jj);
-    const uint4 zv = *reinterpret_cast<const uint4*>(km + L::kKz + 8 * jj);
-    uint4 rv = make_uint4(kH_One, kH_One, kH_One, kH_One);
-    if (!kLean) rv = *reinterpret_cast<const uint4*>(km + L::kKr + 8 * jj);
-    const uint32_t s4[4] = {sv.x, sv.y, sv.z, sv.w}, z4[4] = {zv.x, zv.y, zv.z, zv.w};
-    const uint32_t r4[4] = {rv.x, rv.y, rv.z, rv.w};
+    const int jj = tt & 15, r0 = tt >> 4, ch = 16 * (jj >> 1) + 4 * (jj & 1);
     float2 rs[4], rz[4];
     float m = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      rs[e] = mul_h2(r4[e], s4[e]);
-      rz[e] = mul_h2(r4[e], z4[e]);
-      m = fmax3f(m, rs[e].x, rs[e].y);
+    for (int e = 0; e < 2; ++e) {
+      const uint2 sv = *reinterpret_cast<const uint2*>(km + L::kKs + ch + 8 * e);
+      const uint2 zv = *reinterpret_cast<const uint2*>(km + L::kKz + ch + 8 * e);
+      uint2 rv = make_uint2(kH_One, kH_One);
+      if (!kLean) rv = *reinterpret_cast<const uint2*>(km + L::kKr + ch + 8 * e);
+      rs[2 * e] = mul_h2(rv.x, sv.x);
+      rs[2 * e + 1] = mul_h2(rv.y, sv.y);
+      rz[2 * e] = mul_h2(rv.x, zv.x);
+      rz[2 * e + 1] = mul_h2(rv.y, zv.y);
+      m = fmax3f(m, rs[2 * e].x, rs[2 * e].y);
+      m = fmax3f(m, rs[2 * e + 1].x, rs[2 * e + 1].y);
     }
     // the scales are positive: their maximum over the tile's channels as integers
     m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
     const float2 sc = tc_pow2_scale(m, 0);          // the largest r s into [1, 2)
     const float2 sc2 = make_float2(sc.x, sc.x);
-    const float zf = sc.x / kKF;                    // beta in the units of S
+    const float zf = sc.x / (kKF * 64.f);           // beta in the units of S, over its operand's 64
     const float2 zf2 = make_float2(zf, zf);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -535,8 +641,8 @@ struct TreeTeam {
 #pragma unroll
     for (int k = 0; k < R / 16; ++k) {
       const int r = r0 + 16 * k;
-      const float4* p = reinterpret_cast<const float4*>(qs + r * kD + 8 * jj);
-      const float4 u = p[0], v = p[1];
+      const float4* p = reinterpret_cast<const float4*>(qs + r * kD);
+      const float4 u = p[jj], v = p[16 + jj];
       const float2 x[4] = {make_float2(u.x, u.y), make_float2(u.z, u.w), make_float2(v.x, v.y), make_float2(v.z, v.w)};
       uint32_t hi[4], lo[4];
       float2 b2 = make_float2(0.f, 0.f);
@@ -546,20 +652,35 @@ struct TreeTeam {
         b2 = __ffma2_rn(x[e], rz[e], b2);
       }
       b[k] = b2.x + b2.y;
-      *reinterpret_cast<uint4*>(sm + S::kB0 + tree_qo(r, 8 * jj)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(b_lo() + tree_qo(r + kLoRow, 8 * jj)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      const int kk = 64 * (jj & 1) + 8 * (jj >> 1);
+      *reinterpret_cast<uint4*>(sm + S::kB0 + tree_qo(r, kk)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(sm + S::kB0 + tree_qo_lo(r, kk)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    // over the row's 16 threads: thread j ends up with row r0 + 16 (j & 3)'s sum (or (j & 1)'s)
+    constexpr int kRows = R / 16;
+#pragma unroll
+    for (int o = kRows / 2; o >= 1; o >>= 1) {
+      const bool up = (jj & o) != 0;
+#pragma unroll
+      for (int i = 0; i < o; ++i) {
+        const float send = up ? b[i] : b[i + o], keep = up ? b[i + o] : b[i];
+        b[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+      }
     }
 #pragma unroll
-    for (int k = 0; k < R / 16; ++k) {
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) b[k] += __shfl_xor_sync(0xffffffffu, b[k], o);
-      if (jj == 0) beta()[r0 + 16 * k] = b[k];
+    for (int o = kRows; o < 16; o <<= 1) b[0] += __shfl_xor_sync(0xffffffffu, b[0], o);
+    if (jj < kRows) {
+      const int r = r0 + 16 * jj;
+      const __half h = __float2half_rn(b[0]);
+      uint8_t* ext = sm + S::kExt + (r & 7) * 2;
+      *reinterpret_cast<__half*>(ext + ((r >> 3) << 4)) = h;                                     // K element 0
+      *reinterpret_cast<__half*>(ext + 128 + (((r >> 3) ^ 1) << 4)) = __float2half_rn(b[0] - __half2float(h));   // 1
     }
     return sc.y;
   }
 
   // Operands of fresh tokens [f0, f0 + 128) of the cursor's sequence: keys and values as
-  // they are, q as it is (hi rows; lo rows 0).
+  // they are, q as it is (hi rows).
   __device__ const uint16_t* fresh_row(int f, bool value) const {
     const TreeCursor& c = cur();
     if (f < c.ws) return a.ws + ((static_cast<int64_t>(c.s) * a.hkv + c.h) * 2 + (value ? 1 : 0)) * (kB * kD) + f * kD;
@@ -590,22 +711,26 @@ struct TreeTeam {
       if (p < c.nt)
         w = *reinterpret_cast<const uint4*>(a.q + ((c0 + p) * hq + c.h * a.group + row % a.group) * kD + 8 * jj);
       *reinterpret_cast<uint4*>(sm + S::kB0 + tree_qo(rr, 8 * jj)) = w;
-      *reinterpret_cast<uint4*>(b_lo() + tree_qo(rr + kLoRow, 8 * jj)) = make_uint4(0, 0, 0, 0);
     }
-    if (tt < R) beta()[tt] = 0.f;
   }
   __device__ void fresh_values(int f0) {
     const TreeCursor& c = cur();
-    uint32_t r[32];
-    const int n = c.ws + c.nt;
+    const int nw = c.ws - f0, n = nw + c.nt;               // workspace tokens, all tokens from f0 on
+    const uint16_t* w = a.ws + ((static_cast<int64_t>(c.s) * a.hkv + c.h) * 2 + 1) * (kB * kD) + f0 * kD + t;
+    const int64_t step = static_cast<int64_t>(a.hkv) * kD;
+    const uint16_t* v = a.v_new + (static_cast<int64_t>(a.cu[c.s]) * a.hkv + c.h) * kD + t - nw * step;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const int f = f0 + 64 * half + 2 * i;
-      const uint32_t x = f < n ? fresh_row(f, true)[t] : 0;
-      const uint32_t y = f + 1 < n ? fresh_row(f + 1, true)[t] : 0;
-      r[i] = x | (y << 16);
+    for (int part = 0; part < 2; ++part) {
+      uint32_t r[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int f = 64 * half + 32 * part + 2 * i;
+        const uint32_t x = f < nw ? w[f * kD] : f < n ? v[f * step] : 0;
+        const uint32_t y = f + 1 < nw ? w[(f + 1) * kD] : f + 1 < n ? v[(f + 1) * step] : 0;
+        r[i] = x | (y << 16);
+      }
+      tree_st16(trow + kTrAV + 32 * half + 16 * part, r);
     }
-    tc_st32(trow + kTrAV + 32 * half, r);
   }
 
   // Wait for a product; every thread of the team agrees on the outcome at the next barrier.
@@ -626,23 +751,21 @@ struct TreeTeam {
     int chunk_i;       // index among the drafted tokens, or -1
     bool key, fresh;
   };
-  // Scores of 16 rows relative to their running max: x = f (S + beta) (then cap and bias) -
-  // max; masked keys -inf.
+  // Scores of 16 rows relative to their running max: x = f S (then cap and bias) - max; masked
+  // keys -inf.
   __device__ void scores(int ch, const Keys& k, float (&x)[16]) {
-    tree_read<R>(trow + kTrS, half, ch, x);
+    read16(ch, x);
     const float2 f2 = make_float2(k.f, k.f);
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       const int col = CT * half + 16 * ch + i;
-      const float4 b = *reinterpret_cast<const float4*>(beta() + col), m = *reinterpret_cast<const float4*>(mrow() + col);
-      float2 u = __fadd2_rn(make_float2(x[i], x[i + 1]), make_float2(b.x, b.y));
-      float2 v = __fadd2_rn(make_float2(x[i + 2], x[i + 3]), make_float2(b.z, b.w));
+      const float4 m = *reinterpret_cast<const float4*>(mrow() + col);
       if (!kMod) {
-        u = __ffma2_rn(u, f2, make_float2(-m.x, -m.y));
-        v = __ffma2_rn(v, f2, make_float2(-m.z, -m.w));
+        const float2 u = __ffma2_rn(make_float2(x[i], x[i + 1]), f2, make_float2(m.x, m.y));
+        const float2 v = __ffma2_rn(make_float2(x[i + 2], x[i + 3]), f2, make_float2(m.z, m.w));
         x[i] = u.x; x[i + 1] = u.y; x[i + 2] = v.x; x[i + 3] = v.y;
       } else {
-        const float s[4] = {u.x * k.f, u.y * k.f, v.x * k.f, v.y * k.f}, mm[4] = {m.x, m.y, m.z, m.w};
+        const float s[4] = {x[i] * k.f, x[i + 1] * k.f, x[i + 2] * k.f, x[i + 3] * k.f}, mm[4] = {m.x, m.y, m.z, m.w};
         const int4 pq = *reinterpret_cast<const int4*>(pos() + col);
         const float4 sl = *reinterpret_cast<const float4*>(slope() + col);
         const int pp[4] = {pq.x, pq.y, pq.z, pq.w};
@@ -655,7 +778,7 @@ struct TreeTeam {
           const int64_t gap = static_cast<int64_t>(pp[e]) - k.pk;
           y = fmaf(-ss[e], static_cast<float>(gap), y);
           if (a.window > 0 && gap >= a.window) y = -INFINITY;
-          x[i + e] = y - mm[e];
+          x[i + e] = y + mm[e];
         }
       }
       if (k.fresh) {
@@ -674,31 +797,37 @@ struct TreeTeam {
       float x[16];
       scores(ch, k, x);
       float m = tree_reduce<true>(x, lane);
-      if (lane < 16) part()[warp * 32 + 16 * ch + lane] = valid ? m : -INFINITY;
+      if (lane < 16) part()[warp * CT + 16 * ch + lane] = valid ? m : -INFINITY;
     }
     bar();
     if (tt < R) {                                   // row tt: its half's four warps
-      const float* p = part() + 4 * (tt / CT) * 32 + tt % CT;
-      float d = fmax3f(fmaxf(p[0], p[32]), p[64], p[96]);   // relative to the running max
+      const float* p = part() + 4 * (tt / CT) * CT + tt % CT;
+      float d = fmax3f(fmaxf(p[0], p[CT]), p[2 * CT], p[3 * CT]);   // relative to the running max
       if (row_set || d == -INFINITY) d = fmaxf(d, 0.f);     // a row's first max may be any
       else row_set = true;
       gam()[tt] = d;
-      mrow()[tt] += d;
+      mrow()[tt] -= d;
       const bool miss = __any_sync(0xffffffffu, !row_set);
-      if (lane == 0) csmax()[8 + warp] = miss ? 1.f : 0.f;
+      if (lane == 0) small()[8 + warp] = miss ? 1.f : 0.f;
     }
     bar();
-    pending = csmax()[8] != 0.f || (R == 64 && csmax()[9] != 0.f);
+    pending = small()[8] != 0.f || (R == 64 && small()[9] != 0.f);
 #pragma unroll
     for (int i = 0; i < CT; i += 4) {
       const float4 d = *reinterpret_cast<const float4*>(gam() + CT * half + i);
-      const float dd[4] = {d.x, d.y, d.z, d.w};
+      // (a row's first max: nothing to scale yet)
+      lsum[i] *= ex2(fminf(-d.x, 0.f));
+      lsum[i + 1] *= ex2(fminf(-d.y, 0.f));
+      lsum[i + 2] *= ex2(fminf(-d.z, 0.f));
+      lsum[i + 3] *= ex2(fminf(-d.w, 0.f));
+    }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float corr = ex2(fminf(-dd[e], 0.f));         // (a row's first max: nothing to scale yet)
-        acc[i + e] *= corr;
-        lsum[i + e] *= corr;
-      }
+    for (int ch = 0; ch < CT / 16; ++ch) {
+      float v[16];
+      get_acc(ch, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] *= ex2(fminf(-gam()[CT * half + 16 * ch + i], 0.f));
+      put_acc(ch, v);
     }
   }
 
@@ -710,8 +839,10 @@ struct TreeTeam {
 #pragma unroll
       for (int e = 0; e < 4; ++e) split2p(pp[4 * c + e], hi[e], lo[e]);
       const int cc = CT / 8 * half + 2 * ch + c;
-      *reinterpret_cast<uint4*>(sm + S::kB0 + tree_po(cc, t)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(b_lo() + tree_po(cc + kLoRow / 8, t)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      uint8_t* b = sm + S::kB0;
+      *reinterpret_cast<uint4*>(b + tree_po(cc, t)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(R == 64 ? b + 16384 + tree_po(cc, t) : b + tree_po(cc + 4, t)) =
+          make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   }
 
@@ -719,8 +850,8 @@ struct TreeTeam {
   __device__ void join_rows() {
     bar();
     if (tt < R) {
-      const float* p = part() + 4 * (tt / CT) * 32 + tt % CT;
-      gam()[tt] = (p[0] + p[32]) + (p[64] + p[96]);
+      const float* p = part() + 4 * (tt / CT) * CT + tt % CT;
+      gam()[tt] = (p[0] + p[CT]) + (p[2 * CT] + p[3 * CT]);
     }
     bar();
   }
@@ -731,7 +862,7 @@ struct TreeTeam {
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = lsum[16 * ch + i];
       const float m = tree_reduce<false>(v, lane);
-      if (lane < 16) part()[warp * 32 + 16 * ch + lane] = m;
+      if (lane < 16) part()[warp * CT + 16 * ch + lane] = m;
     }
     join_rows();
   }
@@ -741,43 +872,53 @@ struct TreeTeam {
   __device__ bool unrotate() {
     sum_lsum();
     {
-      uint32_t hrow[32];
+      // row t of H: bit b of the column flips the sign where t has it; two columns a register
+      uint32_t h[32];
+      h[0] = 0x3C003C00u ^ ((t & 1) ? 0x80000000u : 0u) ^ ((half && (t & 64)) ? 0x80008000u : 0u);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int j = 64 * half + 2 * i;
-        hrow[i] = 0x3C003C00u ^ ((__popc(t & j) & 1) ? 0x8000u : 0u) ^ ((__popc(t & (j + 1)) & 1) ? 0x80000000u : 0u);
-      }
-      tc_st32(trow + kTrAV + 32 * half, hrow);
+      for (int b = 0; b < 5; ++b)
+#pragma unroll
+        for (int i = 0; i < (1 << b); ++i) h[i | (1 << b)] = h[i] ^ ((t >> (b + 1)) & 1 ? 0x80008000u : 0u);
+      tc_st32(trow + kTrAV + 32 * half, h);
     }
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < CT; ++i) {
-      const float l = gam()[CT * half + i];
-      acc[i] = l > 0.f ? acc[i] / l : 0.f;
-      top = fmaxf(top, fabsf(acc[i]));
+    for (int ch = 0; ch < CT / 16; ++ch) {
+      float v[16];
+      get_acc(ch, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float l = gam()[CT * half + 16 * ch + i];
+        v[i] = l > 0.f ? __fdividef(v[i], l) : 0.f;
+        top = fmaxf(top, fabsf(v[i]));
+      }
+      put_acc(ch, v);
     }
     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-    if (lane == 0) csmax()[warp] = top;
+    if (lane == 0) small()[warp] = top;
     bar();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, csmax()[i]);
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, small()[i]);
     const float2 sc = tc_pow2_scale(top, 13);
     const float2 sc2 = make_float2(sc.x, sc.x);
 #pragma unroll
     for (int ch = 0; ch < CT / 16; ++ch) {
+      float v[16];
+      get_acc(ch, v);
       float2 pp[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) pp[i] = __fmul2_rn(make_float2(acc[16 * ch + 2 * i], acc[16 * ch + 2 * i + 1]), sc2);
+      for (int i = 0; i < 8; ++i) pp[i] = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), sc2);
       store_p(ch, pp);
     }
-    product(true);
+    product_pv(false);
     wait_pv();
 #pragma unroll
     for (int ch = 0; ch < CT / 16; ++ch) {
       float v[16];
-      tree_read<R>(trow + kTrO, half, ch, v);
+      read16(ch, v);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[16 * ch + i] = v[i] * (gam()[CT * half + 16 * ch + i] * (kInvSqrt128 * sc.y));
+      for (int i = 0; i < 16; ++i) v[i] *= gam()[CT * half + 16 * ch + i] * (kInvSqrt128 * sc.y);
+      put_acc(ch, v);
     }
     tc_fence_before();
     return named_bar_and(bar_id, kTreeTeamThreads, ok);
@@ -787,8 +928,13 @@ struct TreeTeam {
     sum_lsum();
     float* out = a.part + rec_idx * tree_rec_floats(R);
 #pragma unroll
-    for (int i = 0; i < CT; ++i) out[(CT * half + i) * kD + t] = acc[i];
-    if (tt < R) *reinterpret_cast<float2*>(out + R * kD + 2 * tt) = make_float2(row_set ? mrow()[tt] : kNoMax, gam()[tt]);
+    for (int ch = 0; ch < CT / 16; ++ch) {
+      float v[16];
+      get_acc(ch, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) out[(CT * half + 16 * ch + i) * kD + t] = v[i];
+    }
+    if (tt < R) *reinterpret_cast<float2*>(out + R * kD + 2 * tt) = make_float2(row_set ? -mrow()[tt] : kNoMax, gam()[tt]);
     bar();
   }
 
@@ -813,7 +959,7 @@ struct TreeTeam {
       } else {
         valid_of()[stg] = 1;
         mbar_arrive_expect_tx(rec_bar, L::kBytes);
-        bulk_g2s(sm + S::kRec + stg * kRecPitch, a.cache + (blk * a.hkv + c.h) * static_cast<int64_t>(L::kBytes), L::kBytes,
+        bulk_g2s(sm + S::kRec + stg * S::kRecPitch, a.cache + (blk * a.hkv + c.h) * static_cast<int64_t>(L::kBytes), L::kBytes,
                  rec_bar);
       }
       ++c.ti;
@@ -827,40 +973,52 @@ struct TreeTeam {
   // One item: packed tile `ti` in stage used % kTreeStages, or the fresh tile at f0. False
   // after a wait that timed out.
   __device__ bool item(bool fresh, int ti, int f0, uint32_t used, uint32_t& issued) {
-    bool valid = true;
-    float cs = 1.f, cz = 0.f, rv = 1.f;
+    bool valid = true, wide = false;
+    float cs = 1.f, cw = 0.f, rv = 1.f, cmax = 1.f;
     Keys key{0.f, 0, -1, true, fresh};
     if (!fresh) {
       const uint32_t stg = used % kTreeStages;
-      const uint8_t* rec = sm + S::kRec + stg * kRecPitch;
+      const uint8_t* rec = sm + S::kRec + stg * S::kRecPitch;
       const uint16_t* km = reinterpret_cast<const uint16_t*>(rec + L::kKMetaOff);
       const uint16_t* vm = reinterpret_cast<const uint16_t*>(rec + L::kVMetaOff);
       ok = mbar_wait(&bars()[kTbRec + stg], (used / kTreeStages) & 1u, a.flags) && ok;
       valid = valid_of()[stg] != 0;
       const bool go = __all_sync(0xffffffffu, ok) && valid;
-      float kinv = 1.f;
+      const int tok = tree_token(t);
       if (go) {
-        tree_keys<KB>(rec + L::kKCodeOff, t, half, trow + kTrAK + 32 * half);
-        kinv = fold(rec);
-      }
-      product(false);
-      if (go) {
-        tree_values<VB>(rec + L::kVCodeOff, t, half, trow + kTrAV + 32 * half);
+        tree_keys<KB>(rec + L::kKCodeOff, tok, half, trow + kTrAK + 32 * half);
+        const float kinv = fold(rec);
         // S is in units of code / kKF, q 2^e, r s 2^k, and q_r lacks its 1 / sqrt(128)
-        key.f = h2f_bits(km[L::kKc + t]) * (a.scale * kInvSqrt128 * kKF * kinv * qinv);
-        const float cv = kLean ? 1.f : h2f_bits(vm[L::kVc + t]);
-        cs = cv * h2f_bits(vm[L::kVs + t]);
-        cz = cv * h2f_bits(vm[L::kVz + t]);
+        key.f = h2f_bits(km[L::kKc + tok]) * (a.scale * kInvSqrt128 * kKF * kinv * qinv);
+        const float cv = kLean ? 1.f : h2f_bits(vm[L::kVc + tok]);
+        const float sv = h2f_bits(vm[L::kVs + tok]);
+        const float w = fmaf(kMid, sv, h2f_bits(vm[L::kVz + tok]));   // z from the middle of the code range
+        const bool near = fabsf(w) <= kWide * sv;
+        const float u = __fdividef(w, sv), uh = near ? rintf(u * (1.f / kUStep)) * kUStep : 0.f;
+        cs = cv * sv;
+        cw = near ? 0.f : cv * w;
         rv = h2f_bits(vm[L::kVr + t]);
+        if (half == 0) {
+          const __half2 u2 = __float2half2_rn(near ? (u - uh) * (1.f / kVF) : 0.f);
+          const uint32_t uu = *reinterpret_cast<const uint32_t*>(&u2);
+          reinterpret_cast<uint4*>(sm + S::kU)[t] = make_uint4(uu, uu, uu, uu);
+          reinterpret_cast<__half*>(sm + S::kAdd)[t] = __float2half_rn((uh - kMid) * (1.f / kVF));
+          // the warp's largest c s; negative where a token's zero is far off
+          const float cm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(cs)));
+          const bool far = __any_sync(0xffffffffu, !near);
+          if (lane == 0) small()[warp] = far ? -cm : cm;
+        }
       }
-      const float cm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(cs)));
-      if (lane == 0) csmax()[warp] = cm;
-      key.pk = (cur().first + ti) * kB + t;
+      key.pk = (cur().first + ti) * kB + tok;
+      product_qk(false);
+      if (go) tree_values<VB>(rec + L::kVCodeOff, t, half, reinterpret_cast<const uint16_t*>(sm + S::kAdd), trow + kTrAV + 32 * half);
+      const float4 c4 = *reinterpret_cast<const float4*>(small());
+      cmax = fmaxf(fmaxf(fabsf(c4.x), fabsf(c4.y)), fmaxf(fabsf(c4.z), fabsf(c4.w)));
+      wide = valid && fminf(fminf(c4.x, c4.y), fminf(c4.z, c4.w)) < 0.f;
     } else {
       fresh_keys(f0);
-      product(false);
+      product_qk(true);
       fresh_values(f0);
-      if (lane == 0) csmax()[warp] = 1.f;
       const TreeCursor& c = cur();
       const int ft = f0 + t;
       key.f = a.scale;
@@ -869,76 +1027,78 @@ struct TreeTeam {
       key.pk = max(a.seq_lens[c.s], 0) / kB * kB + ft;
       if (kMod && key.chunk_i >= 0 && a.positions != nullptr) key.pk = a.positions[a.cu[c.s] + key.chunk_i];
     }
-    tc_operands_written();
-    ok = named_bar_and(bar_id, kTreeTeamThreads, ok);   // beta visible, the record read; every wait succeeded
-    if (!ok) return false;
-    if (tt == 0 && !fresh) issued = refill(issued, used + 1 + kTreeStages);
 
     wait_qk();
-    float x[16];
+    float x[CT];
     float top = -INFINITY;
 #pragma unroll
     for (int ch = 0; ch < CT / 16; ++ch) {
-      scores(ch, key, x);
+      scores(ch, key, *reinterpret_cast<float(*)[16]>(&x[16 * ch]));
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) top = fmax3f(top, x[i], x[i + 1]);
+      for (int i = 0; i < 16; i += 2) top = fmax3f(top, x[16 * ch + i], x[16 * ch + i + 1]);
     }
-    const float4 c4 = *reinterpret_cast<const float4*>(csmax());
     // p' <= 2^kTau max(c s) 2^e < 2^14
-    const float2 psc = tc_pow2_scale(fmaxf(fmaxf(c4.x, c4.y), fmaxf(c4.z, c4.w)), 13 - static_cast<int>(kTau));
-    bool again = CT > 16;                  // the scores are not (all) at hand
+    const float2 psc = tc_pow2_scale(cmax, 13 - static_cast<int>(kTau));
     if (tc_bar_or(bar_id, kTreeTeamThreads, (valid && top > kTau) || pending || !ok)) {
       ok = named_bar_and(bar_id, kTreeTeamThreads, ok);
       if (!ok) return false;
       rescale(key, valid);
-      again = true;
+#pragma unroll
+      for (int ch = 0; ch < CT / 16; ++ch) scores(ch, key, *reinterpret_cast<float(*)[16]>(&x[16 * ch]));
     }
     if (valid) {
       const float csq = cs * psc.x;
-      const float2 cs2 = make_float2(csq, csq), cz2 = make_float2(cz, cz);
+      const float2 cs2 = make_float2(csq, csq);
 #pragma unroll
       for (int ch = 0; ch < CT / 16; ++ch) {
-        if (again) scores(ch, key, x);
         float2 pp[8];
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-          const float2 p = make_float2(ex2(x[i]), ex2(x[i + 1]));
-          const float2 l = __fadd2_rn(make_float2(lsum[16 * ch + i], lsum[16 * ch + i + 1]), p);
-          lsum[16 * ch + i] = l.x;
-          lsum[16 * ch + i + 1] = l.y;
+          const int j = 16 * ch + i;
+          const float2 p = make_float2(ex2(x[j]), ex2(x[j + 1]));
+          const float2 l = __fadd2_rn(make_float2(lsum[j], lsum[j + 1]), p);
+          lsum[j] = l.x;
+          lsum[j + 1] = l.y;
           pp[i / 2] = __fmul2_rn(p, cs2);
-          const float2 z = __fmul2_rn(p, cz2);
-          x[i] = z.x;
-          x[i + 1] = z.y;
         }
         store_p(ch, pp);
-        if (!fresh) {                      // gamma, first half
-          const float m = tree_reduce<false>(x, lane);
-          if (lane < 16) part()[warp * 32 + 16 * ch + lane] = m;
-        }
       }
     }
-    product(true);
-    if (valid && !fresh) join_rows();      // gamma
-    wait_pv();
-    if (valid) {
-      const float of = (fresh ? 1.f : kVF) * psc.y;
-      const float2 of2 = make_float2(of, of), rv2 = make_float2(rv, rv);
+    if (wide) {                            // the far tokens' part of gamma, summed over the lanes
 #pragma unroll
       for (int ch = 0; ch < CT / 16; ++ch) {
-        float o[16];
-        tree_read<R>(trow + kTrO, half, ch, o);
+        float g[16];
+        scores(ch, key, g);
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (!fresh) w = *reinterpret_cast<const float4*>(gam() + CT * half + 16 * ch + i);
-          const int j = 16 * ch + i;
-          const float2 y = __ffma2_rn(rv2, __ffma2_rn(make_float2(o[i], o[i + 1]), of2, make_float2(w.x, w.y)),
-                                      make_float2(acc[j], acc[j + 1]));
-          const float2 z = __ffma2_rn(rv2, __ffma2_rn(make_float2(o[i + 2], o[i + 3]), of2, make_float2(w.z, w.w)),
-                                      make_float2(acc[j + 2], acc[j + 3]));
-          acc[j] = y.x; acc[j + 1] = y.y; acc[j + 2] = z.x; acc[j + 3] = z.y;
+        for (int i = 0; i < 16; ++i) g[i] = cw != 0.f ? ex2(g[i]) * cw : 0.f;
+        const float m = tree_reduce<false>(g, lane);
+        if (lane < 16) part()[warp * CT + 16 * ch + lane] = m;
+      }
+    }
+    product_pv(!fresh);
+    // while PV runs; the record was read before the barriers above
+    if (tt == 0 && !fresh) issued = refill(issued, used + 1 + kTreeStages);
+    if (wide) join_rows();
+    wait_pv();
+    if (valid) {
+      const float of = rv * ((fresh ? 1.f : kVF) * psc.y);
+      const float2 of2 = make_float2(of, of);
+#pragma unroll
+      for (int ch = 0; ch < CT / 16; ++ch) {
+        float o[16], y[16];
+        read16(ch, o);
+        get_acc(ch, y);
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const float2 v = __ffma2_rn(of2, make_float2(o[i], o[i + 1]), make_float2(y[i], y[i + 1]));
+          y[i] = v.x;
+          y[i + 1] = v.y;
         }
+        if (wide) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) y[i] = fmaf(rv, gam()[CT * half + 16 * ch + i], y[i]);
+        }
+        put_acc(ch, y);
       }
     }
     tc_fence_before();
@@ -984,23 +1144,25 @@ struct TreeTeam {
 
   // Every product complete before TMEM is released.
   __device__ void finish() {
-    if (tt == kTreeIssuer) {
-      umma_commit(&bars()[kTbFin]);
-      mbar_wait(&bars()[kTbFin], 0, a.flags);
+    if (warp == kTreeIssuer) {
+      if (tree_elect()) {
+        umma_commit(&bars()[kTbFin]);
+        mbar_wait(&bars()[kTbFin], 0, a.flags);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   }
 };
 
 template <int KB, int VB, bool kLean, int R, bool kMod>
-__global__ void __launch_bounds__(kTreeThreads, 1) tree_split_kernel(const __grid_constant__ TreeArgs a) {
+__global__ void __launch_bounds__(tree_teams(R) * kTreeTeamThreads, 1) tree_split_kernel(const __grid_constant__ TreeArgs a) {
   using S = TreeSm<KB, VB, kLean, R>;
   extern __shared__ __align__(1024) uint8_t smem[];
   tree_dep_launch();
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + S::kSlot);
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
   if (threadIdx.x == 0) {
-    for (int j = 0; j < kTreeTeams; ++j) {
+    for (int j = 0; j < S::kTeams; ++j) {
       uint64_t* bars = reinterpret_cast<uint64_t*>(smem + j * S::kTeam + S::kX + S::kBars);
       for (int i = 0; i <= kTbFin; ++i) mbar_init(&bars[i], 1);
     }
@@ -1010,12 +1172,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_split_kernel(const __gri
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
   tree_dep_wait();                               // the scan's prefix
   const int j = warp >> 3;
-  const int64_t team = static_cast<int64_t>(blockIdx.x) * kTreeTeams + j;
+  const int64_t team = static_cast<int64_t>(blockIdx.x) * S::kTeams + j;
   const int64_t total = a.prefix[a.n_seqs];
-  TreeTeam<KB, VB, kLean, R, kMod> tm(a, smem + j * S::kTeam, tmem + j * kTrCols, j);
+  TreeTeam<KB, VB, kLean, R, kMod> tm(a, smem + j * S::kTeam, tmem + j * tree_cols(R), j);
+  tm.init();                                     // (made visible with the first operands)
   tm.run(team * total / a.n_teams, (team + 1) * total / a.n_teams, team);
   tm.finish();
   tc_fence_before();
@@ -1088,7 +1251,7 @@ cudaError_t launch_tree_cfg(const TreeArgs& a, cudaStream_t stream) {
   cudaError_t err = set_smem_once(tree_split_kernel<KB, VB, kLean, R, kMod>, S::kBytes, smem_set);
   if (err == cudaSuccess) err = tree_launch(tree_scan_kernel<R>, dim3(1), 1024, 0, false, stream, a);
   if (err == cudaSuccess)
-    err = tree_launch(tree_split_kernel<KB, VB, kLean, R, kMod>, dim3(a.n_teams / kTreeTeams), kTreeThreads, S::kBytes,
+    err = tree_launch(tree_split_kernel<KB, VB, kLean, R, kMod>, dim3(a.n_teams / S::kTeams), S::kTeams * kTreeTeamThreads, S::kBytes,
                       true, stream, a);
   if (err == cudaSuccess) err = tree_launch(tree_merge_kernel<R>, dim3(a.max_tree, a.n_seqs), 256, 0, true, stream, a);
   return err;
@@ -1113,7 +1276,7 @@ size_t tree_head_bytes(int n_seqs) {   // prefix, first
 size_t tree_scratch_bytes(int n_seqs, int hkv, int group, int max_tree) {
   const int r = tree_rows(group, max_tree);
   const size_t units = static_cast<size_t>(n_seqs) * hkv * ((group * max_tree + r - 1) / r);
-  return tree_head_bytes(n_seqs) + (units + kTreeTeams * kTreeMaxCtas) * tree_rec_floats(r) * sizeof(float);
+  return tree_head_bytes(n_seqs) + (units + kTreeMaxTeams * kTreeMaxCtas) * tree_rec_floats(r) * sizeof(float);
 }
 
 cudaError_t launch_tree(const uint16_t* q, const uint16_t* k_new, const uint16_t* v_new, const uint64_t* tree_mask,
@@ -1144,7 +1307,7 @@ cudaError_t launch_tree(const uint16_t* q, const uint16_t* k_new, const uint16_t
   cudaError_t err = cudaGetDevice(&dev);
   if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (err != cudaSuccess) return err;
-  a.n_teams = kTreeTeams * std::max(1, std::min(sms, kTreeMaxCtas));
+  a.n_teams = tree_teams(rows) * std::max(1, std::min(sms, kTreeMaxCtas));
   const bool mod = score.softcap > 0.f || score.window > 0 || score.slopes != nullptr;
   if (k_bits == 4 && v_bits == 2)
     return lean ? launch_tree_preset<4, 2, true>(a, rows, mod, stream) : launch_tree_preset<4, 2, false>(a, rows, mod, stream);
