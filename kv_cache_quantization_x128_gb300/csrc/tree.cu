@@ -398,7 +398,7 @@ struct TreeTeam {
   // in as one more product, whose A has the same value in every channel's row. A token whose
   // zero is more than kWide steps off the middle of the code range (a constant group, whose step
   // has its least value) has u^ = -kMid and no rest there; its part is summed over the lanes.
-  static constexpr float kWide = VB == 4 ? 4.f : 1.f;
+  static constexpr float kWide = 1000.f;
   static constexpr float kUStep = VB == 4 ? 1.f / 128.f : 1.f / 256.f;
   const TreeArgs& a;
   uint8_t* sm;
@@ -510,11 +510,11 @@ struct TreeTeam {
   __device__ void init() {
     for (int i = tt; i < 16; i += kTreeTeamThreads)
       reinterpret_cast<uint4*>(sm + S::kOne)[i] =
-          i < 2 ? make_uint4(0x54005400u, 0x54005400u, 0x54005400u, 0x54005400u) : make_uint4(0, 0, 0, 0);
+          i < 2 ? make_uint4(0x60006000u, 0x60006000u, 0x60006000u, 0x60006000u) : make_uint4(0, 0, 0, 0);
     for (int i = tt; i < 128; i += kTreeTeamThreads) reinterpret_cast<uint4*>(sm + S::kExt)[i] = make_uint4(0, 0, 0, 0);
   }
 
-  static __device__ int q_slot(int g) { return 16 * ((g >> 1) & 1) + 2 * (g >> 2) + (g & 1); }
+  static __device__ int q_slot(int g) { return 16 * ((g >> 1) & 1) + (g >> 2) + 8 * (g & 1); }
 
   // Rows of the unit at the cursor: row tables, q_r scaled by a power of two in shared memory.
   __device__ void enter() {
@@ -609,7 +609,7 @@ struct TreeTeam {
   // row's 16 takes channels ch .. ch + 3 and ch + 8 .. ch + 11, ch = 16 (j >> 1) + 4 (j & 1).
   __device__ float fold(const uint8_t* rec) {
     const uint16_t* km = reinterpret_cast<const uint16_t*>(rec + L::kKMetaOff);
-    const int jj = tt & 15, r0 = tt >> 4, ch = 16 * (jj >> 1) + 4 * (jj & 1);
+    const int jj = tt & 15, r0 = tt >> 4, ch = 16 * (jj & 7) + 4 * (jj >> 3);
     float2 rs[4], rz[4];
     float m = 0.f;
 #pragma unroll
@@ -624,12 +624,14 @@ struct TreeTeam {
       rz[2 * e + 1] = mul_h2(rv.y, zv.y);
       m = fmax3f(m, rs[2 * e].x, rs[2 * e].y);
       m = fmax3f(m, rs[2 * e + 1].x, rs[2 * e + 1].y);
+      m = fmax3f(m, fabsf(rz[2 * e].x) * (1.f / 64.f), fabsf(rz[2 * e].y) * (1.f / 64.f));
+      m = fmax3f(m, fabsf(rz[2 * e + 1].x) * (1.f / 64.f), fabsf(rz[2 * e + 1].y) * (1.f / 64.f));
     }
     // the scales are positive: their maximum over the tile's channels as integers
     m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
     const float2 sc = tc_pow2_scale(m, 0);          // the largest r s into [1, 2)
     const float2 sc2 = make_float2(sc.x, sc.x);
-    const float zf = sc.x / (kKF * 64.f);           // beta in the units of S, over its operand's 64
+    const float zf = sc.x * (1.f / (kKF * 512.f));           // beta in the units of S, over its operand's 64
     const float2 zf2 = make_float2(zf, zf);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -652,7 +654,7 @@ struct TreeTeam {
         b2 = __ffma2_rn(x[e], rz[e], b2);
       }
       b[k] = b2.x + b2.y;
-      const int kk = 64 * (jj & 1) + 8 * (jj >> 1);
+      const int kk = 64 * (jj >> 3) + 8 * (jj & 7);
       *reinterpret_cast<uint4*>(sm + S::kB0 + tree_qo(r, kk)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       *reinterpret_cast<uint4*>(sm + S::kB0 + tree_qo_lo(r, kk)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
@@ -993,16 +995,15 @@ struct TreeTeam {
         const float cv = kLean ? 1.f : h2f_bits(vm[L::kVc + tok]);
         const float sv = h2f_bits(vm[L::kVs + tok]);
         const float w = fmaf(kMid, sv, h2f_bits(vm[L::kVz + tok]));   // z from the middle of the code range
-        const bool near = fabsf(w) <= kWide * sv;
-        const float u = __fdividef(w, sv), uh = near ? rintf(u * (1.f / kUStep)) * kUStep : 0.f;
+        const float zv = h2f_bits(vm[L::kVz + tok]); const float u0 = __fdividef(zv, sv); const bool near = fabsf(u0) <= kWide; const float u = near ? u0 : 0.f; const int e_ = __float_as_int(fabsf(u) + 16.f) & 0x7f800000; const float step = __int_as_float(e_ - (10 << 23)), inv = __int_as_float((264 << 23) - e_); const float uh = rintf(u * inv) * step;
         cs = cv * sv;
-        cw = near ? 0.f : cv * w;
+        cw = near ? 0.f : cv * zv;
         rv = h2f_bits(vm[L::kVr + t]);
         if (half == 0) {
           const __half2 u2 = __float2half2_rn(near ? (u - uh) * (1.f / kVF) : 0.f);
           const uint32_t uu = *reinterpret_cast<const uint32_t*>(&u2);
           reinterpret_cast<uint4*>(sm + S::kU)[t] = make_uint4(uu, uu, uu, uu);
-          reinterpret_cast<__half*>(sm + S::kAdd)[t] = __float2half_rn((uh - kMid) * (1.f / kVF));
+          reinterpret_cast<__half*>(sm + S::kAdd)[t] = __float2half_rn(uh * (1.f / kVF));
           // the warp's largest c s; negative where a token's zero is far off
           const float cm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(cs)));
           const bool far = __any_sync(0xffffffffu, !near);

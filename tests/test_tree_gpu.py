@@ -104,6 +104,28 @@ def test_large_scores(env):
     check(env, make([500, 300], [6, 3], 8, 1, seed=76, q_scale=0.01))
 
 
+@pytest.mark.parametrize("preset", ["k4v2", "k4v4", "k2v2", "k4v2l"])
+def test_constant_and_biased_groups(env, preset):
+    """Tiles whose groups are constant (keys equal over the tokens, values that rotate to a constant;
+    their steps have the least value) or far from zero."""
+    from oracle import kvarn_oracle as o
+    rng = np.random.default_rng(92)
+    p = make([900, 700], [5, 9], 8, 1, preset, seed=92)
+    k, v = synth.prefill_kv(6 * 128, 1, seed=93)
+    k, v = (x.reshape(6, 128, 128).copy() for x in (k, v))
+    k[0] = k[0, :1]                                          # every token's key the same
+    k[1] += np.float16(8) * rng.standard_normal(128).astype(np.float16)      # keys with a large mean
+    v[2, ::3] = 0
+    v[2, ::3, 0] = np.float16(1.5)                           # rotates to a constant
+    v[3] = 0
+    v[4, 5:90] += np.float16(6)                              # values with a large mean
+    k[5], v[5] = np.float16(0.25), np.float16(0)
+    p["cache"], _, _ = o.quantize_tiles(k[:, None], v[:, None], preset=preset)
+    for bt in (p["bt"], np.where(p["bt"] >= 0, (p["bt"] + 1) % 6, p["bt"]).astype(np.int32)):
+        p["bt"] = bt
+        check(env, p)
+
+
 def test_rows_that_attend_little(env):
     rng = np.random.default_rng(77)
     lens, counts = [0, 0, 140], [6, 64, 5]
