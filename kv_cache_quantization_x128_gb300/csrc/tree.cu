@@ -1189,44 +1189,64 @@ __global__ void __launch_bounds__(tree_teams(R) * kTreeTeamThreads, 1) tree_spli
 }
 
 // ------------------------------------------------------------------ merge
-// Block (token p, sequence s): warp w joins the records of q-heads w, w + 8, ...; lane l
-// holds channels 4l .. 4l + 3.
+// A warp per output row (token p, q-head m) of sequence blockIdx.y: joins the records of the teams
+// that had items of the row's unit, 32 at a time (their maxima and sums one a lane, then the
+// rows, lane l channels 4l .. 4l + 3, their loads independent of each other).
 template <int R>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
-  tree_dep_wait();
-  const int p = blockIdx.x, s = blockIdx.y, lane = threadIdx.x & 31;
+  const int s = blockIdx.y, lane = threadIdx.x & 31, hq = a.hkv * a.group;
+  const int id = blockIdx.x * 8 + (threadIdx.x >> 5), p = id / hq, m = id - p * hq;
   const TreeSeq q = tree_seq<R>(a, s, false);
+  tree_dep_wait();
   if (p >= q.nt) return;
-  const int hq = a.hkv * a.group;
-  const int64_t total = a.prefix[a.n_seqs];
+  const int64_t total = a.prefix[a.n_seqs], n = a.n_teams;
   const int64_t items = q.full - a.first[s] + q.fresh;
-  for (int m = threadIdx.x >> 5; m < hq; m += 8) {
-    const int h = m / a.group, row = p * a.group + m % a.group, u = row / R, r = row % R;
-    const int64_t g0 = a.prefix[s] + (static_cast<int64_t>(h) * q.units + u) * items, g1 = g0 + items - 1;
-    const int64_t unit = (static_cast<int64_t>(s) * a.hkv + h) * a.max_units + u;
-    float top = kNoMax, sum = 0.f;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t g = g0; g <= g1;) {
-      // team k owns items [k total / n, (k + 1) total / n): the one that has item g, then the one behind its last
-      const int64_t k = ((g + 1) * a.n_teams - 1) / total;
-      g = (k + 1) * total / a.n_teams;
-      const float* rec = a.part + (k + unit) * tree_rec_floats(R);
-      const float2 ml = *reinterpret_cast<const float2*>(rec + R * kD + 2 * r);
-      const float4 v = *reinterpret_cast<const float4*>(rec + r * kD + 4 * lane);
-      const float mn = fmaxf(top, ml.x);
-      const float c0 = ex2(top - mn), c1 = ex2(ml.x - mn);
-      top = mn;
-      sum = sum * c0 + ml.y * c1;
-      y.x = y.x * c0 + v.x * c1;
-      y.y = y.y * c0 + v.y * c1;
-      y.z = y.z * c0 + v.z * c1;
-      y.w = y.w * c0 + v.w * c1;
+  const int h = m / a.group, row = p * a.group + (m - h * a.group), u = row / R, r = row - u * R;
+  const int64_t g0 = a.prefix[s] + (static_cast<int64_t>(h) * q.units + u) * items;
+  const int64_t unit = (static_cast<int64_t>(s) * a.hkv + h) * a.max_units + u;
+  // team k owns items [k total / n, (k + 1) total / n): item g belongs to ((g + 1) n - 1) / total. Where
+  // there are fewer items than teams every item has a team of its own.
+  const bool sparse = total < n;
+  const int64_t k0 = ((g0 + 1) * n - 1) / total;
+  const int count = static_cast<int>(sparse ? items : ((g0 + items) * n - 1) / total - k0 + 1);
+  float top = kNoMax, sum = 0.f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < count; i0 += 32) {
+    const int left = min(count - i0, 32);
+    int64_t rec = 0;
+    float2 ml = make_float2(kNoMax, 0.f);
+    if (lane < left) {
+      const int64_t k = sparse ? ((g0 + i0 + lane + 1) * n - 1) / total : k0 + i0 + lane;
+      rec = (k + unit) * tree_rec_floats(R);
+      ml = *reinterpret_cast<const float2*>(a.part + rec + R * kD + 2 * r);
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const __half2 o0 = __floats2half2_rn(y.x * inv, y.y * inv), o1 = __floats2half2_rn(y.z * inv, y.w * inv);
-    *reinterpret_cast<uint2*>(a.out + ((static_cast<int64_t>(a.cu[s]) + p) * hq + m) * kD + 4 * lane) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&o0), *reinterpret_cast<const uint32_t*>(&o1));
+    float mx = ml.x;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float mn = fmaxf(top, mx), c0 = ex2(top - mn), w = ex2(ml.x - mn);
+    top = mn;
+    float l = ml.y * w;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    sum = sum * c0 + l;
+    y.x *= c0;
+    y.y *= c0;
+    y.z *= c0;
+    y.w *= c0;
+#pragma unroll 4
+    for (int j = 0; j < left; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const float4 v = *reinterpret_cast<const float4*>(a.part + __shfl_sync(0xffffffffu, rec, j) + r * kD + 4 * lane);
+      y.x = fmaf(v.x, wj, y.x);
+      y.y = fmaf(v.y, wj, y.y);
+      y.z = fmaf(v.z, wj, y.z);
+      y.w = fmaf(v.w, wj, y.w);
+    }
   }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const __half2 o0 = __floats2half2_rn(y.x * inv, y.y * inv), o1 = __floats2half2_rn(y.z * inv, y.w * inv);
+  *reinterpret_cast<uint2*>(a.out + ((static_cast<int64_t>(a.cu[s]) + p) * hq + m) * kD + 4 * lane) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&o0), *reinterpret_cast<const uint32_t*>(&o1));
 }
 
 template <typename... KArgs, typename... Args>
@@ -1254,7 +1274,8 @@ cudaError_t launch_tree_cfg(const TreeArgs& a, cudaStream_t stream) {
   if (err == cudaSuccess)
     err = tree_launch(tree_split_kernel<KB, VB, kLean, R, kMod>, dim3(a.n_teams / S::kTeams), S::kTeams * kTreeTeamThreads, S::kBytes,
                       true, stream, a);
-  if (err == cudaSuccess) err = tree_launch(tree_merge_kernel<R>, dim3(a.max_tree, a.n_seqs), 256, 0, true, stream, a);
+  if (err == cudaSuccess) err = tree_launch(tree_merge_kernel<R>, dim3((a.max_tree * a.hkv * a.group + 7) / 8, a.n_seqs), 256, 0,
+                      true, stream, a);
   return err;
 }
 
