@@ -3,24 +3,25 @@
 // the orthonormal rotation keeps attention scores, the output is un-rotated).
 //
 // The rows of a (sequence, kv-head) are its drafted tokens times the group's q-heads
-// (row = token * group + head), cut into units of up to kR rows. A unit's items are its
-// packed tiles and then its fresh tiles (up to 128 tokens each: the workspace tokens
+// (row = token * group + head), cut into units of up to R = 32 or 64 rows. A unit's items are
+// its packed tiles and then its fresh tiles (up to 128 tokens each: the workspace tokens
 // followed by the drafted ones). The flattened items are cut into one contiguous range
 // per team (stream-K), so a few long sequences fill the GPU and ragged batches balance.
 //   tree_scan_kernel   prefix of items per sequence, first tile inside the window
-//   tree_split_kernel  one persistent CTA per SM, two teams of 8 warps; a team leaving a
-//                      unit writes a partial record
+//   tree_split_kernel  one persistent CTA per SM with two or three teams of 8 warps; a team
+//                      leaving a unit writes a partial record
 //   tree_merge_kernel  a warp per output row joins the records
 //
 // Per item and team, all products with M = 128 on the 5th-generation tensor core, tokens
-// (then channels) as TMEM lanes, A in TMEM, B in shared memory:
-//   keys    thread (lane = token, half = channels 64 half ..) turns codes into fp16 in TMEM;
-//           q' = q_r r^K s^K 2^e as fp16 hi + lo rows, beta = sum_i q_r,i r_i z_i
-//   QK^T    S[token][row] = codes . q'           (8 K steps, hi and lo)
-//           x = c^K_t (S + beta) in the log2 domain, cap, bias, masks
+// (then channels) as TMEM lanes and rows as columns, A in TMEM, B in shared memory:
+//   keys    thread (lane = token, half = channels 64 half ..) turns codes into fp16 in TMEM
+//   fold    q' = q_r r^K s^K 2^e as fp16 hi + lo rows, beta = sum_i q_r,i r_i z_i
+//   QK^T    S[token][row] = codes . q' + 1 beta  (8 K steps, hi and lo, and one of beta)
+//           x = c^K_t S in the log2 domain, cap, bias, masks
 //   values  thread (lane = channel) turns codes into fp16 in TMEM (under QK^T)
-//   PV      O[channel][row] = codes . p',  p' = p c^V s^V 2^e as fp16 hi + lo
-//           acc += r^V_channel (O + gamma), gamma = sum_t p c^V z^V
+//   PV      O[channel][row] = (codes + u^) . p' + 1 (u - u^) . p',
+//           p' = p c^V s^V 2^e as fp16 hi + lo, u = z^V / s^V of the token
+//           acc += r^V_channel O
 // The hi + lo pairs carry q' and p' to ~22 bits: rounded once to fp16, scores of keys with
 // outlier channels are off by some 1e-3 and so are the outputs. The tensor core drops
 // subnormal fp16 operands, hence the powers of two.
@@ -28,6 +29,15 @@
 // kTau, so that most tiles need no reduction over tokens (lanes); p stays <= 2^kTau.
 // Before fresh tiles, or before a record is written, the accumulator of the packed part is
 // rotated back by one more product, with the +-1 Hadamard matrix as A.
+//
+// Measured (fp16 out, k4v2, 64 q-heads over 8 kv-heads): 64 sequences of 16384 tokens with 8
+// drafted 865 us, 1.1 TB/s of records and 318 TFLOP/s of 275 GFLOP (the pairs double what the
+// tensor core does). Bound by instruction issue: 138 M warp instructions a 256 (sequence,
+// kv-head) x 128 tiles at 2 a cycle and SM, the tensor pipe 31 % busy, DRAM 14 %. Left out in
+// turn, the fold is worth 22 % of the time, p's writing 5 %, the softmax 8 %, the conversions of
+// codes 3 and 2 %, the accumulation 3 %: no part is waited for, all are issued. Slower were one
+// warp of 17 that issues all products (registers capped at 96: 1603 us), the fold one tile ahead
+// (982), and the next keys' conversion under PV (922).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -68,6 +78,7 @@ struct TreeArgs {
   int64_t num_blocks, n_tokens;
   int n_seqs, max_tree, hkv, group, max_blocks, window;
   int n_teams, max_units;   // teams; units of a (sequence, kv-head) at most
+  int group_inv;            // ceil(2^16 / group)
   float scale, softcap;     // scale includes log2(e) where no cap is set
 };
 
@@ -166,11 +177,13 @@ struct TreeCursor {
   int packed, items;     // packed tiles, all items of the unit
   int units, nt, ws;     // units of a kv-head, drafted and workspace tokens
   int first;             // first packed tile
+  int64_t c0;            // first drafted token's row of q
 };
 template <int R>
 __device__ __forceinline__ void tree_enter(const TreeArgs& a, TreeCursor& c) {
   const TreeSeq q = tree_seq<R>(a, c.s, false);
   c.first = a.first[c.s];
+  c.c0 = a.cu[c.s];
   c.packed = q.full - c.first;
   c.items = c.packed + q.fresh;
   c.units = q.units;
@@ -285,6 +298,11 @@ __device__ __forceinline__ void tree_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tree_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tree_add16(uint32_t (&r)[16], const uint16_t* add) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -392,14 +410,12 @@ struct TreeTeam {
   using S = TreeSm<KB, VB, kLean, R>;
   static constexpr int CT = R / 2;               // rows (columns of the products) of a thread
   static constexpr float kKF = KB == 4 ? 8.f : 2.f, kVF = VB == 4 ? 8.f : 2.f;   // codes were converted to code / kKF
-  static constexpr float kMid = VB == 4 ? 7.5f : 1.5f;   // of the value codes
-  // gamma_row = sum_t p c z = sum_t p' u, u = z / s, is folded into PV: the value operand is
-  // code + u^, u^ the multiple of kUStep nearest to u (exact in fp16), and the rest u - u^ goes
-  // in as one more product, whose A has the same value in every channel's row. A token whose
-  // zero is more than kWide steps off the middle of the code range (a constant group, whose step
-  // has its least value) has u^ = -kMid and no rest there; its part is summed over the lanes.
+  // A token's value is s (code + u), u = z / s. Most of u goes into the operand: code + u^, u^ the
+  // multiple of a power of two nearest to u that fp16 holds exactly with every code (2^-6 below
+  // |u| = 16, twice that below 48, ..). The rest u - u^ goes in as one more product, whose A has the same value in every
+  // channel's row. A token whose zero is more than kWide steps from 0 (a constant group, whose
+  // step has its least value) has neither; its part p c z is summed over the lanes.
   static constexpr float kWide = 1000.f;
-  static constexpr float kUStep = VB == 4 ? 1.f / 128.f : 1.f / 256.f;
   const TreeArgs& a;
   uint8_t* sm;
   uint32_t tm, trow;                             // TMEM address of the team, of the thread's warp
@@ -433,6 +449,11 @@ struct TreeTeam {
   __device__ int64_t& ahead_n() const { return *reinterpret_cast<int64_t*>(sm + S::kX + S::kAheadN); }
   __device__ volatile uint32_t* valid_of() const { return reinterpret_cast<volatile uint32_t*>(sm + S::kX + S::kValid); }
   __device__ void bar() { named_bar(bar_id, kTreeTeamThreads); }
+  // Drafted token of a row (row / group, exact for the 512 rows there can be) and the row of q.
+  __device__ int token_of(int row) const { return (row * a.group_inv) >> 16; }
+  __device__ const uint16_t* q_row(int64_t c0, int h, int row, int p) const {
+    return a.q + ((c0 + p) * a.hkv * a.group + h * a.group + (row - p * a.group)) * kD;
+  }
   static __device__ uint32_t tree_qo_lo(int r, int k) { return R == 64 ? 16384 + tree_qo(r, k) : tree_qo(r + 32, k); }
 
   // The thread's operand writes are done; once everyone's are, the issuer starts the product.
@@ -506,7 +527,7 @@ struct TreeTeam {
     }
   }
 
-  // The constant operand of beta (64 at two K elements) and the zeros of its other one.
+  // The constant operand of beta (512 at two K elements) and the zeros of its other one.
   __device__ void init() {
     for (int i = tt; i < 16; i += kTreeTeamThreads)
       reinterpret_cast<uint4*>(sm + S::kOne)[i] =
@@ -519,10 +540,10 @@ struct TreeTeam {
   // Rows of the unit at the cursor: row tables, q_r scaled by a power of two in shared memory.
   __device__ void enter() {
     const TreeCursor& c = cur();
-    const int64_t c0 = a.cu[c.s];
-    const int hq = a.hkv * a.group, row0 = c.u * R, nt = c.nt, h = c.h;
+    const int64_t c0 = c.c0;
+    const int row0 = c.u * R, nt = c.nt, h = c.h;
     if (tt < R) {
-      const int row = row0 + tt, p = row / a.group;
+      const int row = row0 + tt, p = token_of(row);
       const bool live = p < nt;
       mrow()[tt] = 0.f;
       uint64_t w = 0;
@@ -530,28 +551,27 @@ struct TreeTeam {
       mask()[tt] = w;
       if (kMod) {
         pos()[tt] = live && a.positions != nullptr ? a.positions[c0 + p] : 0;
-        slope()[tt] = live && a.slopes != nullptr ? a.slopes[h * a.group + row % a.group] * kLog2e : 0.f;
+        slope()[tt] = live && a.slopes != nullptr ? a.slopes[h * a.group + (row - p * a.group)] * kLog2e : 0.f;
       }
     }
     const int jj = tt & 15, r0 = tt >> 4;
     float m = 0.f;
     float* qs = reinterpret_cast<float*>(sm + S::kQ);
-#pragma unroll
-    for (int k = 0; k < R / 16; ++k) {
-      const int r = r0 + 16 * k, row = row0 + r, p = row / a.group;
+    auto load = [&](int k) {
+      const int row = row0 + r0 + 16 * k, p = token_of(row);
+      return p < nt ? *reinterpret_cast<const uint4*>(q_row(c0, h, row, p) + 8 * jj) : make_uint4(0, 0, 0, 0);
+    };
+    uint4 next = load(0);
+#pragma unroll 1
+    for (int k = 0; k < R / 16; ++k) {             // (not unrolled: run once, its time is that of fetching the code)
       float x[8];
-      if (p < nt) {
-        const uint4 w = *reinterpret_cast<const uint4*>(a.q + ((c0 + p) * hq + h * a.group + row % a.group) * kD + 8 * jj);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+      const uint32_t ws[4] = {next.x, next.y, next.z, next.w};
+      if (k + 1 < R / 16) next = load(k + 1);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = h2pair(reinterpret_cast<const uint16_t*>(&ws[e]));
-          x[2 * e] = f.x;
-          x[2 * e + 1] = f.y;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = h2pair(reinterpret_cast<const uint16_t*>(&ws[e]));
+        x[2 * e] = f.x;
+        x[2 * e + 1] = f.y;
       }
 #pragma unroll
       for (int bit = 1; bit < 8; bit <<= 1)
@@ -564,17 +584,14 @@ struct TreeTeam {
           }
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) {
-        const bool up = (jj & o) != 0;
+        const float sg = (jj & o) != 0 ? -1.f : 1.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float other = __shfl_xor_sync(0xffffffffu, x[i], o);
-          x[i] = up ? (other - x[i]) : (x[i] + other);
-        }
+        for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], sg, __shfl_xor_sync(0xffffffffu, x[i], o));
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
       // channels 4 G .. at 16-byte slot 16 e + j of the row (fold's thread j reads slots j, 16 + j)
-      float4* dst = reinterpret_cast<float4*>(qs + r * kD);
+      float4* dst = reinterpret_cast<float4*>(qs + (r0 + 16 * k) * kD);
       dst[q_slot(2 * jj)] = make_float4(x[0], x[1], x[2], x[3]);
       dst[q_slot(2 * jj + 1)] = make_float4(x[4], x[5], x[6], x[7]);
     }
@@ -631,7 +648,7 @@ struct TreeTeam {
     m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
     const float2 sc = tc_pow2_scale(m, 0);          // the largest r s into [1, 2)
     const float2 sc2 = make_float2(sc.x, sc.x);
-    const float zf = sc.x * (1.f / (kKF * 512.f));           // beta in the units of S, over its operand's 64
+    const float zf = sc.x * (1.f / (kKF * 512.f));           // beta in the units of S, over its operand's 512
     const float2 zf2 = make_float2(zf, zf);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -686,52 +703,59 @@ struct TreeTeam {
   __device__ const uint16_t* fresh_row(int f, bool value) const {
     const TreeCursor& c = cur();
     if (f < c.ws) return a.ws + ((static_cast<int64_t>(c.s) * a.hkv + c.h) * 2 + (value ? 1 : 0)) * (kB * kD) + f * kD;
-    return (value ? a.v_new : a.k_new) + (static_cast<int64_t>(a.cu[c.s] + (f - c.ws)) * a.hkv + c.h) * kD;
+    return (value ? a.v_new : a.k_new) + ((c.c0 + (f - c.ws)) * a.hkv + c.h) * kD;
   }
   __device__ void fresh_keys(int f0) {
     const TreeCursor& c = cur();
-    const int f = f0 + t;
-    uint32_t r[32];
-    if (f < c.ws + c.nt) {
-      const uint4* src = reinterpret_cast<const uint4*>(fresh_row(f, false) + 64 * half);
+    const int f = f0 + t, n = c.ws + c.nt, jj = tt & 15, r0 = tt >> 4;
+    const int64_t c0 = c.c0;
+    uint4 w[R / 16];
+    const uint4* src = reinterpret_cast<const uint4*>(fresh_row(min(f, n - 1), false) + 64 * half);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 v = src[i];
-        r[4 * i] = v.x; r[4 * i + 1] = v.y; r[4 * i + 2] = v.z; r[4 * i + 3] = v.w;
+    for (int i = 0; i < R / 16; ++i) {
+      const int row = c.u * R + r0 + 16 * i, p = token_of(row);
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (p < c.nt) w[i] = *reinterpret_cast<const uint4*>(q_row(c0, c.h, row, p) + 8 * jj);
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      uint4 k[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) k[i] = src[4 * p + i];
+      uint32_t r[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        r[4 * i] = f < n ? k[i].x : 0;
+        r[4 * i + 1] = f < n ? k[i].y : 0;
+        r[4 * i + 2] = f < n ? k[i].z : 0;
+        r[4 * i + 3] = f < n ? k[i].w : 0;
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) r[i] = 0;
+      tree_st16(trow + kTrAK + 32 * half + 16 * p, r);
     }
-    tc_st32(trow + kTrAK + 32 * half, r);
-    const int64_t c0 = a.cu[c.s];
-    const int hq = a.hkv * a.group, jj = tt & 15, r0 = tt >> 4;
 #pragma unroll
-    for (int k = 0; k < R / 16; ++k) {
-      const int rr = r0 + 16 * k, row = c.u * R + rr, p = row / a.group;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (p < c.nt)
-        w = *reinterpret_cast<const uint4*>(a.q + ((c0 + p) * hq + c.h * a.group + row % a.group) * kD + 8 * jj);
-      *reinterpret_cast<uint4*>(sm + S::kB0 + tree_qo(rr, 8 * jj)) = w;
-    }
+    for (int i = 0; i < R / 16; ++i) *reinterpret_cast<uint4*>(sm + S::kB0 + tree_qo(r0 + 16 * i, 8 * jj)) = w[i];
   }
   __device__ void fresh_values(int f0) {
     const TreeCursor& c = cur();
     const int nw = c.ws - f0, n = nw + c.nt;               // workspace tokens, all tokens from f0 on
     const uint16_t* w = a.ws + ((static_cast<int64_t>(c.s) * a.hkv + c.h) * 2 + 1) * (kB * kD) + f0 * kD + t;
     const int64_t step = static_cast<int64_t>(a.hkv) * kD;
-    const uint16_t* v = a.v_new + (static_cast<int64_t>(a.cu[c.s]) * a.hkv + c.h) * kD + t - nw * step;
+    const uint16_t* v = a.v_new + (c.c0 * a.hkv + c.h) * kD + t - nw * step;
+#pragma unroll 1
+    for (int part = 0; part < 4; ++part) {
+      uint16_t x[16];
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      uint32_t r[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int f = 64 * half + 32 * part + 2 * i;
-        const uint32_t x = f < nw ? w[f * kD] : f < n ? v[f * step] : 0;
-        const uint32_t y = f + 1 < nw ? w[(f + 1) * kD] : f + 1 < n ? v[(f + 1) * step] : 0;
-        r[i] = x | (y << 16);
+      for (int i = 0; i < 16; ++i) {                       // every load at a row that is there, none waits for another
+        const int f = min(64 * half + 16 * part + i, n - 1);
+        x[i] = *(f < nw ? w + f * kD : v + f * step);
       }
-      tree_st16(trow + kTrAV + 32 * half + 16 * part, r);
+      uint32_t r[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int f = 64 * half + 16 * part + 2 * i;
+        r[i] = (f < n ? x[2 * i] : 0u) | ((f + 1 < n ? x[2 * i + 1] : 0u) << 16);
+      }
+      tree_st8(trow + kTrAV + 32 * half + 8 * part, r);
     }
   }
 
@@ -750,8 +774,8 @@ struct TreeTeam {
   struct Keys {        // what the thread's token (lane) is in the current item
     float f;           // factor of S
     int pk;            // position
-    int chunk_i;       // index among the drafted tokens, or -1
-    bool key, fresh;
+    uint32_t seen;     // fresh tiles: bit i, whether the thread's i-th row attends it
+    bool fresh;
   };
   // Scores of 16 rows relative to their running max: x = f S (then cap and bias) - max; masked
   // keys -inf.
@@ -786,7 +810,7 @@ struct TreeTeam {
       if (k.fresh) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (!(k.key && (k.chunk_i < 0 || ((mask()[col + e] >> k.chunk_i) & 1)))) x[i + e] = -INFINITY;
+          if (!((k.seen >> (16 * ch + i + e)) & 1u)) x[i + e] = -INFINITY;
       }
     }
   }
@@ -977,7 +1001,7 @@ struct TreeTeam {
   __device__ bool item(bool fresh, int ti, int f0, uint32_t used, uint32_t& issued) {
     bool valid = true, wide = false;
     float cs = 1.f, cw = 0.f, rv = 1.f, cmax = 1.f;
-    Keys key{0.f, 0, -1, true, fresh};
+    Keys key{0.f, 0, 0u, fresh};
     if (!fresh) {
       const uint32_t stg = used % kTreeStages;
       const uint8_t* rec = sm + S::kRec + stg * S::kRecPitch;
@@ -994,8 +1018,14 @@ struct TreeTeam {
         key.f = h2f_bits(km[L::kKc + tok]) * (a.scale * kInvSqrt128 * kKF * kinv * qinv);
         const float cv = kLean ? 1.f : h2f_bits(vm[L::kVc + tok]);
         const float sv = h2f_bits(vm[L::kVs + tok]);
-        const float w = fmaf(kMid, sv, h2f_bits(vm[L::kVz + tok]));   // z from the middle of the code range
-        const float zv = h2f_bits(vm[L::kVz + tok]); const float u0 = __fdividef(zv, sv); const bool near = fabsf(u0) <= kWide; const float u = near ? u0 : 0.f; const int e_ = __float_as_int(fabsf(u) + 16.f) & 0x7f800000; const float step = __int_as_float(e_ - (10 << 23)), inv = __int_as_float((264 << 23) - e_); const float uh = rintf(u * inv) * step;
+        const float zv = h2f_bits(vm[L::kVz + tok]);
+        const float u0 = __fdividef(zv, sv);
+        const bool near = fabsf(u0) <= kWide;
+        const float u = near ? u0 : 0.f;
+        // 2^(e - 10) where 2^e <= |u| + 16 < 2^(e + 1): |code + u^| < 2^(e + 1) has 11 bits above it
+        const int e = __float_as_int(fabsf(u) + 16.f) & 0x7f800000;
+        const float step = __int_as_float(e - (10 << 23)), inv = __int_as_float((264 << 23) - e);
+        const float uh = rintf(u * inv) * step;
         cs = cv * sv;
         cw = near ? 0.f : cv * zv;
         rv = h2f_bits(vm[L::kVr + t]);
@@ -1022,11 +1052,16 @@ struct TreeTeam {
       fresh_values(f0);
       const TreeCursor& c = cur();
       const int ft = f0 + t;
+      const int ci = ft - c.ws;                  // index among the drafted tokens (negative: a workspace token)
       key.f = a.scale;
-      key.key = ft < c.ws + c.nt;
-      if (key.key) key.chunk_i = max(ft - c.ws, -1);
-      key.pk = max(a.seq_lens[c.s], 0) / kB * kB + ft;
-      if (kMod && key.chunk_i >= 0 && a.positions != nullptr) key.pk = a.positions[a.cu[c.s] + key.chunk_i];
+      key.pk = (c.first + c.packed) * kB + ft;
+      if (ci < 0) {
+        key.seen = ~0u;
+      } else if (ci < c.nt) {
+#pragma unroll
+        for (int i = 0; i < CT; ++i) key.seen |= static_cast<uint32_t>((mask()[CT * half + i] >> ci) & 1u) << i;
+        if (kMod && a.positions != nullptr) key.pk = a.positions[c.c0 + ci];
+      }
     }
 
     wait_qk();
@@ -1286,7 +1321,9 @@ cudaError_t launch_tree_preset(const TreeArgs& a, int rows, bool mod, cudaStream
   return mod ? launch_tree_cfg<KB, VB, kLean, 32, true>(a, stream) : launch_tree_cfg<KB, VB, kLean, 32, false>(a, stream);
 }
 
-// Rows of a unit: 32 where the longest tree has no more (half the arithmetic of a tile), 64 otherwise.
+// Rows of a unit: 32 where the longest tree has no more (a tile of 4 drafted tokens of 8 heads costs
+// 0.76 of the 64-row one: 195 against 255 us for 16 sequences of 16384 tokens), 64 otherwise (a tile
+// is unpacked once for them, against twice).
 int tree_rows(int group, int max_tree) { return group * max_tree <= 32 ? 32 : 64; }
 
 size_t tree_head_bytes(int n_seqs) {   // prefix, first
@@ -1323,6 +1360,7 @@ cudaError_t launch_tree(const uint16_t* q, const uint16_t* k_new, const uint16_t
   a.window = score.window;
   a.softcap = score.softcap;
   a.scale = score.softcap > 0.f ? score.scale / score.softcap * kLog2e : score.scale * kLog2e;
+  a.group_inv = (65536 + group - 1) / group;
   const int rows = tree_rows(group, max_tree);
   a.max_units = (group * max_tree + rows - 1) / rows;
   int dev = 0, sms = 0;
