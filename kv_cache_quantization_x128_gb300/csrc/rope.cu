@@ -15,7 +15,8 @@
 // Memory bound: a row is read and written once. Eight lanes take a row, a lane sixteen of its
 // channels as two 16-byte accesses, chosen so that both members of a pair are its own and
 // a rotation needs no exchange; the norm's sum takes three shuffles for the four rows of a warp.
-// MEASURED
+// 65536 tokens of 64 q-heads over 8 kv-heads, fp16, normed: 456 us, 5.9 TB/s of 2.68 GB (87 % of a
+// plain copy's rate); two blocks an SM at 128 registers, three at 80 spill (599 us).
 #include <cuda_bf16.h>
 
 #include "kvarn_common.cuh"
@@ -99,7 +100,7 @@ __device__ __forceinline__ void rope_store(uint16_t* dst, const float (&x)[8]) {
 template <class T, bool kInter>
 __device__ __forceinline__ void rope_rows(const T* src, uint16_t* dst, int heads, int p0, int p1, const float* w, float eps,
                                           bool turn, const float2* c, int ch0, int ch1, bool rot0, bool rot1) {
-  constexpr int kBatch = sizeof(T) == 4 ? 2 : 4;   // passes in flight
+  constexpr int kBatch = 2;   // passes in flight: 456 us for 65536 tokens of 64 + 8 + 8 rows; 1 548, 4 478 (spills)
   const int row = (threadIdx.x & 31) >> 3;
   // a pair is (xa, xb): channels i of the two groups, or two neighbours of one
   float ca[8], sa[8], cb[8], sb[8];                // w cos, w sin of a pair's members
