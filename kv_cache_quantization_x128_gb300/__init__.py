@@ -277,32 +277,38 @@ def _dtype_code(t, name):
 
 def _device_call(lead, tensors, stream, call):
     """call(stream handle) with `lead`'s device current: the calls below launch on the
-    device of their tensors, on its current stream unless one is given."""
+    device of their tensors, on its current stream unless one is given. (The handle of the
+    current stream is asked for directly: a Stream object around it costs 2 us a call.)"""
     import torch
-    if not lead.is_cuda:
+    dev = lead.get_device()
+    if dev < 0:
         raise ValueError("tensors must be CUDA tensors")
-    dev = lead.device
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors are on {dev} and on {t.device}")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"tensors are on {dev}, the stream is on {stream.device}")
-    if dev.index == torch.cuda.current_device():
-        _check(call(ctypes.c_void_p((stream or torch.cuda.current_stream(dev)).cuda_stream)))
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors are on {lead.device} and on {t.device}")
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"tensors are on {lead.device}, the stream is on {stream.device}")
+    else:
+        handle = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        _check(call(handle))
     else:
         with torch.cuda.device(dev):
-            _check(call(ctypes.c_void_p((stream or torch.cuda.current_stream(dev)).cuda_stream)))
+            _check(call(handle))
 
 
 def _heads(t, name, n, heads, dtype):
     """Row stride of a [n, heads, 128] tensor whose rows are contiguous inside."""
-    if t.dim() != 3 or tuple(t.shape) != (n, heads, HEAD_DIM):
+    if t.shape != (n, heads, HEAD_DIM):
         raise ValueError(f"{name} must be [{n}, {heads}, {HEAD_DIM}], got {list(t.shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != HEAD_DIM):
+    row, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != HEAD_DIM):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    return t.stride(0)
+    return row
 
 
 def kvarn_qk_norm_rope(q, k, v, positions, q_out, k_out, v_out, meta: KvarnMeta, q_weight=None, k_weight=None,
