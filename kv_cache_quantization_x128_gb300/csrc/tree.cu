@@ -43,6 +43,7 @@
 #include <algorithm>
 
 #include "decode_tc.cuh"
+#include "kvarn_codes.cuh"
 #include "kvarn_launch.h"
 
 namespace kvarn {
@@ -280,15 +281,6 @@ __device__ __forceinline__ uint32_t tree_po(int c, int tok) {
 }
 
 // ------------------------------------------------------------------ operands
-// A record's 16-byte parts (keys: of a token; 4-bit values: of a channel; 2-bit values: the
-// cells of a channel) hold the elements 16 j + 8 a + 2 c + e in part c. Half h of a team takes
-// parts 2h and 2h + 1, so the K index of such an operand is not the element's own but
-//   64 (c >> 1) + 8 j + 4 a + 2 (c & 1) + e,
-// and the other operand is laid out to match: q' by its writer, p' by the token that a lane
-// stands for (tree_token is the inverse for tokens).
-__device__ __forceinline__ int tree_token(int t) {
-  return (t & 3) | ((t >> 6) & 1) << 2 | ((t >> 2) & 1) << 3 | ((t >> 3) & 7) << 4;
-}
 // Thread t of the warp: 16 consecutive columns of TMEM lane (base lane + t) from r.
 __device__ __forceinline__ void tree_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -315,85 +307,20 @@ __device__ __forceinline__ void tree_add16(uint32_t (&r)[16], const uint16_t* ad
     }
   }
 }
-// Rows of 64 bytes of 4-bit codes: row `row`'s parts 2 half, 2 half + 1 as fp16 code / 8
-// (+ add, by K element) to 32 TMEM columns. Lanes read their two parts in an order of their own, which leaves 2-way
-// bank conflicts of 4-way ones.
-template <bool kAdd>
-__device__ __forceinline__ void tree_codes4(const uint8_t* codes, int row, int half, const uint16_t* add, uint32_t taddr) {
-  const uint4* p = reinterpret_cast<const uint4*>(codes + row * 64) + 2 * half;
-  const bool swap = (row >> 1) & 1;
-  const uint4 x = p[swap ? 1 : 0], y = p[swap ? 0 : 1];
-  const uint32_t w[2][4] = {{swap ? y.x : x.x, swap ? y.y : x.y, swap ? y.z : x.z, swap ? y.w : x.w},
-                            {swap ? x.x : y.x, swap ? x.y : y.y, swap ? x.z : y.z, swap ? x.w : y.w}};
-#pragma unroll
-  for (int mm = 0; mm < 2; ++mm) {
-    uint32_t r[16];
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const uint32_t u = w[c][2 * mm + m];
-        cvt4(u & 0x0F0F0F0Fu, r[8 * m + c], r[8 * m + 2 + c]);
-        cvt4((u >> 4) & 0x0F0F0F0Fu, r[8 * m + 4 + c], r[8 * m + 6 + c]);
-      }
-    if (kAdd) tree_add16(r, add + 32 * mm);
-    tree_st16(taddr + 16 * mm, r);
-  }
-}
-// 2-bit codes [part][word] as fp16 code / 2 (+ add) to 32 TMEM columns.
-template <bool kAdd>
-__device__ __forceinline__ void tree_codes2(const uint32_t (&w)[2][2], const uint16_t* add, uint32_t taddr) {
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    uint32_t r[16];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t v0[4], v1[4];
-      cvt2(w[c][u] & 0x33333333u, v0);
-      cvt2((w[c][u] >> 2) & 0x33333333u, v1);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        r[4 * b + c] = v0[b];
-        r[4 * b + 2 + c] = v1[b];
-      }
-    }
-    if (kAdd) tree_add16(r, add + 32 * u);
-    tree_st16(taddr + 16 * u, r);
-  }
-}
-// Keys of token `tok`.
+// Keys of token `tok`, and values of channel t plus their token's `add` (by K element; sums
+// exact in fp16), to 32 TMEM columns.
 template <int KB>
 __device__ __forceinline__ void tree_keys(const uint8_t* codes, int tok, int half, uint32_t taddr) {
-  if (KB == 4) {
-    tree_codes4<false>(codes, tok, half, nullptr, taddr);
-  } else {
-    const uint4 v = reinterpret_cast<const uint4*>(codes + tok * 32)[half];
-    const uint32_t w[2][2] = {{v.x, v.y}, {v.z, v.w}};
-    tree_codes2<false>(w, nullptr, taddr);
-  }
+  key_codes<KB>(codes, tok, half, [&](int i, uint32_t (&r)[16]) { tree_st16(taddr + 16 * i, r); });
 }
-// Values of channel t plus their token's `add` (by K element; sums exact in fp16).
 template <int VB>
 __device__ __forceinline__ void tree_values(const uint8_t* codes, int t, int half, const uint16_t* add, uint32_t taddr) {
-  if (VB == 4) {
-    tree_codes4<true>(codes, t, half, add + 64 * half, taddr);
-  } else {
-    const uint2* p = reinterpret_cast<const uint2*>(codes + (t >> 4) * 512 + (t & 7) * 64 + ((t >> 3) & 1) * 8 + half * 32);
-    const bool swap = (t >> 1) & 1;
-    const uint2 x = p[swap ? 2 : 0], y = p[swap ? 0 : 2];
-    const uint32_t w[2][2] = {{swap ? y.x : x.x, swap ? y.y : x.y}, {swap ? x.x : y.x, swap ? x.y : y.y}};
-    tree_codes2<true>(w, add + 64 * half, taddr);
-  }
+  value_codes<VB>(codes, t, half, [&](int i, uint32_t (&r)[16]) {
+    tree_add16(r, add + 64 * half + 32 * i);
+    tree_st16(taddr + 16 * i, r);
+  });
 }
 
-// One lane of the (converged) warp. Chosen this way, rather than by its number, the compiler
-// keeps the operands of the UMMAs it issues in uniform registers: 16 of them (N = 64) take
-// 600 cycles from the first to the completion of the last, 1020 otherwise.
-__device__ __forceinline__ bool tree_elect() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
-  return p != 0;
-}
 // An operand with its M (or N) elements contiguous, not swizzled, whose groups of 8 are all the
 // same 16 bytes a K element (stride 0): the operand's 128 rows are 8 that repeat.
 __device__ __forceinline__ uint64_t tree_desc_same(uint32_t saddr) {
@@ -462,7 +389,7 @@ struct TreeTeam {
     tc_operands_written();
     bar();
     if (warp != kTreeIssuer) return;
-    if (tree_elect()) {
+    if (elect_one()) {
       tc_fence_after();
       // bit 15: A, bit 16: B with M or N contiguous
       constexpr uint32_t kId = idesc_f16_f32(128, R), kIdSame = kId | (1u << 15) | (1u << 16);
@@ -489,7 +416,7 @@ struct TreeTeam {
       return;
     }
     named_bar(bar_id + 1, kTreeTeamThreads);
-    if (tree_elect()) {
+    if (elect_one()) {
       tc_fence_after();
       constexpr uint32_t kId = idesc_f16_f32(128, R) | (1u << 16), kIdSame = kId | (1u << 15);
       const uint64_t d = smem_desc_sw128(smem_u32(sm + S::kB0));
@@ -1010,7 +937,7 @@ struct TreeTeam {
       ok = mbar_wait(&bars()[kTbRec + stg], (used / kTreeStages) & 1u, a.flags) && ok;
       valid = valid_of()[stg] != 0;
       const bool go = __all_sync(0xffffffffu, ok) && valid;
-      const int tok = tree_token(t);
+      const int tok = code_token(t);
       if (go) {
         tree_keys<KB>(rec + L::kKCodeOff, tok, half, trow + kTrAK + 32 * half);
         const float kinv = fold(rec);
@@ -1181,7 +1108,7 @@ struct TreeTeam {
   // Every product complete before TMEM is released.
   __device__ void finish() {
     if (warp == kTreeIssuer) {
-      if (tree_elect()) {
+      if (elect_one()) {
         umma_commit(&bars()[kTbFin]);
         mbar_wait(&bars()[kTbFin], 0, a.flags);
       }
