@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kReadThreads, 3) read_kernel(const ReadArgs a)
 
 // ------------------------------------------------------------------ fp16, bf16
 constexpr int kRtTeam = 256, kRtTeams = 2;               // threads of a team, teams of a block
+constexpr int kRtThreads = kRtTeams * (kRtTeam + 64);    // and two warps a team: one fetches its items, one issues its products
 constexpr uint32_t kRtHi = 0, kRtLo = 64, kRtD = 128, kRtCols = 256;   // TMEM columns of a team
 struct ReadDesc {
   void* out;              // output row of the tile's row 0
@@ -281,7 +282,7 @@ struct ReadSm {
   static constexpr int kA = kW + 8 * 256, kBt = kA + 512, kBeta = kBt + 512;   // [128] f32 each, twice
   static constexpr int kTab = 1536;
   static constexpr int kDesc = kA + 2 * kTab, kBars = kDesc + 2 * static_cast<int>(sizeof(ReadDesc));
-  static constexpr int kTeam = (kBars + 24 + 1023) / 1024 * 1024;
+  static constexpr int kTeam = (kBars + 40 + 1023) / 1024 * 1024;
   static constexpr int kSlot = kRtTeams * kTeam, kBytes = kSlot + 16;
   static_assert(kBytes <= 232448, "read shared memory");
 };
@@ -314,50 +315,66 @@ struct ReadTeam {
   uint32_t tm, trow;
   int tt, t, half, lane, warp, bar_id;
 
-  __device__ ReadTeam(const ReadArgs& a_, uint8_t* sm_, uint32_t tm_, int team) : a(a_), sm(sm_), tm(tm_), bar_id(1 + team) {
-    tt = static_cast<int>(threadIdx.x) - team * kRtTeam;
+  __device__ ReadTeam(const ReadArgs& a_, uint8_t* sm_, uint32_t tm_, int team, int tt_)
+      : a(a_), sm(sm_), tm(tm_), tt(tt_), bar_id(1 + team) {
     t = tt & 127;
     half = tt >> 7;
     lane = tt & 31;
     warp = __shfl_sync(0xffffffffu, tt >> 5, 0);
     trow = tm + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
   }
-  __device__ uint64_t* bars() const { return reinterpret_cast<uint64_t*>(sm + S::kBars); }   // records [2], product
+  __device__ uint64_t* bars() const { return reinterpret_cast<uint64_t*>(sm + S::kBars); }   // filled [2], product, free [2]
   __device__ ReadDesc& desc(int stg) const { return reinterpret_cast<ReadDesc*>(sm + S::kDesc)[stg]; }
   __device__ float* table(int off, int stg) const { return reinterpret_cast<float*>(sm + off + stg * S::kTab); }
 
-  // Warp 0: the next item into stage `stg`. The cursor is one item ahead of it: the block table's
-  // entry was asked for a call ago.
-  __device__ void fetch(ReadCursor& c, ReadItem& ahead, int& blk, bool& more, int stg) {
-    const uint8_t* rec = nullptr;
-    const uint16_t* ws = nullptr;
-    bool live = false;
-    ReadItem it = ahead;
-    while (!live && more) {
-      it = ahead;
-      const int b = blk;
-      locate(c, ahead, blk, more);
-      live = read_source(a, it, b, lane == 0, L::kBytes, rec, ws);
-    }
-    if (lane != 0) return;
-    ReadDesc& d = desc(stg);
-    d.live = live;
-    if (!live) return;
-    d.out = read_out<T>(a, it.g, it.row0, it.h);
-    d.ws = ws;
-    d.lo = it.lo;
-    d.hi = it.hi;
-    d.g = it.g;
-    if (rec == nullptr) return;
-    uint8_t* dst = sm + S::kRec + stg * S::kStage;
-    const uint32_t codes = it.g ? L::kVCodeBytes : L::kKCodeBytes;
-    mbar_arrive_expect_tx(&bars()[stg], codes + L::kMetaBytes);
-    bulk_g2s(dst, rec + (it.g ? L::kVCodeOff : L::kKCodeOff), codes, &bars()[stg]);
-    bulk_g2s(dst + S::kCodes, rec + (it.g ? L::kVMetaOff : L::kKMetaOff), L::kMetaBytes, &bars()[stg]);
-  }
-  __device__ void locate(ReadCursor& c, ReadItem& ahead, int& blk, bool& more) {
-    more = c.next(a, static_cast<int64_t>(gridDim.x) * kRtTeams, blockIdx.x == 0 && bar_id == 1, ahead);
+  // The fetching warp: items `first`, and every n-th from there, into the two stages in turn, as they
+  // become free; the last is none. The cursor is an item ahead, so that the block table's entry is there.
+  __device__ void fetch(int64_t first) {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRtTeams;
+    const bool report = blockIdx.x == 0 && bar_id == 1;
+    ReadCursor c(first);
+    ReadItem ahead{};
+    int blk = -1;
+    bool more = c.next(a, step, report, ahead), live = true;
     if (more) blk = read_block(a, ahead);
+    for (uint32_t k = 0; live; ++k) {
+      const uint8_t* rec = nullptr;
+      const uint16_t* ws = nullptr;
+      ReadItem it = ahead;
+      live = false;
+      while (!live && more) {
+        it = ahead;
+        const int b = blk;
+        more = c.next(a, step, report, ahead);
+        if (more) blk = read_block(a, ahead);
+        live = read_source(a, it, b, lane == 0, L::kBytes, rec, ws);
+      }
+      const int stg = k & 1;
+      bool ok = true;
+      if (k >= 2) ok = mbar_wait(&bars()[3 + stg], ((k >> 1) - 1) & 1u, a.flags);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      if (lane == 0) {
+        ReadDesc& d = desc(stg);
+        d.live = live;
+        if (live) {
+          d.out = read_out<T>(a, it.g, it.row0, it.h);
+          d.ws = ws;
+          d.lo = it.lo;
+          d.hi = it.hi;
+          d.g = it.g;
+        }
+        if (live && rec != nullptr) {
+          uint8_t* dst = sm + S::kRec + stg * S::kStage;
+          const uint32_t codes = it.g ? L::kVCodeBytes : L::kKCodeBytes;
+          mbar_arrive_expect_tx(&bars()[stg], codes + L::kMetaBytes);
+          bulk_g2s(dst, rec + (it.g ? L::kVCodeOff : L::kKCodeOff), codes, &bars()[stg]);
+          bulk_g2s(dst + S::kCodes, rec + (it.g ? L::kVMetaOff : L::kKMetaOff), L::kMetaBytes, &bars()[stg]);
+        } else {
+          tc_arrive(&bars()[stg]);
+        }
+      }
+      __syncwarp();
+    }
   }
 
   // The lane's channels 4 lane .. 4 lane + 3: w, and y of the transform.
@@ -415,17 +432,21 @@ struct ReadTeam {
     const uint32_t s0 = ((p & 1) ? 0x80000000u : 0u) ^ ((half && (p & 64)) ? 0x80008000u : 0u);
     const uint32_t b1 = (p & 2) ? 0x80008000u : 0u, b2 = (p & 4) ? 0x80008000u : 0u;
     const uint32_t low[4] = {s0, s0 ^ b1, s0 ^ b2, s0 ^ b1 ^ b2};
+    uint32_t f[8] = {};
+#pragma unroll
+    for (int b = 0; b < 3; ++b)
+#pragma unroll
+      for (int i = 0; i < (1 << b); ++i) f[i | (1 << b)] = f[i] ^ ((p >> (3 + b)) & 1 ? 0x80008000u : 0u);
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
       uint32_t r[32];
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const uint32_t f = __popc((p >> 3) & q) & 1 ? 0x80008000u : 0u;
         const uint4 v = reinterpret_cast<const uint4*>(wt + 128 * part)[q];
-        r[4 * q] = v.x ^ low[0] ^ f;
-        r[4 * q + 1] = v.y ^ low[1] ^ f;
-        r[4 * q + 2] = v.z ^ low[2] ^ f;
-        r[4 * q + 3] = v.w ^ low[3] ^ f;
+        r[4 * q] = v.x ^ low[0] ^ f[q];
+        r[4 * q + 1] = v.y ^ low[1] ^ f[q];
+        r[4 * q + 2] = v.z ^ low[2] ^ f[q];
+        r[4 * q + 3] = v.w ^ low[3] ^ f[q];
       }
       tc_st32(trow + (part ? kRtLo : kRtHi) + 32 * half, r);
     }
@@ -510,67 +531,65 @@ struct ReadTeam {
     }
   }
 
-  // Staged rows to the output, 16 lanes a row.
+  // Staged rows to the output, 16 lanes a row. (Row 16 i + c, c < 16, is the token that c is plus a
+  // constant of i, in either order.)
   __device__ void store_rows(int stg, const ReadDesc& d, int64_t stride) {
-    T* out = static_cast<T*>(d.out) + 8 * (tt & 15);
-    const uint8_t* src = sm + S::kB0 + stg * S::kBPitch + 16 * (tt & 15);
+    const int c = tt >> 4, t0 = d.g ? code_token(c) : c;
+    T* out = static_cast<T*>(d.out) + t0 * stride + 8 * (tt & 15);
+    const uint8_t* src = sm + S::kB0 + stg * S::kBPitch + c * kReadPitch + 16 * (tt & 15);
+    const bool whole = d.lo == 0 && d.hi == kB;
 #pragma unroll
     for (int i = 0; i < kB / 16; ++i) {
-      const int n = 16 * i + (tt >> 4), tok = d.g ? code_token(n) : n;
-      if (tok >= d.lo && tok < d.hi) *reinterpret_cast<uint4*>(out + tok * stride) = *reinterpret_cast<const uint4*>(src + n * kReadPitch);
+      const int k = d.g ? (i & 1) * 32 + (i >> 1 & 1) * 64 + (i >> 2) * 4 : 16 * i;
+      if (whole || (t0 + k >= d.lo && t0 + k < d.hi))
+        *reinterpret_cast<uint4*>(out + k * stride) = *reinterpret_cast<const uint4*>(src + 16 * i * kReadPitch);
     }
-  }
-  __device__ bool wait_record(int stg, uint32_t& ph) {
-    const bool ok = mbar_wait(&bars()[stg], (ph >> stg) & 1u, a.flags);
-    ph ^= 1u << stg;
-    return ok;
   }
 
-  // Item k's product runs while item k - 1's rows are stored, item k + 2's record is fetched and item
-  // k + 1 is prepared; then k's rows are staged.
-  __device__ void run(int64_t first) {
-    const int64_t stride = static_cast<int64_t>(a.hkv) * kD;
-    ReadCursor cursor(first);
-    ReadItem ahead{};
-    int blk = -1;
-    bool more = false;
-    if (warp == 0) {
-      locate(cursor, ahead, blk, more);
-      fetch(cursor, ahead, blk, more, 0);
-      fetch(cursor, ahead, blk, more, 1);
+  // The issuing warp: every item's product, once the team has its operands. (A warp of the team would
+  // be held by it for 1100 cycles an item, and the others at the next barrier.)
+  __device__ void issue() {
+    for (uint32_t k = 0;; ++k) {
+      const int stg = k & 1;
+      bool ok = mbar_wait(&bars()[stg], (k >> 1) & 1u, a.flags);
+      const ReadDesc d = desc(stg);
+      ok = named_bar_and(bar_id, kRtTeam + 32, ok);
+      if (!ok || !d.live) return;
+      if (d.ws == nullptr && elect_one()) product(stg, d.g);
+      __syncwarp();
     }
-    named_bar(bar_id, kRtTeam);
-    uint32_t ph = 0, done = 0;                  // phases of the record barriers, of the product's
-    bool ok = true;
+  }
+
+  // Item k's product runs while item k - 1's rows are stored and item k + 1 is prepared; then k's
+  // rows are staged.
+  __device__ void run() {
+    const int64_t stride = static_cast<int64_t>(a.hkv) * kD;
+    uint32_t ph = 0, done = 0;                  // phases of the filled barriers (by stage), of the product's
     int stg = 0;
-    ReadDesc last{};                            // the item before, whose rows are staged (if live)
-    {
-      const ReadDesc d = desc(0);
-      if (d.live && d.ws == nullptr) {
-        ok = wait_record(0, ph);
-        if (__all_sync(0xffffffffu, ok)) prepare(0, d.g);
-      }
+    ReadDesc d{}, last{};                       // the item, and the one before, whose rows are staged (if live)
+    bool ok = mbar_wait(&bars()[0], 0, a.flags);
+    if (__all_sync(0xffffffffu, ok)) {
+      d = desc(0);
+      if (d.live && d.ws == nullptr) prepare(0, d.g);
     }
     for (;; stg ^= 1) {
-      const ReadDesc d = desc(stg);
       const bool packed = d.live && d.ws == nullptr;
       if (packed && __all_sync(0xffffffffu, ok)) signs(d.g);
       tc_operands_written();
-      ok = named_bar_and(bar_id, kRtTeam, ok);
+      ok = named_bar_and(bar_id, kRtTeam + 32, ok);
       if (!ok) break;
-      if (packed && warp == 7) {
-        if (elect_one()) product(stg, d.g);
-        __syncwarp();
-      }
+      if (tt == 0 && d.live) tc_arrive(&bars()[3 + stg]);   // the record and the description were read
       if (last.live) store_rows(stg ^ 1, last, stride);
       if (!d.live) break;
       if (!packed) read_workspace<T>(d.ws, static_cast<T*>(d.out), stride, d.lo, d.hi, tt, kRtTeam);
-      named_bar(bar_id, kRtTeam);               // the stored rows' place is free
-      if (warp == 0) fetch(cursor, ahead, blk, more, stg);
-      const ReadDesc& next = desc(stg ^ 1);
-      if (next.live && next.ws == nullptr) {
-        ok = wait_record(stg ^ 1, ph);
-        if (__all_sync(0xffffffffu, ok)) prepare(stg ^ 1, next.g);
+      named_bar(bar_id + kRtTeams, kRtTeam);    // the stored rows' place is free
+      ph ^= 1u << stg;
+      last = d;
+      last.live = packed;
+      ok = mbar_wait(&bars()[stg ^ 1], (ph >> (stg ^ 1)) & 1u, a.flags);
+      if (__all_sync(0xffffffffu, ok)) {
+        d = desc(stg ^ 1);
+        if (d.live && d.ws == nullptr) prepare(stg ^ 1, d.g);
       }
       if (packed) {
         ok = mbar_wait(&bars()[2], done, a.flags) && ok;
@@ -579,8 +598,6 @@ struct ReadTeam {
         if (__all_sync(0xffffffffu, ok)) stage_rows(stg);
       }
       tc_fence_before();
-      last = d;
-      last.live = packed;
     }
     if (!ok && tt == 0) {                       // after a timeout: what may be in flight
       mbar_wait(&bars()[2], done, a.flags);
@@ -590,14 +607,14 @@ struct ReadTeam {
 };
 
 template <class T, int KB, int VB, bool kLean>
-__global__ void __launch_bounds__(kRtTeam * kRtTeams, 1) read_tc_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kRtThreads, 1) read_tc_kernel(const ReadArgs a) {
   using S = ReadSm<KB, VB, kLean>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + S::kSlot);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
   if (threadIdx.x == 0) {
     for (int j = 0; j < kRtTeams; ++j)
-      for (int i = 0; i < 3; ++i) mbar_init(reinterpret_cast<uint64_t*>(smem + j * S::kTeam + S::kBars) + i, 1);
+      for (int i = 0; i < 5; ++i) mbar_init(reinterpret_cast<uint64_t*>(smem + j * S::kTeam + S::kBars) + i, 1);
     fence_mbar_init();
   }
   if (warp == 0) tmem_alloc(slot, kRtTeams * kRtCols);
@@ -605,9 +622,15 @@ __global__ void __launch_bounds__(kRtTeam * kRtTeams, 1) read_tc_kernel(const Re
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
-  const int j = warp >> 3;
-  ReadTeam<T, KB, VB, kLean> team(a, smem + j * S::kTeam, tmem + j * kRtCols, j);
-  team.run(static_cast<int64_t>(blockIdx.x) * kRtTeams + j);
+  const int extra = warp - kRtTeams * 8;         // 0, 1: fetch for a team; 2, 3: issue for a team
+  const int j = extra >= 0 ? extra % kRtTeams : warp >> 3;
+  ReadTeam<T, KB, VB, kLean> team(a, smem + j * S::kTeam, tmem + j * kRtCols, j, threadIdx.x & (kRtTeam - 1));
+  if (extra >= kRtTeams)
+    team.issue();
+  else if (extra >= 0)
+    team.fetch(static_cast<int64_t>(blockIdx.x) * kRtTeams + j);
+  else
+    team.run();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -626,7 +649,7 @@ cudaError_t launch_read_cfg(const ReadArgs& a, int sms, cudaStream_t stream) {
     err = set_smem_once(read_tc_kernel<T, KB, VB, kLean>, kSmem, smem_set);
     if (err != cudaSuccess) return err;
     const int64_t grid = std::min(static_cast<int64_t>(sms), (most + kRtTeams - 1) / kRtTeams);
-    read_tc_kernel<T, KB, VB, kLean><<<static_cast<unsigned>(grid), kRtTeam * kRtTeams, kSmem, stream>>>(a);
+    read_tc_kernel<T, KB, VB, kLean><<<static_cast<unsigned>(grid), kRtThreads, kSmem, stream>>>(a);
   } else {
     err = set_smem_once(read_kernel<KB, VB, kLean>, kSmem, smem_set);
     if (err != cudaSuccess) return err;
