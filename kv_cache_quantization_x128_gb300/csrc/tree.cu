@@ -62,6 +62,7 @@ __host__ __device__ constexpr int tree_teams(int r) { return r == 32 ? 3 : 2; }
 constexpr uint32_t kTrAK = 0, kTrAV = 64, kTrS = 128, kTrAcc = 192;
 __host__ __device__ constexpr uint32_t tree_cols(int r) { return r == 32 ? 160 : 256; }
 constexpr float kTau = 8.0f;
+constexpr float kFloatMax = 3.402823466e+38f;
 constexpr float kNoMax = -1.0e30f;     // running max of a record whose row saw no key
 
 struct TreeArgs {
@@ -515,8 +516,10 @@ struct TreeTeam {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], sg, __shfl_xor_sync(0xffffffffu, x[i], o));
       }
+      float top = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+      m = fmaxf(m, top <= kFloatMax ? top : 0.f);   // (a row with an infinity spoils itself only)
       // channels 4 G .. at 16-byte slot 16 e + j of the row (fold's thread j reads slots j, 16 + j)
       float4* dst = reinterpret_cast<float4*>(qs + (r0 + 16 * k) * kD);
       dst[q_slot(2 * jj)] = make_float4(x[0], x[1], x[2], x[3]);
@@ -662,27 +665,66 @@ struct TreeTeam {
 #pragma unroll
     for (int i = 0; i < R / 16; ++i) *reinterpret_cast<uint4*>(sm + S::kB0 + tree_qo(r0 + 16 * i, 8 * jj)) = w[i];
   }
-  __device__ void fresh_values(int f0) {
+  // A value that is not finite is left out of the product, where it would reach the rows that do
+  // not attend its token (0 x infinity), and reported in small()[12].
+  static __device__ bool finite(uint32_t h) { return (h & 0x7C00u) != 0x7C00u; }
+  // Channel t of value f of a tile's (the workspace's rows from w on, then the drafted tokens').
+  struct FreshValues {
+    const uint16_t *w, *v;
+    int64_t step;
+    int nw, n;         // workspace tokens, all tokens from f0 on
+    __device__ uint32_t at(int f) const { return *(f < nw ? w + f * kD : v + f * step); }
+  };
+  __device__ FreshValues fresh_source(int f0) const {
     const TreeCursor& c = cur();
-    const int nw = c.ws - f0, n = nw + c.nt;               // workspace tokens, all tokens from f0 on
-    const uint16_t* w = a.ws + ((static_cast<int64_t>(c.s) * a.hkv + c.h) * 2 + 1) * (kB * kD) + f0 * kD + t;
-    const int64_t step = static_cast<int64_t>(a.hkv) * kD;
-    const uint16_t* v = a.v_new + (c.c0 * a.hkv + c.h) * kD + t - nw * step;
+    FreshValues x;
+    x.nw = c.ws - f0;
+    x.n = x.nw + c.nt;
+    x.w = a.ws + ((static_cast<int64_t>(c.s) * a.hkv + c.h) * 2 + 1) * (kB * kD) + f0 * kD + t;
+    x.step = static_cast<int64_t>(a.hkv) * kD;
+    x.v = a.v_new + (c.c0 * a.hkv + c.h) * kD + t - x.nw * x.step;
+    return x;
+  }
+  __device__ void fresh_values(int f0) {
+    const FreshValues src = fresh_source(f0);
+    bool all = true;
 #pragma unroll 1
     for (int part = 0; part < 4; ++part) {
-      uint16_t x[16];
+      const int p0 = 64 * half + 16 * part;
+      uint32_t x[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {                       // every load at a row that is there, none waits for another
-        const int f = min(64 * half + 16 * part + i, n - 1);
-        x[i] = *(f < nw ? w + f * kD : v + f * step);
-      }
+      for (int i = 0; i < 16; ++i) x[i] = src.at(min(p0 + i, src.n - 1));   // loads of rows that are there, none waits for another
       uint32_t r[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int f = 64 * half + 16 * part + 2 * i;
-        r[i] = (f < n ? x[2 * i] : 0u) | ((f + 1 < n ? x[2 * i + 1] : 0u) << 16);
+      for (int i = 0; i < 16; ++i) {
+        const bool live = p0 + i < src.n, ok_i = finite(x[i]);
+        all = all && (ok_i || !live);
+        x[i] = live && ok_i ? x[i] : 0u;
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[i] = x[2 * i] | (x[2 * i + 1] << 16);
       tree_st8(trow + kTrAV + 32 * half + 8 * part, r);
+    }
+    if (!all) small()[12] = 1.f;
+  }
+  // What rows attend, token by token (bit i: the thread's i-th row), and the values left out
+  // above added to the rows that attend them.
+  __device__ uint32_t* attended() const { return reinterpret_cast<uint32_t*>(sm + S::kU) + half * kB; }
+  __device__ void add_infinite(int f0) {
+    const FreshValues src = fresh_source(f0);
+#pragma unroll 1
+    for (int f = 0; f < min(src.n, kB); ++f) {
+      const uint32_t x = src.at(f), bits = attended()[f];
+      if (__all_sync(0xffffffffu, finite(x))) continue;
+      const float add = finite(x) ? 0.f : h2f_bits(static_cast<uint16_t>(x));
+#pragma unroll
+      for (int ch = 0; ch < CT / 16; ++ch) {
+        float y[16];
+        get_acc(ch, y);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] += (bits >> (16 * ch + i)) & 1u ? add : 0.f;
+        put_acc(ch, y);
+      }
     }
   }
 
@@ -974,6 +1016,7 @@ struct TreeTeam {
       cmax = fmaxf(fmaxf(fabsf(c4.x), fabsf(c4.y)), fmaxf(fabsf(c4.z), fabsf(c4.w)));
       wide = valid && fminf(fminf(c4.x, c4.y), fminf(c4.z, c4.w)) < 0.f;
     } else {
+      if (tt == 0) small()[12] = 0.f;            // (read last behind the barriers of the tile before)
       fresh_keys(f0);
       product_qk(true);
       fresh_values(f0);
@@ -1038,6 +1081,13 @@ struct TreeTeam {
         if (lane < 16) part()[warp * CT + 16 * ch + lane] = m;
       }
     }
+    const bool infinite = fresh && small()[12] != 0.f;
+    if (infinite) {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int i = 0; i < CT; ++i) bits |= (x[i] != -INFINITY ? 1u : 0u) << i;
+      attended()[t] = bits;
+    }
     product_pv(!fresh);
     // while PV runs; the record was read before the barriers above
     if (tt == 0 && !fresh) issued = refill(issued, used + 1 + kTreeStages);
@@ -1063,6 +1113,11 @@ struct TreeTeam {
         }
         put_acc(ch, y);
       }
+    }
+    if (infinite) {
+      bar();
+      add_infinite(f0);
+      bar();
     }
     tc_fence_before();
     return true;

@@ -334,3 +334,36 @@ def test_verify_step_together(env):
         from oracle import kvarn_oracle as o
         want = o.decode(f["q"][:n_seqs].astype(np.float64), d["cache"].cpu().numpy(), ws1, bt, l1)
         assert_decode_close(nxt.float().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("hq,counts", [(16, [5, 1, 16]), (64, [7, 13, 2])])
+@pytest.mark.parametrize("place", ["value", "key", "query", "workspace"])
+def test_infinities_stay_with_the_rows_that_attend_them(env, hq, counts, place):
+    """Infinities and NaN in a drafted token's value or key, in a query row, and in a workspace token
+    that a window leaves out: rows that attend them become what the definition says, the others
+    are as if they were not there."""
+    score = dict(window=200) if place == "workspace" else {}
+    p = make([300, 70, 257], counts, hq, 8, seed=130)
+    cu = p["cu"]
+    if place == "value":
+        p["v"][cu[0] + 2, 3, [5, 6, 127]] = np.float16([np.inf, np.nan, -np.inf])
+        p["v"][cu[2], 0, 64] = -np.inf
+    elif place == "key":
+        p["k"][cu[0] + 1, 2, 17] = np.nan
+        p["k"][cu[2] + 1, 7, 0] = np.inf
+    elif place == "query":
+        p["q"][cu[0] + 1, 3, 9] = np.inf
+        p["q"][cu[2], hq - 1, 100] = np.nan
+    else:
+        p["pos"][:] = np.where(np.arange(p["n"]) % 2 == 0, 600, 400)      # windows from 401 on, and from 201 on
+        p["ws"][0, 1, 1, 20, 3] = np.nan                                   # position 276
+        p["ws"][2, 4, 1, 0, 8] = np.inf                                    # position 256
+    got = run(env, p, **score)
+    with np.errstate(all="ignore"):
+        want = vo.tree_attention(p["q"], p["k"], p["v"], p["words"], p["cu"], p["lens"], p["bt"], p["ws"], p["cache"],
+                                 positions=p["pos"], **score)
+    bad = ~np.isfinite(want)
+    assert bad.any() and not bad.all()
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+    assert_decode_close(got[~bad], want[~bad])
