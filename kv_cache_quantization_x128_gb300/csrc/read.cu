@@ -265,28 +265,36 @@ __global__ void __launch_bounds__(kReadThreads, 3) read_kernel(const ReadArgs a)
 }
 
 // ------------------------------------------------------------------ fp16, bf16
-constexpr int kRtTeam = 256, kRtTeams = 2;               // threads of a team, teams of a block
-constexpr int kRtThreads = kRtTeams * (kRtTeam + 64);    // and two warps a team: one fetches its items, one issues its products
-constexpr uint32_t kRtHi = 0, kRtLo = 64, kRtD = 128, kRtCols = 256;   // TMEM columns of a team
+// One block an SM. Warps 0-7 (the front) turn an item's record into its product's operands, warps 8-15
+// (the back) turn the product into rows, one warp fetches records, one issues products; operands,
+// product and rows are double buffered, so that each works on an item of its own. Handed on by
+// mbarriers, each of two (an item's by its number's parity):
+//   filled  the record is there                    fetch  -> front
+//   ready   the operands are, the record is free   front  -> issue, fetch
+//   done    the product is                         issue  -> back
+//   free    and has been read, the tables too      back   -> front
+constexpr int kRtTeam = 256, kRtThreads = 2 * kRtTeam + 64;
+constexpr uint32_t kRtHi = 0, kRtLo = 64, kRtA = 128, kRtD = 256, kRtCols = 512;   // TMEM: two A, two D of 128 columns
+constexpr int kRtFilled = 0, kRtReady = 2, kRtDone = 4, kRtFree = 6;
 struct ReadDesc {
   void* out;              // output row of the tile's row 0
   const uint16_t* ws;     // workspace rows, or NULL
   int lo, hi, g, live;
 };
-// Shared memory of a team. Two B operands; an item's output rows are staged where its own was.
 template <int KB, int VB, bool kLean>
 struct ReadSm {
   using L = RecordLayout<KB, VB, kLean>;
   static constexpr int kCodes = L::kKCodeBytes > L::kVCodeBytes ? L::kKCodeBytes : L::kVCodeBytes;
-  static constexpr int kB0 = 0, kBPitch = (kB * kReadPitch + 1023) / 1024 * 1024;
+  static constexpr int kB0 = 0, kBPitch = 32768;
+  static constexpr int kRows = 2 * kBPitch, kRowsPitch = kB * kReadPitch;   // staged output rows
   static constexpr int kStage = kCodes + L::kMetaBytes;
-  static constexpr int kRec = 2 * kBPitch;               // two stages of codes and metadata
+  static constexpr int kRec = kRows + 2 * kRowsPitch;    // two stages of codes and metadata
   static constexpr int kW = kRec + 2 * kStage;           // [8 warps] 64 fp16 hi, 64 fp16 lo of w
   static constexpr int kA = kW + 8 * 256, kBt = kA + 512, kBeta = kBt + 512;   // [128] f32 each, twice
   static constexpr int kTab = 1536;
-  static constexpr int kDesc = kA + 2 * kTab, kBars = kDesc + 2 * static_cast<int>(sizeof(ReadDesc));
-  static constexpr int kTeam = (kBars + 40 + 1023) / 1024 * 1024;
-  static constexpr int kSlot = kRtTeams * kTeam, kBytes = kSlot + 16;
+  static constexpr int kDesc = kA + 2 * kTab;            // two for the front, two for issue and back
+  static constexpr int kBars = kDesc + 4 * static_cast<int>(sizeof(ReadDesc));
+  static constexpr int kSlot = kBars + 64, kBytes = kSlot + 8;
   static_assert(kBytes <= 232448, "read shared memory");
 };
 
@@ -321,29 +329,36 @@ struct ReadTeam {
   const ReadArgs& a;
   uint8_t* sm;
   uint32_t tm, trow;
-  int tt, t, half, lane, warp, bar_id;
+  int tt, t, half, lane, warp;             // thread tt of front or back: TMEM lane t, half of the columns
 
-  __device__ ReadTeam(const ReadArgs& a_, uint8_t* sm_, uint32_t tm_, int team, int tt_)
-      : a(a_), sm(sm_), tm(tm_), tt(tt_), bar_id(1 + team) {
+  __device__ ReadTeam(const ReadArgs& a_, uint8_t* sm_, uint32_t tm_) : a(a_), sm(sm_), tm(tm_) {
+    tt = threadIdx.x & (kRtTeam - 1);
     t = tt & 127;
     half = tt >> 7;
     lane = tt & 31;
     warp = __shfl_sync(0xffffffffu, tt >> 5, 0);
     trow = tm + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
   }
-  __device__ uint64_t* bars() const { return reinterpret_cast<uint64_t*>(sm + S::kBars); }   // filled [2], product, free [2]
-  __device__ ReadDesc& desc(int stg) const { return reinterpret_cast<ReadDesc*>(sm + S::kDesc)[stg]; }
+  __device__ uint64_t* bar(int kind, uint32_t k) const { return reinterpret_cast<uint64_t*>(sm + S::kBars) + kind + (k & 1); }
+  // Item k's turn at a barrier (warp-uniform).
+  __device__ bool wait(int kind, uint32_t k) const {
+    return __all_sync(0xffffffffu, mbar_wait(bar(kind, k), (k >> 1) & 1u, a.flags));
+  }
+  __device__ void arrive(int kind, uint32_t k) const {   // one of the team's 8 warps
+    __syncwarp();
+    if (lane == 0) tc_arrive(bar(kind, k));
+  }
+  __device__ ReadDesc& desc(int k) const { return reinterpret_cast<ReadDesc*>(sm + S::kDesc)[k]; }
   __device__ float* table(int off, int stg) const { return reinterpret_cast<float*>(sm + off + stg * S::kTab); }
 
-  // The fetching warp: items `first`, and every n-th from there, into the two stages in turn, as they
-  // become free; the last is none. The cursor is an item ahead, so that the block table's entry is there.
-  __device__ void fetch(int64_t first) {
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kRtTeams;
-    const bool report = blockIdx.x == 0 && bar_id == 1;
-    ReadCursor c(first);
+  // The fetching warp: the block's items into the two stages in turn, as they become free; the last is
+  // none. The cursor is an item ahead, so that the block table's entry is there.
+  __device__ void fetch() {
+    const bool report = blockIdx.x == 0;
+    ReadCursor c(blockIdx.x);
     ReadItem ahead{};
     int blk = -1;
-    bool more = c.next(a, step, report, ahead), live = true;
+    bool more = c.next(a, gridDim.x, report, ahead), live = true;
     if (more) blk = read_block(a, ahead);
     for (uint32_t k = 0; live; ++k) {
       const uint8_t* rec = nullptr;
@@ -353,16 +368,16 @@ struct ReadTeam {
       while (!live && more) {
         it = ahead;
         const int b = blk;
-        more = c.next(a, step, report, ahead);
+        more = c.next(a, gridDim.x, report, ahead);
         if (more) blk = read_block(a, ahead);
         live = read_source(a, it, b, lane == 0, L::kBytes, rec, ws);
       }
-      const int stg = k & 1;
-      bool ok = true;
-      if (k >= 2) ok = mbar_wait(&bars()[3 + stg], ((k >> 1) - 1) & 1u, a.flags);
-      if (!__all_sync(0xffffffffu, ok)) return;
+      if (k >= 2 && !wait(kRtReady, k - 2)) {
+        wait(kRtFilled, k - 1);                 // (timed out: the copy still in flight)
+        return;
+      }
       if (lane == 0) {
-        ReadDesc& d = desc(stg);
+        ReadDesc& d = desc(k & 1);
         d.live = live;
         if (live) {
           d.out = read_out<T>(a, it.g, it.row0, it.h);
@@ -371,14 +386,15 @@ struct ReadTeam {
           d.hi = it.hi;
           d.g = it.g;
         }
+        uint64_t* filled = bar(kRtFilled, k);
         if (live && rec != nullptr) {
-          uint8_t* dst = sm + S::kRec + stg * S::kStage;
+          uint8_t* dst = sm + S::kRec + (k & 1) * S::kStage;
           const uint32_t codes = it.g ? L::kVCodeBytes : L::kKCodeBytes;
-          mbar_arrive_expect_tx(&bars()[stg], codes + L::kMetaBytes);
-          bulk_g2s(dst, rec + (it.g ? L::kVCodeOff : L::kKCodeOff), codes, &bars()[stg]);
-          bulk_g2s(dst + S::kCodes, rec + (it.g ? L::kVMetaOff : L::kKMetaOff), L::kMetaBytes, &bars()[stg]);
+          mbar_arrive_expect_tx(filled, codes + L::kMetaBytes);
+          bulk_g2s(dst, rec + (it.g ? L::kVCodeOff : L::kKCodeOff), codes, filled);
+          bulk_g2s(dst + S::kCodes, rec + (it.g ? L::kVMetaOff : L::kKMetaOff), L::kMetaBytes, filled);
         } else {
-          tc_arrive(&bars()[stg]);
+          tc_arrive(filled);
         }
       }
       __syncwarp();
@@ -434,7 +450,7 @@ struct ReadTeam {
   }
   // A of the product: A[channel t][k] = w_k with the sign of H: the parity of channel & k, in
   // K's order of bits.
-  __device__ void signs(int g) {
+  __device__ void signs(int stg, int g) {
     const uint8_t* wt = sm + S::kW + warp * 256;
     const int p = g ? t : (t & 3) | ((t >> 3) & 1) << 2 | ((t >> 4) & 7) << 3 | ((t >> 2) & 1) << 6;
     const uint32_t s0 = ((p & 1) ? 0x80000000u : 0u) ^ ((half && (p & 64)) ? 0x80008000u : 0u);
@@ -456,26 +472,27 @@ struct ReadTeam {
         r[4 * q + 2] = read_xor3(v.z, low[2], f[q]);
         r[4 * q + 3] = read_xor3(v.w, low[3], f[q]);
       }
-      tc_st32(trow + (part ? kRtLo : kRtHi) + 32 * half, r);
+      tc_st32(trow + stg * kRtA + (part ? kRtLo : kRtHi) + 32 * half, r);
     }
   }
   __device__ void product(int stg, int g) {
     tc_fence_after();
-    const uint64_t d = smem_desc_sw128(smem_u32(sm + S::kB0 + stg * S::kBPitch));
+    const uint64_t b = smem_desc_sw128(smem_u32(sm + S::kB0 + stg * S::kBPitch));
+    const uint32_t at = tm + stg * kRtA + kRtHi, d = tm + kRtD + stg * 128;
     if (g == 0) {
       constexpr uint32_t kId = idesc_f16_f32(128, 128);
 #pragma unroll
       for (int s = 0; s < 16; ++s)
-        tc_umma_ts(tm + kRtD, tm + kRtHi + 8 * s, d + ((((s >> 2) & 1) * 16384 + (s & 3) * 32) >> 4), kId, s > 0);
+        tc_umma_ts(d, at + 8 * s, b + ((((s >> 2) & 1) * 16384 + (s & 3) * 32) >> 4), kId, s > 0);
     } else {
       constexpr uint32_t kId = idesc_f16_f32(128, 64) | (1u << 16);   // B with N contiguous
 #pragma unroll
       for (int s = 0; s < 16; ++s)
 #pragma unroll
         for (int n = 0; n < 2; ++n)
-          tc_umma_ts(tm + kRtD + 64 * n, tm + kRtHi + 8 * s, d + ((n * 16384 + (s & 7) * 2048) >> 4), kId, s > 0);
+          tc_umma_ts(d + 64 * n, at + 8 * s, b + ((n * 16384 + (s & 7) * 2048) >> 4), kId, s > 0);
     }
-    umma_commit(&bars()[2]);
+    umma_commit(bar(kRtDone, stg));
   }
   // sum_i H_ch,i y_i for the 128 channels, lane l holding y of 4 l .. 4 l + 3.
   __device__ void transform(int stg, float (&y)[4]) {
@@ -522,7 +539,7 @@ struct ReadTeam {
 #pragma unroll
       for (int sub = 0; sub < 2; ++sub) {
         float x[16];
-        read_ld16x32(trow + (static_cast<uint32_t>(16 * sub) << 16) + kRtD + n0, x);
+        read_ld16x32(trow + (static_cast<uint32_t>(16 * sub) << 16) + kRtD + stg * 128 + n0, x);
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
           uint32_t r[4];
@@ -533,7 +550,7 @@ struct ReadTeam {
             r[e] = pack2<T>(__ffma2_rn(make_float2(x[k], x[k + 1]), av[jj], __fmul2_rn(bv[jj], make_float2(b, b))));
           }
           const int mt = lane >> 3, n = n0 + 8 * (j + (mt >> 1)) + (lane & 7);
-          read_stmatrix(sm + S::kB0 + stg * S::kBPitch + n * kReadPitch + (32 * q + 16 * sub + 8 * (mt & 1)) * 2, r);
+          read_stmatrix(sm + S::kRows + stg * S::kRowsPitch + n * kReadPitch + (32 * q + 16 * sub + 8 * (mt & 1)) * 2, r);
         }
       }
     }
@@ -545,7 +562,7 @@ struct ReadTeam {
     const int c = tt >> 4, t0 = d.g ? code_token(c) : c;
     const int row = a.hkv * (kD * static_cast<int>(sizeof(T)));          // bytes
     uint8_t* out = static_cast<uint8_t*>(d.out) + static_cast<int64_t>(t0) * row + 16 * (tt & 15);
-    const uint8_t* src = sm + S::kB0 + stg * S::kBPitch + c * kReadPitch + 16 * (tt & 15);
+    const uint8_t* src = sm + S::kRows + stg * S::kRowsPitch + c * kReadPitch + 16 * (tt & 15);
     const int64_t step = static_cast<int64_t>(row) * (d.g ? 32 : 16), back = d.g ? static_cast<int64_t>(row) * 4 : 4 * step;
     if (d.lo == 0 && d.hi == kB) {
 #pragma unroll
@@ -568,62 +585,54 @@ struct ReadTeam {
     }
   }
 
-  // The issuing warp: every item's product, once the team has its operands. (A warp of the team would
-  // be held by it for 1100 cycles an item, and the others at the next barrier.)
+  __device__ void front() {
+    for (uint32_t k = 0;; ++k) {
+      const int stg = k & 1;
+      if (!wait(kRtFilled, k)) return;
+      const ReadDesc d = desc(stg);
+      if (k >= 2 && !wait(kRtFree, k - 2)) return;
+      if (d.live && d.ws == nullptr) {
+        prepare(stg, d.g);
+        signs(stg, d.g);
+      }
+      if (tt == 0) desc(2 + stg) = d;
+      tc_operands_written();
+      arrive(kRtReady, k);
+      if (!d.live) return;
+    }
+  }
   __device__ void issue() {
     for (uint32_t k = 0;; ++k) {
       const int stg = k & 1;
-      bool ok = mbar_wait(&bars()[stg], (k >> 1) & 1u, a.flags);
-      const ReadDesc d = desc(stg);
-      ok = named_bar_and(bar_id, kRtTeam + 32, ok);
-      if (!ok || !d.live) return;
-      if (d.ws == nullptr && elect_one()) product(stg, d.g);
+      if (!wait(kRtReady, k)) break;
+      const ReadDesc d = desc(2 + stg);
+      const bool packed = d.live && d.ws == nullptr;
+      if (packed && elect_one()) product(stg, d.g);
       __syncwarp();
+      if (lane == 0) {                          // with the product's own arrival, two
+        tc_arrive(bar(kRtDone, k));
+        if (!packed) tc_arrive(bar(kRtDone, k));
+      }
+      if (!d.live) break;
     }
   }
-
-  // Item k's product runs while item k - 1's rows are stored and item k + 1 is prepared; then k's
-  // rows are staged.
-  __device__ void run() {
-    const int64_t stride = static_cast<int64_t>(a.hkv) * kD;
-    uint32_t ph = 0, done = 0;                  // phases of the filled barriers (by stage), of the product's
-    int stg = 0;
-    ReadDesc d{}, last{};                       // the item, and the one before, whose rows are staged (if live)
-    bool ok = mbar_wait(&bars()[0], 0, a.flags);
-    if (__all_sync(0xffffffffu, ok)) {
-      d = desc(0);
-      if (d.live && d.ws == nullptr) prepare(0, d.g);
-    }
-    for (;; stg ^= 1) {
+  __device__ void back() {
+    for (uint32_t k = 0;; ++k) {
+      const int stg = k & 1;
+      bool ok = wait(kRtDone, k);
+      tc_fence_after();
+      ReadDesc d{};
+      if (ok) d = desc(2 + stg);
       const bool packed = d.live && d.ws == nullptr;
-      if (packed && __all_sync(0xffffffffu, ok)) signs(d.g);
-      tc_operands_written();
-      ok = named_bar_and(bar_id, kRtTeam + 32, ok);
-      if (!ok) break;
-      if (tt == 0 && d.live) tc_arrive(&bars()[3 + stg]);   // the record and the description were read
-      if (last.live) store_rows(stg ^ 1, last);
-      if (!d.live) break;
-      if (!packed) read_workspace<T>(d.ws, static_cast<T*>(d.out), stride, d.lo, d.hi, tt, kRtTeam);
-      named_bar(bar_id + kRtTeams, kRtTeam);    // the stored rows' place is free
-      ph ^= 1u << stg;
-      last = d;
-      last.live = packed;
-      ok = mbar_wait(&bars()[stg ^ 1], (ph >> (stg ^ 1)) & 1u, a.flags);
-      if (__all_sync(0xffffffffu, ok)) {
-        d = desc(stg ^ 1);
-        if (d.live && d.ws == nullptr) prepare(stg ^ 1, d.g);
-      }
-      if (packed) {
-        ok = mbar_wait(&bars()[2], done, a.flags) && ok;
-        done ^= 1u;
-        tc_fence_after();
-        if (__all_sync(0xffffffffu, ok)) stage_rows(stg);
-      }
+      if (packed) stage_rows(stg);
       tc_fence_before();
-    }
-    if (!ok && tt == 0) {                       // after a timeout: what may be in flight
-      mbar_wait(&bars()[2], done, a.flags);
-      for (int i = 0; i < 2; ++i) mbar_wait(&bars()[i], (ph >> i) & 1u, a.flags);
+      arrive(kRtFree, k);
+      ok = named_bar_and(1, kRtTeam, ok);
+      if (!ok || !d.live) return;
+      if (packed)
+        store_rows(stg, d);
+      else
+        read_workspace<T>(d.ws, static_cast<T*>(d.out), static_cast<int64_t>(a.hkv) * kD, d.lo, d.hi, tt, kRtTeam);
     }
   }
 };
@@ -635,28 +644,28 @@ __global__ void __launch_bounds__(kRtThreads, 1) read_tc_kernel(const ReadArgs a
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + S::kSlot);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0);
   if (threadIdx.x == 0) {
-    for (int j = 0; j < kRtTeams; ++j)
-      for (int i = 0; i < 5; ++i) mbar_init(reinterpret_cast<uint64_t*>(smem + j * S::kTeam + S::kBars) + i, 1);
+    for (int i = 0; i < 8; ++i)
+      mbar_init(reinterpret_cast<uint64_t*>(smem + S::kBars) + i, i < kRtReady ? 1 : i >= kRtDone && i < kRtFree ? 2 : 8);
     fence_mbar_init();
   }
-  if (warp == 0) tmem_alloc(slot, kRtTeams * kRtCols);
+  if (warp == 0) tmem_alloc(slot, kRtCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
-  const int extra = warp - kRtTeams * 8;         // 0, 1: fetch for a team; 2, 3: issue for a team
-  const int j = extra >= 0 ? extra % kRtTeams : warp >> 3;
-  ReadTeam<T, KB, VB, kLean> team(a, smem + j * S::kTeam, tmem + j * kRtCols, j, threadIdx.x & (kRtTeam - 1));
-  if (extra >= kRtTeams)
-    team.issue();
-  else if (extra >= 0)
-    team.fetch(static_cast<int64_t>(blockIdx.x) * kRtTeams + j);
+  ReadTeam<T, KB, VB, kLean> team(a, smem, tmem);
+  if (warp < 8)
+    team.front();
+  else if (warp < 16)
+    team.back();
+  else if (warp == 16)
+    team.fetch();
   else
-    team.run();
+    team.issue();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) tmem_dealloc(tmem, kRtTeams * kRtCols);
+  if (warp == 0) tmem_dealloc(tmem, kRtCols);
 }
 
 template <class T, int KB, int VB, bool kLean>
@@ -670,7 +679,7 @@ cudaError_t launch_read_cfg(const ReadArgs& a, int sms, cudaStream_t stream) {
   if constexpr (kTc) {
     err = set_smem_once(read_tc_kernel<T, KB, VB, kLean>, kSmem, smem_set);
     if (err != cudaSuccess) return err;
-    const int64_t grid = std::min(static_cast<int64_t>(sms), (most + kRtTeams - 1) / kRtTeams);
+    const int64_t grid = std::min(static_cast<int64_t>(sms), most);
     read_tc_kernel<T, KB, VB, kLean><<<static_cast<unsigned>(grid), kRtThreads, kSmem, stream>>>(a);
   } else {
     err = set_smem_once(read_kernel<KB, VB, kLean>, kSmem, smem_set);
