@@ -1,5 +1,6 @@
 // Internal launchers shared between the libkvarn translation units.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -23,6 +24,10 @@ inline cudaError_t set_smem_once(Kernel* kernel, int bytes, std::atomic<unsigned
   if (err == cudaSuccess && cacheable) done.fetch_or(1ull << dev, std::memory_order_acq_rel);
   return err;
 }
+
+// TMA map of a matrix [rows][row_elems] of 16-bit elements in boxes of 64 channels x 128
+// rows with the 128-byte swizzle (row_elems a multiple of 64, base 16-byte aligned).
+cudaError_t tile_map(CUtensorMap* m, const void* base, uint64_t row_elems, uint64_t rows);
 
 // k_bits / v_bits / lean: a preset of kvarn.h (4/2, 4/4, 2/2; lean with 4/2 only),
 // checked by the caller.

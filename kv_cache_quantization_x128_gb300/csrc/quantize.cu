@@ -654,8 +654,8 @@ EncodeTiledFn encode_tiled() {
   return fn;
 }
 
-// TMA map of an fp16 matrix [rows][row_elems] read in boxes of 64 channels x 128
-// rows with the 128-byte swizzle (row_elems a multiple of 64, base 16-byte aligned).
+}  // namespace
+
 cudaError_t tile_map(CUtensorMap* m, const void* base, uint64_t row_elems, uint64_t rows) {
   const EncodeTiledFn fn = encode_tiled();
   if (fn == nullptr) return cudaErrorNotSupported;
@@ -669,8 +669,6 @@ cudaError_t tile_map(CUtensorMap* m, const void* base, uint64_t row_elems, uint6
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
-
-}  // namespace
 
 cudaError_t launch_quantize_prefill(const uint16_t* k, const uint16_t* v, const int64_t* slot, int64_t n_tokens,
                                     int hkv, int64_t num_blocks, uint8_t* cache, int k_bits, int v_bits, bool lean,

@@ -39,6 +39,7 @@ constexpr int kReadThreads = 128;
 constexpr int kReadPitch = 272;   // bytes of a staged 256-byte row: 8 rows' 16-byte pieces hit 32 banks
 
 struct ReadArgs {
+  CUtensorMap map[2];             // fp16, bf16: k and v as [n_tokens][hkv * 128]
   const uint8_t* cache;
   const uint16_t* ws;
   const int32_t *block_tables, *seq_lens, *first, *cu;
@@ -277,7 +278,8 @@ constexpr int kRtTeam = 256, kRtThreads = 2 * kRtTeam + 64;
 constexpr uint32_t kRtHi = 0, kRtLo = 64, kRtA = 128, kRtD = 256, kRtCols = 512;   // TMEM: two A, two D of 128 columns
 constexpr int kRtFilled = 0, kRtReady = 2, kRtDone = 4, kRtFree = 6;
 struct ReadDesc {
-  void* out;              // output row of the tile's row 0
+  void* out;              // output row of the tile's row 0, and its place in the output's map
+  int x, y;
   const uint16_t* ws;     // workspace rows, or NULL
   int lo, hi, g, live;
 };
@@ -286,7 +288,7 @@ struct ReadSm {
   using L = RecordLayout<KB, VB, kLean>;
   static constexpr int kCodes = L::kKCodeBytes > L::kVCodeBytes ? L::kKCodeBytes : L::kVCodeBytes;
   static constexpr int kB0 = 0, kBPitch = 32768;
-  static constexpr int kRows = 2 * kBPitch, kRowsPitch = kB * kReadPitch;   // staged output rows
+  static constexpr int kRows = 2 * kBPitch, kRowsPitch = 32768;   // staged output rows, as the map's boxes
   static constexpr int kStage = kCodes + L::kMetaBytes;
   static constexpr int kRec = kRows + 2 * kRowsPitch;    // two stages of codes and metadata
   static constexpr int kW = kRec + 2 * kStage;           // [8 warps] 64 fp16 hi, 64 fp16 lo of w
@@ -381,6 +383,8 @@ struct ReadTeam {
         d.live = live;
         if (live) {
           d.out = read_out<T>(a, it.g, it.row0, it.h);
+          d.x = it.h * kD;
+          d.y = static_cast<int>(it.row0);
           d.ws = ws;
           d.lo = it.lo;
           d.hi = it.hi;
@@ -521,9 +525,13 @@ struct ReadTeam {
     table(S::kA, stg)[n] = av;
     table(S::kBt, stg)[n] = bv;
   }
-  // D to staged rows (row n: D's column n).
-  __device__ void stage_rows(int stg) {
-    const int q = warp & 3, r0 = 32 * q + (lane >> 2);
+  // D to the item's rows, staged by token as two boxes of 64 channels (128-byte swizzled; the tokens
+  // of 8 columns of values differ in 4 of their low bits only, which puts two lanes on a bank).
+  __device__ void stage_rows(int stg, int g) {
+    const int q = warp & 3, r0 = 32 * q + (lane >> 2), mt = lane >> 3, l7 = lane & 7;
+    const int tok0 = g ? (l7 & 3) | half << 2 | (l7 >> 2) << 3 | (mt >> 1) << 4 : l7 | (mt >> 1) << 3 | half << 6;
+    uint8_t* const rows = sm + S::kRows + stg * S::kRowsPitch + (q >> 1) * 16384 + tok0 * 128;
+    const int sw = tok0 & 7, chunk = 4 * (q & 1) + (mt & 1), cj = g ? 4096 : 2048;   // bytes between columns 16 apart
     float be[2][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) be[i >> 1][i & 1] = table(S::kBeta, stg)[r0 + 8 * i];
@@ -549,40 +557,20 @@ struct ReadTeam {
             const float b = be[sub][e & 1];
             r[e] = pack2<T>(__ffma2_rn(make_float2(x[k], x[k + 1]), av[jj], __fmul2_rn(bv[jj], make_float2(b, b))));
           }
-          const int mt = lane >> 3, n = n0 + 8 * (j + (mt >> 1)) + (lane & 7);
-          read_stmatrix(sm + S::kRows + stg * S::kRowsPitch + n * kReadPitch + (32 * q + 16 * sub + 8 * (mt & 1)) * 2, r);
+          read_stmatrix(rows + (2 * c + (j >> 1)) * cj + (((chunk + 2 * sub) ^ sw) << 4), r);
         }
       }
     }
   }
 
-  // Staged rows to the output, 16 lanes a row: the thread's are c + 16 i of the columns (c < 16), in the
-  // order of memory the token of c and then 16 (keys) or 4 and 32 (values) further.
+  // Rows [lo, hi) of a tile that is not read as a whole, 16 lanes a row.
   __device__ void store_rows(int stg, const ReadDesc& d) {
-    const int c = tt >> 4, t0 = d.g ? code_token(c) : c;
-    const int row = a.hkv * (kD * static_cast<int>(sizeof(T)));          // bytes
-    uint8_t* out = static_cast<uint8_t*>(d.out) + static_cast<int64_t>(t0) * row + 16 * (tt & 15);
-    const uint8_t* src = sm + S::kRows + stg * S::kRowsPitch + c * kReadPitch + 16 * (tt & 15);
-    const int64_t step = static_cast<int64_t>(row) * (d.g ? 32 : 16), back = d.g ? static_cast<int64_t>(row) * 4 : 4 * step;
-    if (d.lo == 0 && d.hi == kB) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint8_t* p = out + h * back;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(src + 16 * (4 * h + i) * kReadPitch);
-          p += step;
-        }
-      }
-    } else {
-#pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        const int tok = t0 + (d.g ? 32 * (i & 3) + 4 * (i >> 2) : 16 * i);
-        if (tok >= d.lo && tok < d.hi)
-          *reinterpret_cast<uint4*>(out + (i & 3) * step + (i >> 2) * back) =
-              *reinterpret_cast<const uint4*>(src + 16 * i * kReadPitch);
-      }
-    }
+    const int l = tt & 15, row = a.hkv * (kD * static_cast<int>(sizeof(T)));          // bytes
+    const uint8_t* src = sm + S::kRows + stg * S::kRowsPitch + (l >> 3) * 16384;
+    uint8_t* out = static_cast<uint8_t*>(d.out) + 16 * l;
+    for (int r = d.lo + (tt >> 4); r < d.hi; r += kRtTeam / 16)
+      *reinterpret_cast<uint4*>(out + static_cast<int64_t>(r) * row) =
+          *reinterpret_cast<const uint4*>(src + r * 128 + (((l & 7) ^ (r & 7)) << 4));
   }
 
   __device__ void front() {
@@ -624,21 +612,31 @@ struct ReadTeam {
       ReadDesc d{};
       if (ok) d = desc(2 + stg);
       const bool packed = d.live && d.ws == nullptr;
-      if (packed) stage_rows(stg);
+      if (packed) stage_rows(stg, d.g);
       tc_fence_before();
       arrive(kRtFree, k);
+      fence_proxy_async_smem();
+      if (tt == 0) bulk_wait_read_all();        // the rows of the item before have left
       ok = named_bar_and(1, kRtTeam, ok);
       if (!ok || !d.live) return;
-      if (packed)
+      if (packed && d.lo == 0 && d.hi == kB) {
+        if (tt == 0) {
+          const uint8_t* src = sm + S::kRows + stg * S::kRowsPitch;
+          tma_store_2d(&a.map[d.g], d.x, d.y, src);
+          tma_store_2d(&a.map[d.g], d.x + 64, d.y, src + 16384);
+          bulk_commit();
+        }
+      } else if (packed) {
         store_rows(stg, d);
-      else
+      } else {
         read_workspace<T>(d.ws, static_cast<T*>(d.out), static_cast<int64_t>(a.hkv) * kD, d.lo, d.hi, tt, kRtTeam);
+      }
     }
   }
 };
 
 template <class T, int KB, int VB, bool kLean>
-__global__ void __launch_bounds__(kRtThreads, 1) read_tc_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kRtThreads, 1) read_tc_kernel(const __grid_constant__ ReadArgs a) {
   using S = ReadSm<KB, VB, kLean>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + S::kSlot);
@@ -669,7 +667,7 @@ __global__ void __launch_bounds__(kRtThreads, 1) read_tc_kernel(const ReadArgs a
 }
 
 template <class T, int KB, int VB, bool kLean>
-cudaError_t launch_read_cfg(const ReadArgs& a, int sms, cudaStream_t stream) {
+cudaError_t launch_read_cfg(ReadArgs& a, int sms, cudaStream_t stream) {
   constexpr bool kTc = sizeof(T) == 2;
   constexpr int kSmem = kTc ? ReadSm<KB, VB, kLean>::kBytes : kB * kReadPitch;
   static std::atomic<unsigned long long> smem_set{0};
@@ -678,6 +676,9 @@ cudaError_t launch_read_cfg(const ReadArgs& a, int sms, cudaStream_t stream) {
   cudaError_t err;
   if constexpr (kTc) {
     err = set_smem_once(read_tc_kernel<T, KB, VB, kLean>, kSmem, smem_set);
+    for (int g = 0; g < 2 && err == cudaSuccess; ++g)
+      err = tile_map(&a.map[g], g ? a.v : a.k, static_cast<uint64_t>(a.hkv) * kD,
+                     static_cast<uint64_t>(std::max<int64_t>(a.n_tokens, kB)));   // (used for whole tiles only)
     if (err != cudaSuccess) return err;
     const int64_t grid = std::min(static_cast<int64_t>(sms), most);
     read_tc_kernel<T, KB, VB, kLean><<<static_cast<unsigned>(grid), kRtThreads, kSmem, stream>>>(a);
@@ -691,7 +692,7 @@ cudaError_t launch_read_cfg(const ReadArgs& a, int sms, cudaStream_t stream) {
 }
 
 template <class T>
-cudaError_t launch_read_type(const ReadArgs& a, int k_bits, int v_bits, bool lean, int sms, cudaStream_t stream) {
+cudaError_t launch_read_type(ReadArgs& a, int k_bits, int v_bits, bool lean, int sms, cudaStream_t stream) {
   if (k_bits == 4 && v_bits == 2)
     return lean ? launch_read_cfg<T, 4, 2, true>(a, sms, stream) : launch_read_cfg<T, 4, 2, false>(a, sms, stream);
   if (k_bits == 4 && v_bits == 4 && !lean) return launch_read_cfg<T, 4, 4, false>(a, sms, stream);
