@@ -14,10 +14,10 @@
 //   fp32         read_kernel: thread t decodes token t's 128 channels and rotates them in
 //                registers (seven butterfly stages). The tensor core adds with fewer bits than fp32 has.
 // Memory bound: 7 KB read, 32 KB written an item (fp16, k4v2).
-// 16 sequences of 16384 tokens, 8 kv-heads, fp16 out: 396 us, 3.3 TB/s of 1.31 GB (49 % of a plain
-// copy's rate; the registers' transform took 443). No part dominates: of the 16-bit kernel's time the
-// stores are worth 25 %, the staging of rows, the signs and the preparation 15 % each, the products 4 %;
-// 16 warps an item instead of 8 (two blocks an SM) took 410.
+// 16 sequences of 16384 tokens, 8 kv-heads, fp16 out: 330 us, 4.0 TB/s of 1.31 GB (58 % of a plain
+// copy's rate, five bytes of six written; the registers' transform took 443). Without the front's work
+// 266, without the products 3 less: operands and rows contend for shared memory. Two teams at the front
+// took 333, two at the back 358 (72 registers a thread); rows stored by threads instead of by boxes 372.
 //
 // Items are found on the device: a warp walks the sequences 32 at a time (one a lane, their
 // tile counts scanned by shuffles) and takes every n-th item, so a ragged batch costs no
