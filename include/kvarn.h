@@ -435,7 +435,7 @@ KVARN_API kvarn_status kvarn_tree_attention(const uint16_t* q, const uint16_t* k
  *                 A sequence with n(s) outside 0..min(max_accept, 128) appends nothing
  *                 and raises KVARN_FLAG_BAD_LENGTH; one with a negative length appends
  *                 nothing and keeps its seq_lens_out.
- *   max_accept    row length of accepted, >= 0.
+ *   max_accept    row length of accepted (0 where it is NULL).
  *   seq_lens_out  int32 [n_seqs] or NULL: receives L + n(s). Must not alias seq_lens.
  * A completed tile whose block does not exist is dropped and flagged, as in
  * kvarn_append_decode. k_new and v_new must not overlap the workspace.

@@ -376,8 +376,8 @@ def kvarn_append_tokens(k_new, v_new, cu_tokens, seq_lens, seq_lens_out, block_t
     rows = n * meta.num_kv_heads * HEAD_DIM
     width = 0
     if accepted is not None:
-        if accepted.dim() != 2 or accepted.shape[0] != n_seqs:
-            raise ValueError(f"accepted must be [{n_seqs}, max_accept], got {list(accepted.shape)}")
+        if accepted.dim() != 2 or accepted.shape[0] != n_seqs or accepted.shape[1] < 1:
+            raise ValueError(f"accepted must be [{n_seqs}, max_accept >= 1], got {list(accepted.shape)}")
         width = int(accepted.shape[1])
     args = (_ptr(k_new, "k_new", f16, rows), _ptr(v_new, "v_new", f16, rows),
             _ptr(cu_tokens, "cu_tokens", i32, n_seqs + 1), n, _ptr(accepted, "accepted", i32),

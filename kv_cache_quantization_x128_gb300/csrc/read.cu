@@ -91,7 +91,7 @@ struct ReadItem {
 };
 // Items first, first + stride, .. of all; the warp calls and answers together.
 struct ReadCursor {
-  int64_t item, base, total, incl, mine;   // base: items of the sequences before this round's 32
+  int64_t item, base, total, incl, mine;   // base: items of the sequences before the current 32
   ReadRange rg;
   int s0;
   __device__ explicit ReadCursor(int64_t first) : item(first), base(0), total(0), incl(0), mine(0), rg{0, 0, 0, 0}, s0(-32) {}

@@ -31,12 +31,12 @@
 // rotated back by one more product, with the +-1 Hadamard matrix as A.
 //
 // Measured (fp16 out, k4v2, 64 q-heads over 8 kv-heads): 64 sequences of 16384 tokens with 8
-// drafted 865 us, 1.1 TB/s of records and 318 TFLOP/s of 275 GFLOP (the pairs double what the
-// tensor core does). Bound by instruction issue: 138 M warp instructions a 256 (sequence,
-// kv-head) x 128 tiles at 2 a cycle and SM, the tensor pipe 31 % busy, DRAM 14 %. Left out in
-// turn, the fold is worth 22 % of the time, p's writing 5 %, the softmax 8 %, the conversions of
-// codes 3 and 2 %, the accumulation 3 %: no part is waited for, all are issued. Slower were one
-// warp of 17 that issues all products (registers capped at 96: 1603 us), the fold one tile ahead
+// drafted 870 us, 1.1 TB/s of records and 316 TFLOP/s of 275 GFLOP (the pairs double what the
+// tensor core does). Bound by instruction issue: 8.4 K warp instructions a tile of 64 rows at 2.0 a
+// cycle and SM, shared memory 47 % and the tensor pipe 32 % busy, DRAM 14 %. Left out in turn, the
+// fold is worth 22 % of the time, p's writing 5 %, the softmax 8 %, the conversions of codes 3 and
+// 2 %, the accumulation 3 %: no part is waited for, all are issued. Slower were one warp of 17
+// that issues all products (registers capped at 96: 1603 us), the fold one tile ahead
 // (982), and the next keys' conversion under PV (922).
 #include <cuda_runtime.h>
 
@@ -54,8 +54,9 @@ constexpr int kTreeIssuer = 7;         // the warp of a team that issues its UMM
 constexpr int kTreeStages = 2;
 constexpr int kTreeMaxCtas = 160;      // sizes the scratch
 constexpr int kTreeMaxTeams = 3;
-// Units of 32 rows: three teams, 80 registers a thread, accumulators in registers. Units of 64
-// rows: two teams, 128 registers, accumulators in TMEM (32 of them a thread would spill).
+// Units of 32 rows: three teams, 80 registers a thread, accumulators in registers (4 sequences of
+// 131072 tokens, 4 drafted: 317 us; two teams of 128 registers 321). Units of 64 rows: two teams,
+// 128 registers, accumulators in TMEM (32 of them a thread would spill).
 __host__ __device__ constexpr int tree_teams(int r) { return r == 32 ? 3 : 2; }
 // TMEM columns of a team: the key and value operands, S and O (O is written once S has been
 // read), and for 64 rows the accumulator.

@@ -222,3 +222,15 @@ def test_python_checks(kv):
     with pytest.raises(ValueError):
         kv._dtype_code(torch.zeros(1, dtype=torch.float64), "q")
     assert kv._heads(torch.zeros(5, 384).unflatten(1, (3, 128))[:, 1:2], "k", 5, 1, torch.float32) == 384
+
+
+@pytest.mark.parametrize("shape", [(2, 0), (3, 4), (2,)])
+def test_python_refuses_rows_of_accepted_that_are_none(shape):
+    torch = pytest.importorskip("torch")
+    import kv_cache_quantization_x128_gb300 as kv
+    i32 = lambda *n: torch.zeros(*n, dtype=torch.int32)
+    k = torch.zeros(4, 2, 128, dtype=torch.float16)
+    ws = torch.zeros(2, 2, 2, 128, 128, dtype=torch.float16)
+    with pytest.raises(ValueError, match="accepted must be"):
+        kv.kvarn_append_tokens(k, k, i32(3), i32(2), i32(2), i32(2, 1), ws, torch.zeros(1, dtype=torch.uint8),
+                               kv.make_meta(2, 2, 2, 1), accepted=i32(*shape), n_accepted=i32(2))
