@@ -450,8 +450,9 @@ KVARN_API kvarn_status kvarn_append_tokens(const uint16_t* k_new, const uint16_t
  * Cached tokens back as plain rows: tokens first[s] .. first[s] + n - 1 of sequence s, n =
  * cu_tokens[s+1] - cu_tokens[s], into rows cu_tokens[s] .. of k_out and v_out (to hand
  * a sequence to another engine, to keep a prefix elsewhere, to check a cache). A packed
- * token is H (r c (code s + z)) in fp32, rounded once to `dtype`; a token of the partial
- * last tile is the workspace's. One launch, no scratch.
+ * token is H (r c (code s + z)), summed in fp32 and rounded once to `dtype` (for a 16-bit
+ * dtype the channels' scales enter the sums with 22 bits); a token of the partial last
+ * tile is the workspace's. One launch, no scratch.
  *   first         int32 [n_seqs] or NULL: 0.
  *   cu_tokens     int32 [n_seqs + 1], non-decreasing.
  *   n_tokens      rows of k_out and v_out (0 .. 2^31 - 1); rows behind it are not written.
