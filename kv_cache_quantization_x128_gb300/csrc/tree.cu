@@ -339,6 +339,10 @@ struct TreeTeam {
   using S = TreeSm<KB, VB, kLean, R>;
   static constexpr int CT = R / 2;               // rows (columns of the products) of a thread
   static constexpr float kKF = KB == 4 ? 8.f : 2.f, kVF = VB == 4 ? 8.f : 2.f;   // codes were converted to code / kKF
+  // beta is carried over this constant of its other operand. In units of S it is sum q_r r z / kKF over 128
+  // channels with |q_r| < 2^13 and |r z| < 2^7 (fold's scaling), so the operand stays below 128 2^13 2^7 / (kKF kBetaOne) =
+  // 2^15 for either width (fp16 ends at 65504); keys that are flat after the rotation, and a query along them, come near.
+  static constexpr float kBetaOne = 4096.f / kKF;
   // A token's value is s (code + u), u = z / s. Most of u goes into the operand: code + u^, u^ the
   // multiple of a power of two nearest to u that fp16 holds exactly with every code (2^-6 below
   // |u| = 16, twice that below 48, ..). The rest u - u^ goes in as one more product, whose A has the same value in every
@@ -456,11 +460,13 @@ struct TreeTeam {
     }
   }
 
-  // The constant operand of beta (512 at two K elements) and the zeros of its other one.
+  // The constant operand of beta (kBetaOne at two K elements) and the zeros of its other one.
   __device__ void init() {
+    constexpr uint32_t kOne2 = KB == 4 ? 0x60006000u : 0x68006800u;   // fp16 pair
+    static_assert(kBetaOne == (KB == 4 ? 512.f : 2048.f), "kOne2 is kBetaOne twice");
     for (int i = tt; i < 16; i += kTreeTeamThreads)
       reinterpret_cast<uint4*>(sm + S::kOne)[i] =
-          i < 2 ? make_uint4(0x60006000u, 0x60006000u, 0x60006000u, 0x60006000u) : make_uint4(0, 0, 0, 0);
+          i < 2 ? make_uint4(kOne2, kOne2, kOne2, kOne2) : make_uint4(0, 0, 0, 0);
     for (int i = tt; i < 128; i += kTreeTeamThreads) reinterpret_cast<uint4*>(sm + S::kExt)[i] = make_uint4(0, 0, 0, 0);
   }
 
@@ -579,7 +585,7 @@ struct TreeTeam {
     m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
     const float2 sc = tc_pow2_scale(m, 0);          // the largest r s into [1, 2)
     const float2 sc2 = make_float2(sc.x, sc.x);
-    const float zf = sc.x * (1.f / (kKF * 512.f));           // beta in the units of S, over its operand's 512
+    const float zf = sc.x * (1.f / (kKF * kBetaOne));        // beta in the units of S, over kBetaOne
     const float2 zf2 = make_float2(zf, zf);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
