@@ -1031,8 +1031,9 @@ struct TreeTeam {
       const int ft = f0 + t;
       const int ci = ft - c.ws;                  // index among the drafted tokens (negative: a workspace token)
       key.f = a.scale;
-      key.pk = (c.first + c.packed) * kB + ft;
       if (ci < 0) {
+        // behind all of the sequence's tiles, also those that a short block table leaves out
+        if (kMod) key.pk = a.seq_lens[c.s] / kB * kB + ft;
         key.seen = ~0u;
       } else if (ci < c.nt) {
 #pragma unroll

@@ -37,3 +37,38 @@ def test_keys_constant_in_one_channel(env, preset, sign, size, noise, q_size, q_
     q[..., 5] += q_size
     p["q"] = q.astype(np.float16)
     check(env, p)
+
+
+def _kept(p, keep, scores):
+    """The definition over one sequence and kv-head of which only the cached tokens `keep` are there, at their own
+    positions: scores(query row, head, keys, gaps) -> scores, -inf where masked."""
+    n, hq, _ = p["q"].shape
+    k, v = vo.cached_tokens(p["cache"], p["ws"], p["full_bt"][0], 0, p["lens"][0], 0)
+    out = np.zeros(p["q"].shape)
+    for t in range(n):
+        mine = [j for j in range(n) if p["words"][t] >> j & 1]
+        kk = np.concatenate([k[keep], p["k"][mine, 0].astype(np.float64)])
+        vv = np.concatenate([v[keep], p["v"][mine, 0].astype(np.float64)])
+        gap = int(p["pos"][t]) - np.concatenate([keep, p["pos"][mine].astype(np.int64)])
+        for m in range(hq):
+            x = scores(p["q"][t, m].astype(np.float64), m, kk, gap)
+            if np.isfinite(x).any():
+                w = np.exp(x - x.max())
+                out[t, m] = w / w.sum() @ vv
+    return out
+
+
+@pytest.mark.parametrize("score", [dict(window=200), dict(window=45), dict(slopes=[0.5, 0.02, 0.0, 0.11]),
+                                   dict(window=150, slopes=[0.01, 0.3, 0.0, 0.05])])
+@pytest.mark.parametrize("t", [3, 17])
+def test_positions_behind_a_short_table(env, t, score):
+    """Of a sequence longer than its block table the tiles behind the table are left out; its workspace tokens keep
+    their positions."""
+    kv, _ = env
+    p = make([5 * 128 + 60], [t], 4, 1, seed=142)
+    p["full_bt"], p["bt"] = p["bt"], p["bt"][:, :2].copy()
+    got = run(env, p, expect=kv.FLAG_BAD_LENGTH, **score)
+    slopes, window = np.array(score.get("slopes", [0.0] * 4)), score.get("window", 1 << 40)
+    keep = np.concatenate([np.arange(256), np.arange(640, 700)])
+    want = _kept(p, keep, lambda q, m, k, gap: np.where(gap < window, k @ q / np.sqrt(128) - slopes[m] * gap, -np.inf))
+    assert_decode_close(got, want)
