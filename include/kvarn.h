@@ -171,7 +171,7 @@ typedef struct {
   int64_t v_stride;
 } kvarn_rope;
 
-/* How kvarn_tree_attention turns q.k into a score. */
+/* How kvarn_tree_attention turns q.k into a score. scale and softcap are not subnormal. */
 typedef struct {
   float scale;          /* factor of q.k; 0: 1/sqrt(128)                               */
   float softcap;        /* > 0: scaled score x -> softcap * tanh(x / softcap); 0: none */

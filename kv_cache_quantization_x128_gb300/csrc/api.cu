@@ -25,6 +25,13 @@ __attribute__((format(printf, 2, 3))) kvarn_status fail(kvarn_status st, const c
   return st;
 }
 
+bool subnormal(float x) {
+  uint32_t u;
+  std::memcpy(&u, &x, sizeof(u));
+  u &= 0x7fffffffu;
+  return u != 0 && u < 0x00800000u;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 kvarn_status check_meta(const kvarn_meta* m) {
@@ -324,6 +331,8 @@ kvarn_status kvarn_tree_attention(const uint16_t* q, const uint16_t* k_new, cons
   if (score != nullptr) sc = *score;
   if (!(sc.scale >= 0.0f) || !(sc.scale <= 3.0e38f)) return fail(KVARN_EINVAL, "score scale must be finite and >= 0");
   if (!(sc.softcap >= 0.0f) || !(sc.softcap <= 3.0e38f)) return fail(KVARN_EINVAL, "softcap must be finite and >= 0");
+  // (a host that flushes subnormal numbers to 0 would read them as "none")
+  if (subnormal(sc.scale) || subnormal(sc.softcap)) return fail(KVARN_EINVAL, "score scale and softcap must not be subnormal");
   if (sc.window < 0) return fail(KVARN_EINVAL, "window must be >= 0 (got %lld)", (long long)sc.window);
   if (sc.reserved != 0) return fail(KVARN_EINVAL, "score reserved must be 0");
   if (sc.scale == 0.0f) sc.scale = 0.088388347648318440f;
