@@ -45,6 +45,7 @@
 #include "decode_tc.cuh"
 #include "kvarn_codes.cuh"
 #include "kvarn_launch.h"
+#include "tree_unit.cuh"
 
 namespace kvarn {
 namespace {
@@ -379,12 +380,13 @@ struct TreeTeam {
   float acc[R == 32 ? CT : 1], lsum[CT];
   float qinv;                                    // 2^-e of the stored q_r
   uint32_t qph, pph;
-  bool ok;
+  uint32_t issued, used;                         // packed tiles: copies started (thread 0), taken
+  bool ok;                                       // no wait of the thread has run out; the team's only where a barrier agreed on it
   bool row_set;                                  // thread tt < R: row tt has seen a key
   bool pending;                                  // some row of the unit has not (the team agrees)
 
   __device__ TreeTeam(const TreeArgs& a_, uint8_t* sm_, uint32_t tm_, int team)
-      : a(a_), sm(sm_), tm(tm_), bar_id(1 + 2 * team), qinv(1.f), qph(0), pph(0), ok(true), row_set(false), pending(true) {
+      : a(a_), sm(sm_), tm(tm_), bar_id(1 + 2 * team), qinv(1.f), qph(0), pph(0), issued(0), used(0), ok(true), row_set(false), pending(true) {
     tt = static_cast<int>(threadIdx.x) - team * kTreeTeamThreads;
     t = tt & 127;
     half = tt >> 7;
@@ -998,9 +1000,9 @@ struct TreeTeam {
     return issued;
   }
 
-  // One item: packed tile `ti` in stage used % kTreeStages, or the fresh tile at f0. False
-  // after a wait that timed out.
-  __device__ bool item(bool fresh, int ti, int f0, uint32_t used, uint32_t& issued) {
+  // One item: packed tile `ti` in stage used % kTreeStages, or the fresh tile at f0. False where the
+  // team agreed that a wait has run out; the wait for the last product counts at the next agreement.
+  __device__ bool item(bool fresh, int ti, int f0) {
     bool valid = true, wide = false;
     float cs = 1.f, cw = 0.f, rv = 1.f, cmax = 1.f;
     Keys key{0.f, 0, 0u, fresh};
@@ -1157,10 +1159,18 @@ struct TreeTeam {
     return true;
   }
 
+  // The steps of tree_unit.
+  __device__ bool packed_item(int ti) {
+    const bool go = item(false, ti, 0);
+    ++used;
+    return go;
+  }
+  __device__ bool fresh_item(int ti) { return item(true, 0, (ti - cur().packed) * kB); }
+  __device__ bool agreed() { return ok = named_bar_and(bar_id, kTreeTeamThreads, ok); }
+
   // Items [gb, ge).
   __device__ void run(int64_t gb, int64_t ge, int64_t team) {
     if (gb >= ge) return;
-    uint32_t issued = 0, used = 0;             // packed tiles: copies started (thread 0), taken
     if (tt == 0) {
       TreeCursor c;
       tree_locate<R>(a, gb, c);
@@ -1172,20 +1182,12 @@ struct TreeTeam {
     bar();
     for (int64_t left = ge - gb; left > 0;) {  // a unit
       const TreeCursor& c = cur();
-      int ti = c.ti;
-      const int packed = c.packed;
+      const int ti = c.ti;
       const int end = static_cast<int>(min(static_cast<int64_t>(c.items), ti + left));
       left -= end - ti;
+      const int last = min(c.packed, end);
       enter();
-      const int last = min(packed, end);
-      bool rotated = ti < last;                // acc will hold rotated channels
-      for (; ti < last && ok; ++ti, ++used) ok = item(false, ti, 0, used, issued) && ok;
-      if (!ok) break;
-      if (rotated && !unrotate()) break;
-      for (; ti < end && ok; ++ti) ok = item(true, 0, (ti - packed) * kB, used, issued) && ok;
-      if (!ok) break;
-      ok = named_bar_and(bar_id, kTreeTeamThreads, ok);
-      if (!ok) break;
+      if (!tree_unit(*this, ti, last, end)) break;
       flush(team + (static_cast<int64_t>(c.s) * a.hkv + c.h) * a.max_units + c.u);
       if (tt == 0 && left > 0) tree_next_unit<R>(a, cur());
       bar();
