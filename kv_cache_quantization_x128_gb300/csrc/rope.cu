@@ -217,6 +217,7 @@ __device__ __forceinline__ void rope_copy(const T* src, uint16_t* dst, int heads
 template <class T, bool kInter>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const RopeArgs a) {
   __shared__ unsigned long long turn[64];                      // inv_freq / (2 pi), 2^64 to a turn
+  __shared__ float off[64];                                    // 0; NaN where inv_freq is not finite: so are its angles, at any position
   __shared__ __align__(16) float2 cs[kRopeWarps][64];          // (cos, sin) of a warp's token
   __shared__ float ws[2][kD];                                  // norm weights of q and k
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = lane & 7;
@@ -224,6 +225,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const RopeArgs a)
   const bool rotate = a.inv_freq != nullptr;
   if (rotate && tid < half) {
     double f = static_cast<double>(a.inv_freq[tid]) * 0.15915494309189535;   // 1 / (2 pi)
+    off[tid] = static_cast<float>(f - f);
     f -= floor(f);
     turn[tid] = f < 1.0 ? static_cast<unsigned long long>(f * 18446744073709551616.0) : 0ull;
   }
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const RopeArgs a)
           const unsigned long long p = static_cast<unsigned long long>(pos) * turn[f];
           float sn, cn;
           sincospif(static_cast<float>(static_cast<int>(p >> 32)) * 4.656612873077393e-10f, &sn, &cn);   // 2^-31: half turns
-          cs[warp][f] = make_float2(cn, sn);
+          cs[warp][f] = make_float2(cn + off[f], sn + off[f]);
         }
       }
       __syncwarp();
