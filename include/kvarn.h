@@ -166,7 +166,8 @@ typedef struct {
   int32_t rotary_dim;   /* rotated channels of a head, the first ones: 16, 32, 64, 128 */
   int32_t interleaved;  /* 0: pairs (i, i + rotary_dim/2); 1: pairs (2i, 2i + 1)       */
   float norm_eps;       /* added to the mean square, in (0, 1)                         */
-  int64_t q_stride;     /* elements between tokens' rows; whole multiples of 16 bytes  */
+  int64_t q_stride;     /* elements between tokens' rows, multiples of 16 bytes (not
+                           looked at for a single token) */
   int64_t k_stride;
   int64_t v_stride;
 } kvarn_rope;

@@ -281,8 +281,8 @@ kvarn_status kvarn_qk_norm_rope(const void* q, const void* k, const void* v, con
   const int64_t widths[3] = {static_cast<int64_t>(meta->num_q_heads) * KVARN_HEAD_DIM,
                              static_cast<int64_t>(meta->num_kv_heads) * KVARN_HEAD_DIM,
                              static_cast<int64_t>(meta->num_kv_heads) * KVARN_HEAD_DIM};
-  for (int i = 0; i < (v != nullptr ? 3 : 2); ++i) {
-    if (n_tokens > 1 && strides[i] < widths[i])
+  for (int i = 0; i < (v != nullptr ? 3 : 2) && n_tokens > 1; ++i) {   // (a single row's stride is not used)
+    if (strides[i] < widths[i])
       return fail(KVARN_EINVAL, "the row stride of %c is smaller than a row (%lld)", "qkv"[i], (long long)strides[i]);
     if (strides[i] % piece != 0)
       return fail(KVARN_EALIGN, "the row stride of %c must be a multiple of 16 bytes (%lld elements)", "qkv"[i],

@@ -39,3 +39,19 @@ def test_frequencies_that_are_no_numbers(env, rotary, bad, interleaved):
             assert bool(torch.isnan(g[..., hit]).all()), value
             assert torch.equal(g[..., ~hit], w[..., ~hit])
         assert torch.equal(got[2], v)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16", "float32"])
+def test_one_row_of_any_stride(env, dtype):
+    """The stride between rows of a single row is no stride: tensors may carry any number there."""
+    kv, torch = env
+    t = getattr(torch, dtype)
+    q, k, v = (torch.randn(1, h, 128, device="cuda").to(t) for h in (6, 2, 2))
+    meta = kv.make_meta(2, 6, 1, 1)
+    outs = [[torch.empty(1, h, 128, dtype=torch.float16, device="cuda") for h in (6, 2, 2)] for _ in range(2)]
+    kv.kvarn_qk_norm_rope(q, k, v, None, *outs[0], meta)
+    odd = [x.as_strided(x.shape, (s, 128, 1)) for x, s in zip((q, k, v), (1, 7, 130))]
+    kv.kvarn_qk_norm_rope(*odd, None, *outs[1], meta)
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    none = [x.as_strided((0,) + x.shape[1:], (1, 128, 1)) for x in (q, k, v)]
+    kv.kvarn_qk_norm_rope(*none, None, *[x[:0] for x in outs[1]], meta)
