@@ -23,8 +23,9 @@
 //           p' = p c^V s^V 2^e as fp16 hi + lo, u = z^V / s^V of the token
 //           acc += r^V_channel O
 // The hi + lo pairs carry q' and p' to ~22 bits: rounded once to fp16, scores of keys with
-// outlier channels are off by some 1e-3 and so are the outputs. The tensor core drops
-// subnormal fp16 operands, hence the powers of two.
+// outlier channels are off by some 1e-3 and so are the outputs. The powers of two leave the pairs fp16's range, down to its
+// subnormal steps (the products keep them): q' to 2^-37 of the unit's largest, so that a row of q loses bits only
+// beside one whose scores are above some 10^7; p' to 2^-30 of the running max's, of which 131072 tokens together are 1e-4.
 // The running max is lazy: a tile rescales only when a score exceeds it by more than
 // kTau, so that most tiles need no reduction over tokens (lanes); p stays <= 2^kTau.
 // Before fresh tiles, or before a record is written, the accumulator of the packed part is
@@ -367,6 +368,9 @@ struct TreeTeam {
   // channels with |q_r| < 2^13 and |r z| < 2^7 (fold's scaling), so the operand stays below 128 2^13 2^7 / (kKF kBetaOne) =
   // 2^15 for either width (fp16 ends at 65504); keys that are flat after the rotation, and a query along them, come near.
   static constexpr float kBetaOne = 4096.f / kKF;
+  // What fp16 leaves of it goes in 2^11 larger (below 2^14), over a constant as much smaller: a row of q far below the
+  // unit's largest, whose power of two it shares, keeps its bits (10^7 below: scores off by 1e-2 of themselves otherwise).
+  static constexpr float kBetaLo = 2048.f;
   // A token's value is s (code + u), u = z / s. Most of u goes into the operand: code + u^, u^ the
   // multiple of a power of two nearest to u that fp16 holds exactly with every code (2^-6 below
   // |u| = 16, twice that below 48, ..). The rest u - u^ goes in as one more product, whose A has the same value in every
@@ -485,13 +489,14 @@ struct TreeTeam {
     }
   }
 
-  // The constant operand of beta (kBetaOne at two K elements) and the zeros of its other one.
+  // The constant operand of beta (kBetaOne for the high part, kBetaOne / kBetaLo for the low one, at K elements 0
+  // and 1) and the zeros of its other one.
   __device__ void init() {
-    constexpr uint32_t kOne2 = KB == 4 ? 0x60006000u : 0x68006800u;   // fp16 pair
-    static_assert(kBetaOne == (KB == 4 ? 512.f : 2048.f), "kOne2 is kBetaOne twice");
+    constexpr uint32_t kHi2 = KB == 4 ? 0x60006000u : 0x68006800u, kLo2 = KB == 4 ? 0x34003400u : 0x3C003C00u;   // fp16 pairs
+    static_assert(kBetaOne == (KB == 4 ? 512.f : 2048.f) && kBetaLo == 2048.f, "the constants as fp16");
     for (int i = tt; i < 16; i += kTreeTeamThreads)
       reinterpret_cast<uint4*>(sm + S::kOne)[i] =
-          i < 2 ? make_uint4(kOne2, kOne2, kOne2, kOne2) : make_uint4(0, 0, 0, 0);
+          i == 0 ? make_uint4(kHi2, kHi2, kHi2, kHi2) : i == 1 ? make_uint4(kLo2, kLo2, kLo2, kLo2) : make_uint4(0, 0, 0, 0);
     for (int i = tt; i < 128; i += kTreeTeamThreads) reinterpret_cast<uint4*>(sm + S::kExt)[i] = make_uint4(0, 0, 0, 0);
   }
 
@@ -655,7 +660,7 @@ struct TreeTeam {
       const __half h = __float2half_rn(b[0]);
       uint8_t* ext = sm + S::kExt + (r & 7) * 2;
       *reinterpret_cast<__half*>(ext + ((r >> 3) << 4)) = h;                                     // K element 0
-      *reinterpret_cast<__half*>(ext + 128 + (((r >> 3) ^ 1) << 4)) = __float2half_rn(b[0] - __half2float(h));   // 1
+      *reinterpret_cast<__half*>(ext + 128 + (((r >> 3) ^ 1) << 4)) = __float2half_rn((b[0] - __half2float(h)) * kBetaLo);   // 1
     }
     return sc.y;
   }

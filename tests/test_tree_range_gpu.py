@@ -72,3 +72,32 @@ def test_positions_behind_a_short_table(env, t, score):
     keep = np.concatenate([np.arange(256), np.arange(640, 700)])
     want = _kept(p, keep, lambda q, m, k, gap: np.where(gap < window, k @ q / np.sqrt(128) - slopes[m] * gap, -np.inf))
     assert_decode_close(got, want)
+
+
+def _extreme(preset, t, size, seed):
+    """Keys of `size` in the cache, the workspace and the drafted tokens, values of about 1."""
+    rng = np.random.default_rng(seed)
+    p = make([256 + 40], [t], 8, 1, preset, seed=seed)
+
+    def keys(*shape):
+        return (size * rng.standard_normal(shape + (128,))).clip(-6e4, 6e4).astype(np.float16)
+
+    p["cache"] = quantized(keys(2, 128), rng.standard_normal((2, 128, 128)), preset)
+    p["bt"] = np.array([[0, 1, -1]], np.int32)
+    p["ws"][0, 0, 0, :40], p["ws"][0, 0, 1, :40] = keys(40), rng.standard_normal((40, 128))
+    p["k"], p["v"] = keys(t, 1), rng.standard_normal((t, 1, 128)).astype(np.float16)
+    return p, rng
+
+
+@pytest.mark.parametrize("preset", ["k4v2", "k4v4", "k2v2", "k4v2l"])
+@pytest.mark.parametrize("t", [2, 4, 9])
+@pytest.mark.parametrize("big,small,size", [(3e3, 3e-2, 1e2), (3e4, 3e-2, 1e2), (3e4, 3e-3, 1e3)])
+def test_query_rows_far_apart(env, preset, t, big, small, size):
+    """One row of q up to ten million times the others of its sequence and kv-head, and keys that give the others
+    scores of about 3."""
+    p, rng = _extreme(preset, t, size, 145)
+    q = small * rng.standard_normal((t, 8, 128))
+    q[t // 2, 3] = big / 3 * np.clip(rng.standard_normal(128), -3, 3)
+    p["q"] = q.astype(np.float16)
+    check(env, p)
+    check(env, p, window=250)
