@@ -85,6 +85,7 @@ struct TreeArgs {
   int n_teams, max_units;   // teams; units of a (sequence, kv-head) at most
   int group_inv;            // ceil(2^16 / group)
   float scale;              // of q.k, times log2(e)
+  float none;               // -0: a product that a sum follows is fma(x, y, -0), which the compiler cannot contract with it
   float cap, cap_two;       // cap times log2(e) (0: none), and 2 log2(e) over that
 };
 
@@ -783,8 +784,9 @@ struct TreeTeam {
     uint32_t seen;     // fresh tiles: bit i, whether the thread's i-th row attends it
     bool fresh;
   };
-  // Scores of 16 rows relative to their running max: x = f S (then cap and bias) - max; masked
-  // keys -inf.
+  // Scores of 16 rows relative to their running max: x = f S (then cap and bias) - max; masked keys -inf. f S is rounded
+  // before the maximum is taken off, as it was for that: the largest is 0, however large it is. kWhole: f S without it.
+  template <bool kWhole = false>
   __device__ void scores(int ch, const Keys& k, float (&x)[16]) {
     read16(ch, x);
     const float2 f2 = make_float2(k.f, k.f);
@@ -797,10 +799,11 @@ struct TreeTeam {
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
       const int col = CT * half + 16 * ch + i;
-      const float4 m = *reinterpret_cast<const float4*>(mrow() + col);
+      const float4 m = kWhole ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(mrow() + col);
       if (!kMod) {
-        const float2 u = __ffma2_rn(make_float2(x[i], x[i + 1]), f2, make_float2(m.x, m.y));
-        const float2 v = __ffma2_rn(make_float2(x[i + 2], x[i + 3]), f2, make_float2(m.z, m.w));
+        const float2 none = make_float2(a.none, a.none);
+        const float2 u = __fadd2_rn(__ffma2_rn(make_float2(x[i], x[i + 1]), f2, none), make_float2(m.x, m.y));
+        const float2 v = __fadd2_rn(__ffma2_rn(make_float2(x[i + 2], x[i + 3]), f2, none), make_float2(m.z, m.w));
         x[i] = u.x; x[i + 1] = u.y; x[i + 2] = v.x; x[i + 3] = v.y;
       } else {
         const float mm[4] = {m.x, m.y, m.z, m.w};
@@ -830,18 +833,19 @@ struct TreeTeam {
 #pragma unroll
     for (int ch = 0; ch < CT / 16; ++ch) {
       float x[16];
-      scores(ch, k, x);
+      scores<true>(ch, k, x);
       float m = tree_reduce<true>(x, lane);
       if (lane < 16) part()[warp * CT + 16 * ch + lane] = valid ? m : -INFINITY;
     }
     bar();
     if (tt < R) {                                   // row tt: its half's four warps
       const float* p = part() + 4 * (tt / CT) * CT + tt % CT;
-      float d = fmax3f(fmaxf(p[0], p[CT]), p[2 * CT], p[3 * CT]);   // relative to the running max
-      if (row_set || d == -INFINITY) d = fmaxf(d, 0.f);     // a row's first max may be any
+      const float tile = fmax3f(fmaxf(p[0], p[CT]), p[2 * CT], p[3 * CT]), old = -mrow()[tt];
+      float top = tile;                            // a row's first max may be any
+      if (row_set || tile == -INFINITY) top = fmaxf(tile, old);
       else row_set = true;
-      gam()[tt] = d;
-      mrow()[tt] -= d;
+      gam()[tt] = top - old;
+      mrow()[tt] = -top;
       const bool miss = __any_sync(0xffffffffu, !row_set);
       if (lane == 0) small()[8 + warp] = miss ? 1.f : 0.f;
     }
@@ -1382,6 +1386,7 @@ cudaError_t launch_tree(const uint16_t* q, const uint16_t* k_new, const uint16_t
   a.n_seqs = n_seqs; a.max_tree = max_tree; a.hkv = hkv; a.group = group; a.max_blocks = max_blocks;
   a.window = score.window;
   a.scale = score.scale * kLog2e;
+  a.none = -0.f;
   if (score.softcap > 0.f) {                     // (2^125 for every larger one, which leaves scores as they are too)
     a.cap = std::min(score.softcap * kLog2e, 4.2535296e+37f);
     a.cap_two = 2.f * kLog2e / a.cap;

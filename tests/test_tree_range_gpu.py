@@ -101,3 +101,20 @@ def test_query_rows_far_apart(env, preset, t, big, small, size):
     p["q"] = q.astype(np.float16)
     check(env, p)
     check(env, p, window=250)
+
+
+@pytest.mark.parametrize("preset", ["k4v2", "k2v2"])
+@pytest.mark.parametrize("t", [2, 4, 9, 40])
+@pytest.mark.parametrize("lens", [296, 256, 40, 0])
+def test_scores_beyond_what_is_added_exactly(env, preset, t, lens):
+    """Scores of 10^8 to 10^9, whose neighbours in fp32 are 64 apart: the largest key of a row takes all its weight."""
+    p, rng = _extreme(preset, t, 2e4, 146)
+    p["lens"] = np.array([lens], np.int32)
+    p["q"] = (5e4 / 3 * np.clip(rng.standard_normal((t, 8, 128)), -3, 3)).astype(np.float16)
+    if lens % 128 == 0:
+        p["ws"][:] = 0
+    elif lens < 128:
+        p["bt"][:] = -1
+    p["pos"] = (lens + np.arange(t)).astype(np.int32)
+    check(env, p)
+    check(env, p, window=250)
