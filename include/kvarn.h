@@ -258,6 +258,12 @@ KVARN_API kvarn_status kvarn_append_decode(const uint16_t* k_new, const uint16_t
  * environment variable KVARN_DECODE_SPLIT=tc (read on every call) the k4v2
  * presets run their split phase on the tcgen05 kernel instead of the warp-level
  * one (same results within the decode tolerance; measured slower).
+ * Range: the warp-level kernel (and kvarn_serve_step) carries q_r r s and p c s as
+ * pairs of fp16 numbers as they are. Tensors whose mean is several times their spread
+ * drive the normalisation's r and c far apart; where a value tile's c s is above 65504
+ * its rows are not finite, where a key tile's r s is below 2^-14 scores lose bits (2e-2 at
+ * 2^-19). The tcgen05 split, kvarn_prefill_attention and kvarn_tree_attention scale both
+ * and have no such limit.
  */
 KVARN_API kvarn_status kvarn_decode_attention(const uint16_t* q, const uint8_t* cache,
                                     const uint16_t* workspace, const int32_t* block_tables,
@@ -410,7 +416,10 @@ KVARN_API size_t kvarn_tree_scratch_bytes(const kvarn_meta* meta, int32_t n_seqs
  *   scratch       device buffer of >= kvarn_tree_scratch_bytes(meta, n_seqs, max_tree);
  *                 calls that overlap on the GPU must not share it.
  * Packed tiles in a block outside [0, num_blocks) are not attended (KVARN_FLAG_BAD_BLOCK),
- * nor are those behind max_blocks_per_seq (KVARN_FLAG_BAD_LENGTH).
+ * nor are those behind max_blocks_per_seq (KVARN_FLAG_BAD_LENGTH; workspace tokens keep
+ * their positions).
+ * Scores, weights and sums are fp32; rotated queries times their key scales and weights
+ * times their value scales enter the products as pairs of fp16 numbers (22 bits).
  */
 KVARN_API kvarn_status kvarn_tree_attention(const uint16_t* q, const uint16_t* k_new, const uint16_t* v_new,
                                             const uint64_t* tree_mask, const int32_t* positions,

@@ -25,10 +25,10 @@
 // the running max by more than kTcTau (always on a unit's first tile), so most
 // tiles need no reduction over tokens, and p stays <= 2^kTcTau. The running sum is
 // kept per token slot and reduced when the team leaves a (sequence, kv-head).
-// The tensor core drops subnormal fp16 operands (measured: q' carried as is, its
-// lo parts subnormal, moved outputs by up to 4.5e-3), so q' (per head) and p' (per
-// tile) are scaled by powers of two that bring their largest element near 2^13
-// and the scale is taken out again in fp32.
+// q' (per head) and p' (per tile) are scaled by powers of two that bring their largest
+// element near 2^13, and the scale is taken out again in fp32: carried as they are, what
+// fp16 leaves of the smaller elements (subnormal, in steps of 2^-24) moved outputs by up
+// to 4.5e-3, and large scales overflow.
 // The issuing warp's lane 0 issues every team's UMMAs (a thread issuing UMMAs
 // stalls while the tensor core is busy, so no team thread does) in the order the
 // teams become ready, polling their mbarriers.

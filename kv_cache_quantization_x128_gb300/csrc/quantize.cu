@@ -413,7 +413,7 @@ __global__ void __maxnreg__(128)
   uint8_t* rank = smem + S::kOffRank;
   int n_mine = 0;
   if constexpr (Src::kTail) {
-    // most steps complete no tile: a block without one is done once its rows are written
+    // a block whose items complete no tile (most blocks of most steps) is done once its rows are written
     n_mine = src.scatter_all(tid, rank);
     if (src.first_item(tid & 31, rank, n_mine) >= src.n_items) return;
   }

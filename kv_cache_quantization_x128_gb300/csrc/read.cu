@@ -17,7 +17,8 @@
 // 16 sequences of 16384 tokens, 8 kv-heads, fp16 out: 330 us, 4.0 TB/s of 1.31 GB (58 % of a plain
 // copy's rate, five bytes of six written; the registers' transform took 443). Without the front's work
 // 266, without the products 3 less: operands and rows contend for shared memory. Two teams at the front
-// took 333, two at the back 358 (72 registers a thread); rows stored by threads instead of by boxes 372.
+// took 333, two at the back 358 (72 registers a thread); rows stored by threads instead of by boxes 372. (24 to 36 bytes of
+// spill stores at 96 registers.) fp32 out: 604 us of 2.38 GB, 58 %; k4v4 548 us, 66 % (60 bytes of spills but for k4v4).
 //
 // Items are found on the device: a warp walks the sequences 32 at a time (one a lane, their
 // tile counts scanned by shuffles) and takes every n-th item, so a ragged batch costs no

@@ -26,17 +26,20 @@
 // outlier channels are off by some 1e-3 and so are the outputs. The powers of two leave the pairs fp16's range, down to its
 // subnormal steps (the products keep them): q' to 2^-37 of the unit's largest, so that a row of q loses bits only
 // beside one whose scores are above some 10^7; p' to 2^-30 of the running max's, of which 131072 tokens together are 1e-4.
+// Sums are fp32, in the tensor core's accumulators within a tile; exponentials, the cap's and the rows' divisions are
+// the approximate instructions (about 2^-22).
 // The running max is lazy: a tile rescales only when a score exceeds it by more than
 // kTau, so that most tiles need no reduction over tokens (lanes); p stays <= 2^kTau.
 // Before fresh tiles, or before a record is written, the accumulator of the packed part is
 // rotated back by one more product, with the +-1 Hadamard matrix as A.
 //
 // Measured (fp16 out, k4v2, 64 q-heads over 8 kv-heads): 64 sequences of 16384 tokens with 8
-// drafted 870 us, 1.1 TB/s of records and 316 TFLOP/s of 275 GFLOP (the pairs double what the
-// tensor core does). Bound by instruction issue: 8.4 K warp instructions a tile of 64 rows at 2.0 a
-// cycle and SM, shared memory 47 % and the tensor pipe 32 % busy, DRAM 14 %. Left out in turn, the
-// fold is worth 22 % of the time, p's writing 5 %, the softmax 8 %, the conversions of codes 3 and
-// 2 %, the accumulation 3 %: no part is waited for, all are issued. Slower were one warp of 17
+// drafted 873 us, 1.1 TB/s of records and 315 TFLOP/s of 275 GFLOP (the pairs double what the
+// tensor core does). No unit is at its limit: 8.4 K warp instructions a tile of 64 rows at 2.0 a
+// cycle and SM of 4, shared memory 47 % and the tensor pipe 32 % busy, DRAM 14 %; 16 warps an SM, whose phases wait
+// for one another. Left out in turn, the fold is worth 22 % of the time, p's writing 5 %, the softmax 8 %, the
+// conversions of codes 3 and 2 %, the accumulation 3 %. Spilled registers (128 / 192 bytes of stores / loads for 64
+// rows, 264 to 344 / 364 to 480 for 32 rows) are 1 % of the instructions. Slower were one warp of 17
 // that issues all products (registers capped at 96: 1603 us), the fold one tile ahead
 // (982), and the next keys' conversion under PV (922).
 #include <cuda_runtime.h>
@@ -57,8 +60,8 @@ constexpr int kTreeStages = 2;
 constexpr int kTreeMaxCtas = 160;      // sizes the scratch
 constexpr int kTreeMaxTeams = 3;
 // Units of 32 rows: three teams, 80 registers a thread, accumulators in registers (4 sequences of
-// 131072 tokens, 4 drafted: 317 us; two teams of 128 registers 321). Units of 64 rows: two teams,
-// 128 registers, accumulators in TMEM (32 of them a thread would spill).
+// 131072 tokens, 4 drafted: 316 us; two teams of 128 registers 321). Units of 64 rows: two teams,
+// 128 registers, accumulators in TMEM (32 more of them a thread would not fit).
 __host__ __device__ constexpr int tree_teams(int r) { return r == 32 ? 3 : 2; }
 // TMEM columns of a team: the key and value operands, S and O (O is written once S has been
 // read), and for 64 rows the accumulator.
