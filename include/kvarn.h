@@ -172,6 +172,16 @@ typedef struct {
   int64_t v_stride;
 } kvarn_rope;
 
+/* kvarn_qk_norm_rope_axes' axes. */
+#define KVARN_MAX_AXES 4
+typedef struct {
+  int32_t n_axes;           /* 1..4                                                      */
+  int32_t reserved;         /* 0 */
+  int64_t position_stride;  /* elements between the axes' rows of positions, >= n_tokens,
+                               or 0: the axes share one (not looked at for one axis)     */
+  uint8_t axis[64];         /* axis of each of the rotary_dim / 2 pairs, below n_axes     */
+} kvarn_axes;
+
 /* How kvarn_tree_attention turns q.k into a score. scale and softcap are not subnormal. */
 typedef struct {
   float scale;          /* factor of q.k; 0: 1/sqrt(128)                               */
@@ -270,6 +280,74 @@ KVARN_API kvarn_status kvarn_decode_attention(const uint16_t* q, const uint8_t* 
                                     const int32_t* seq_lens, int32_t n_seqs, uint16_t* out,
                                     void* scratch, size_t scratch_bytes,
                                     const kvarn_meta* meta, void* stream);
+
+/* Bytes of device scratch kvarn_decode_attention_weights needs: the decode's, and 64 bytes for
+ * each entry of weights (n_seqs * num_kv_heads * max_blocks_per_seq). 0 if an argument is invalid. */
+KVARN_API size_t kvarn_decode_weights_scratch_bytes(const kvarn_meta* meta, int32_t n_seqs);
+
+/*
+ * Decode attention that also accumulates each tile's attention weight, for eviction
+ * (kvarn_evict_tiles; a reading of this library, the pages are silent on it). out is
+ * kvarn_decode_attention's; with p_gj the softmax weight that q-head g gives token j,
+ *   weights[s][h][t] <- decay * weights[s][h][t] + sum of p_gj over kv-head h's q-heads and
+ *                       the tokens j of tile t (128 t .. 128 t + 127)
+ * for t = 0 .. ceil(L/128) - 1; entries behind them stay as they are. The workspace's tokens
+ * are tile floor(L/128), so a tile keeps what its tokens got there when it is quantized. With
+ * decay 1 the weights are plain sums; below 1 old steps fade; with 0 the entry is replaced (what it
+ * held is not looked at). Sums are fp32, in the same order at every call.
+ *   decay         in [0, 1], not subnormal.
+ *   weights       float [n_seqs][num_kv_heads][max_blocks_per_seq].
+ *   lse           float [n_seqs][num_q_heads] or NULL: ln of the sum of exp(score) over the
+ *                 attended tokens (-inf where there are none), to join the rows with
+ *                 attention over other tokens.
+ *   scratch       device buffer of >= kvarn_decode_weights_scratch_bytes(meta, n_seqs); calls that
+ *                 overlap on the GPU must not share it (nor weights).
+ * A tile that is not attended (its block outside [0, num_blocks)) gets weight 0 from the step; the
+ * workspace tokens' weight is dropped where floor(L/128) is not below max_blocks_per_seq. Other
+ * arguments, flags and launches are kvarn_decode_attention's; its limits of range do not
+ * hold here (q_r r s and p c s are scaled per head and tile before they become fp16 pairs),
+ * and KVARN_DECODE_SPLIT is not looked at.
+ */
+KVARN_API kvarn_status kvarn_decode_attention_weights(const uint16_t* q, const uint8_t* cache,
+                                                      const uint16_t* workspace, const int32_t* block_tables,
+                                                      const int32_t* seq_lens, int32_t n_seqs, float decay,
+                                                      float* weights, uint16_t* out, float* lse, void* scratch,
+                                                      size_t scratch_bytes, const kvarn_meta* meta, void* stream);
+
+/*
+ * Eviction of packed tiles by accumulated weight, per sequence and kv-head. Sequence s has n =
+ * floor(seq_lens[s] / 128) tiles; b = min(n, budgets[s]) stay (a negative budget: all): its first
+ * f = min(keep_first, b), its last l = min(keep_last, b - f), and the b - f - l of the others
+ * with the largest weights (equal ones: the lowest slot first; -0 is 0, a NaN is below
+ * everything). Workspace tokens are not touched. Each kv-head chooses for itself, and
+ * its records move, bit for bit, into the blocks of the first b entries of the block table:
+ *   - slots below f, and chosen ones below b - l, keep their record (it is not written: blocks
+ *     that sequences share there stay shared);
+ *   - chosen records of slots b - l .. n - l - 1, in order, fill the evicted slots below b - l;
+ *   - the last l records go to slots b - l .. b - 1, in order.
+ * So the last keep_last slots are always the latest tiles, while those between may change order, which
+ * attention over the cache does not see; calls that go by a cached token's position (window
+ * and slopes of kvarn_tree_attention, kvarn_read_tokens' ranges) then count slots.
+ * Entries b .. of the block table's row are free afterwards but for b itself, which
+ * the partial tile will fill. A sequence's blocks below must be its own but for those
+ * that stay in place, and no block may be in a row twice.
+ *   weights       float [n_seqs][num_kv_heads][max_blocks_per_seq].
+ *   weights_out   the same, or weights itself: the weights of the tiles that stay by their new
+ *                 slots, then entry n's (the partial tile's), then zeros.
+ *   seq_lens_out  int32 [n_seqs]: seq_lens[s] - 128 (n - b). Must not alias seq_lens.
+ *   budgets       int32 [n_seqs].
+ *   kept          int32 [n_seqs][num_kv_heads][max_blocks_per_seq], a permutation of a
+ *                 row's slots: the old slots of the b tiles that stay, by new slot; the n - b
+ *                 evicted slots, ascending; -1.
+ * A sequence longer than its block table (KVARN_FLAG_BAD_LENGTH), or with tiles to evict and a
+ * block outside [0, num_blocks) among its n (KVARN_FLAG_BAD_BLOCK), is left as it is: its
+ * lengths and weights are copied and its kept is 0 .. n - 1.
+ * Two launches (the choice; the copies, a programmatic dependent of it); no scratch.
+ */
+KVARN_API kvarn_status kvarn_evict_tiles(const float* weights, float* weights_out, const int32_t* seq_lens,
+                                         int32_t* seq_lens_out, const int32_t* block_tables, const int32_t* budgets,
+                                         int32_t n_seqs, int32_t keep_first, int32_t keep_last, int32_t* kept,
+                                         uint8_t* cache, const kvarn_meta* meta, void* stream);
 
 /*
  * One serving step in one launch: kvarn_append_decode (the new token of every
@@ -380,6 +458,22 @@ KVARN_API kvarn_status kvarn_qk_norm_rope(const void* q, const void* k, const vo
                                           const void* q_weight, const void* k_weight, const float* inv_freq,
                                           const int32_t* positions, int64_t n_tokens, uint16_t* q_out,
                                           uint16_t* k_out, uint16_t* v_out, const kvarn_meta* meta, void* stream);
+
+/*
+ * kvarn_qk_norm_rope for tokens with a position on each of several axes, such as time,
+ * height and width in images and video: pair i turns by
+ *   t = positions[axes->axis[i] * axes->position_stride + token] * inv_freq[i].
+ * Any assignment of pairs to axes is one of axes->axis: one section of pairs after the
+ * other, or dealt in turn. A token of text has the same position on every axis, and is then
+ * rotated as by kvarn_qk_norm_rope, to the bit. axes is a host pointer, read before the call
+ * returns; inv_freq is required; all else is kvarn_qk_norm_rope's.
+ *   positions     int32 [n_axes][position_stride], n_tokens of each row used.
+ */
+KVARN_API kvarn_status kvarn_qk_norm_rope_axes(const void* q, const void* k, const void* v, const kvarn_rope* rope,
+                                               const kvarn_axes* axes, const void* q_weight, const void* k_weight,
+                                               const float* inv_freq, const int32_t* positions, int64_t n_tokens,
+                                               uint16_t* q_out, uint16_t* k_out, uint16_t* v_out,
+                                               const kvarn_meta* meta, void* stream);
 
 /* The most new tokens of a sequence in one kvarn_tree_attention call. */
 #define KVARN_MAX_TREE 64

@@ -22,6 +22,7 @@ KVARN_OK, KVARN_EINVAL, KVARN_EUNSUPPORTED, KVARN_EALIGN, KVARN_ESCRATCH, KVARN_
 FLAG_BAD_SLOTS, FLAG_BAD_BLOCK, FLAG_BAD_LENGTH, FLAG_WAIT_TIMEOUT, FLAG_BAD_INDEX = 0x1, 0x2, 0x4, 0x8, 0x10
 KVARN_F16, KVARN_BF16, KVARN_F32 = range(3)
 KVARN_MAX_TREE = 64
+KVARN_MAX_AXES = 4
 KVARN_WAIT_MBARRIER, KVARN_WAIT_GRID = 0, 1
 
 # exported entry points and their C signatures (include/kvarn.h)
@@ -51,6 +52,11 @@ _SIGS = {
                                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                                ctypes.c_void_p]),
     "kvarn_qk_norm_rope": (ctypes.c_int, [ctypes.c_void_p] * 8 + [ctypes.c_int64] + [ctypes.c_void_p] * 5),
+    "kvarn_qk_norm_rope_axes": (ctypes.c_int, [ctypes.c_void_p] * 9 + [ctypes.c_int64] + [ctypes.c_void_p] * 5),
+    "kvarn_decode_weights_scratch_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_int32]),
+    "kvarn_decode_attention_weights": (ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_int32, ctypes.c_float]
+                                       + [ctypes.c_void_p] * 4 + [ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
+    "kvarn_evict_tiles": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int32] * 3 + [ctypes.c_void_p] * 4),
     "kvarn_tree_scratch_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32]),
     "kvarn_tree_attention": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32]
                              + [ctypes.c_void_p] * 6 + [ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
@@ -93,6 +99,15 @@ class KvarnRope(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
                 ("norm_eps", ctypes.c_float), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
                 ("v_stride", ctypes.c_int64)]
+
+
+_Pairs = ctypes.c_uint8 * 64
+
+
+class KvarnAxes(ctypes.Structure):
+    """Mirror of ``kvarn_axes``."""
+    _fields_ = [("n_axes", ctypes.c_int32), ("reserved", ctypes.c_int32), ("position_stride", ctypes.c_int64),
+                ("axis", _Pairs)]
 
 
 class KvarnScore(ctypes.Structure):
@@ -311,6 +326,22 @@ def _heads(t, name, n, heads, dtype):
     return row
 
 
+def _rope_args(q, k, v, q_out, k_out, v_out, meta, q_weight, k_weight, norm_eps, inv_freq, interleaved):
+    """The C arguments that the norm and rotation calls share: the rows up to their
+    kvarn_rope, and those behind it."""
+    import torch
+    n, hq, hkv = int(q.shape[0]), meta.num_q_heads, meta.num_kv_heads
+    f16 = torch.float16
+    rope = KvarnRope(_dtype_code(q, "q"), HEAD_DIM if inv_freq is None else 2 * inv_freq.numel(), int(bool(interleaved)),
+                     norm_eps, _heads(q, "q", n, hq, q.dtype), _heads(k, "k", n, hkv, q.dtype),
+                     0 if v is None else _heads(v, "v", n, hkv, q.dtype))
+    return ((q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(), ctypes.byref(rope)),
+            (_ptr(q_weight, "q_weight", q.dtype, HEAD_DIM), _ptr(k_weight, "k_weight", q.dtype, HEAD_DIM),
+             _ptr(inv_freq, "inv_freq", torch.float32), _ptr(q_out, "q_out", f16, n * hq * HEAD_DIM),
+             _ptr(k_out, "k_out", f16, n * hkv * HEAD_DIM),
+             None if v is None else _ptr(v_out, "v_out", f16, n * hkv * HEAD_DIM), ctypes.byref(meta)))
+
+
 def kvarn_qk_norm_rope(q, k, v, positions, q_out, k_out, v_out, meta: KvarnMeta, q_weight=None, k_weight=None,
                        norm_eps: float = 1e-6, inv_freq=None, interleaved: bool = False, stream=None):
     """Per-head norm and rotation of projected rows. q [n, Hq, 128], k and v [n, Hkv, 128]
@@ -318,19 +349,78 @@ def kvarn_qk_norm_rope(q, k, v, positions, q_out, k_out, v_out, meta: KvarnMeta,
     [128] of the same type or None (no norm); positions int32 [n]; inv_freq float32
     [rotary_dim / 2] or None (no rotation); outputs fp16, contiguous. v and v_out may be None."""
     import torch
-    n, hq, hkv = int(q.shape[0]), meta.num_q_heads, meta.num_kv_heads
-    f16 = torch.float16
-    rope = KvarnRope(_dtype_code(q, "q"), HEAD_DIM if inv_freq is None else 2 * inv_freq.numel(), int(bool(interleaved)),
-                     norm_eps, _heads(q, "q", n, hq, q.dtype), _heads(k, "k", n, hkv, q.dtype),
-                     0 if v is None else _heads(v, "v", n, hkv, q.dtype))
-    args = (q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(), ctypes.byref(rope),
-            _ptr(q_weight, "q_weight", q.dtype, HEAD_DIM), _ptr(k_weight, "k_weight", q.dtype, HEAD_DIM),
-            _ptr(inv_freq, "inv_freq", torch.float32),
-            _ptr(positions, "positions", torch.int32, n), n, _ptr(q_out, "q_out", f16, n * hq * HEAD_DIM),
-            _ptr(k_out, "k_out", f16, n * hkv * HEAD_DIM),
-            None if v is None else _ptr(v_out, "v_out", f16, n * hkv * HEAD_DIM), ctypes.byref(meta))
+    n = int(q.shape[0])
+    rows, rest = _rope_args(q, k, v, q_out, k_out, v_out, meta, q_weight, k_weight, norm_eps, inv_freq, interleaved)
+    args = (*rows, *rest[:3], _ptr(positions, "positions", torch.int32, n), n, *rest[3:])
     _device_call(q, (k, v, positions, q_out, k_out, v_out, q_weight, k_weight, inv_freq), stream,
                  lambda st: _lib.kvarn_qk_norm_rope(*args, st))
+
+
+def kvarn_qk_norm_rope_axes(q, k, v, positions, axes, q_out, k_out, v_out, meta: KvarnMeta, q_weight=None, k_weight=None,
+                            norm_eps: float = 1e-6, inv_freq=None, interleaved: bool = False, stream=None):
+    """kvarn_qk_norm_rope for tokens with a position on each of several axes (time, height,
+    width): positions int32 [n_axes, n] (rows at any stride, or one row expanded); axes: for each of the
+    rotary_dim / 2 pairs its axis, a sequence of whole numbers as long as inv_freq."""
+    import torch
+    n = int(q.shape[0])
+    if positions.dim() != 2 or positions.shape[1] != n:
+        raise ValueError(f"positions must be [n_axes, {n}], got {list(positions.shape)}")
+    if not positions.is_cuda or positions.dtype != torch.int32:
+        raise ValueError("positions must be a CUDA tensor of torch.int32")
+    if n > 1 and positions.stride(1) != 1:
+        raise ValueError("each axis' positions must be contiguous")
+    if inv_freq is None:
+        raise ValueError("inv_freq is required")
+    if len(axes) != inv_freq.numel():
+        raise ValueError(f"axes must have {inv_freq.numel()} entries, one for each pair, got {len(axes)}")
+    of_pair = bytes(axes if isinstance(axes, (list, tuple)) else [int(x) for x in axes])
+    rows, rest = _rope_args(q, k, v, q_out, k_out, v_out, meta, q_weight, k_weight, norm_eps, inv_freq, interleaved)
+    split = KvarnAxes(int(positions.shape[0]), 0, positions.stride(0), _Pairs.from_buffer_copy(of_pair[:64].ljust(64, b"\0")))
+    args = (*rows, ctypes.byref(split), *rest[:3], positions.data_ptr(), n, *rest[3:])
+    _device_call(q, (k, v, positions, q_out, k_out, v_out, q_weight, k_weight, inv_freq), stream,
+                 lambda st: _lib.kvarn_qk_norm_rope_axes(*args, st))
+
+
+def decode_weights_scratch_bytes(meta: KvarnMeta, n_seqs: int) -> int:
+    return int(_lib.kvarn_decode_weights_scratch_bytes(ctypes.byref(meta), n_seqs))
+
+
+def kvarn_decode_attention_weights(q, cache, workspace, block_tables, seq_lens, weights, out, scratch, meta: KvarnMeta,
+                                   decay: float = 1.0, lse=None, stream=None):
+    """kvarn_decode_attention that also adds each tile's attention weight to weights (float32
+    [n_seqs, Hkv, max_blocks], decay * old + new) and writes the log-sum-exp (float32
+    [n_seqs, Hq], or None). q, out: fp16 [n_seqs, Hq, 128]; scratch: at least
+    decode_weights_scratch_bytes(meta, n_seqs) bytes."""
+    import torch
+    n, f16, f32, i32 = int(q.shape[0]), torch.float16, torch.float32, torch.int32
+    rows, hkv = n * meta.num_q_heads, meta.num_kv_heads
+    args = (_ptr(q, "q", f16, rows * HEAD_DIM), _ptr(cache, "cache", torch.uint8),
+            _ptr(workspace, "workspace", f16, n * hkv * 32768),
+            _ptr(block_tables, "block_tables", i32, n * meta.max_blocks_per_seq), _ptr(seq_lens, "seq_lens", i32, n), n,
+            float(decay), _ptr(weights, "weights", f32, n * hkv * meta.max_blocks_per_seq),
+            _ptr(out, "out", f16, rows * HEAD_DIM), _ptr(lse, "lse", f32, rows), _ptr(scratch, "scratch"),
+            0 if scratch is None else scratch.numel() * scratch.element_size(), ctypes.byref(meta))
+    _device_call(q, (cache, workspace, block_tables, seq_lens, weights, out, lse, scratch), stream,
+                 lambda st: _lib.kvarn_decode_attention_weights(*args, st))
+
+
+def kvarn_evict_tiles(weights, weights_out, seq_lens, seq_lens_out, block_tables, budgets, kept, cache, meta: KvarnMeta,
+                      keep_first: int = 1, keep_last: int = 1, stream=None):
+    """The tiles of least weight leave the cache, for every sequence and kv-head: at most
+    budgets[s] (int32 [n_seqs], negative: all) stay, the first keep_first and last
+    keep_last among them. weights, weights_out (may be the same): float32 [n_seqs, Hkv,
+    max_blocks]; seq_lens / seq_lens_out: int32 [n_seqs]; kept: int32 [n_seqs, Hkv,
+    max_blocks], the old slots by new slot, then the evicted ones, then -1."""
+    import torch
+    n, f32, i32 = int(seq_lens.shape[0]), torch.float32, torch.int32
+    entries = n * meta.num_kv_heads * meta.max_blocks_per_seq
+    args = (_ptr(weights, "weights", f32, entries), _ptr(weights_out, "weights_out", f32, entries),
+            _ptr(seq_lens, "seq_lens", i32, n), _ptr(seq_lens_out, "seq_lens_out", i32, n),
+            _ptr(block_tables, "block_tables", i32, n * meta.max_blocks_per_seq), _ptr(budgets, "budgets", i32, n), n,
+            int(keep_first), int(keep_last), _ptr(kept, "kept", i32, entries), _ptr(cache, "cache", torch.uint8),
+            ctypes.byref(meta))
+    _device_call(seq_lens, (weights, weights_out, seq_lens_out, block_tables, budgets, kept, cache), stream,
+                 lambda st: _lib.kvarn_evict_tiles(*args, st))
 
 
 def tree_scratch_bytes(meta: KvarnMeta, n_seqs: int, max_tree: int) -> int:

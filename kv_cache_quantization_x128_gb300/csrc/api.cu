@@ -84,6 +84,53 @@ kvarn_status cuda_status(cudaError_t e, const char* what) {
     if (st_ != KVARN_OK) return st_;      \
   } while (0)
 
+// kvarn_qk_norm_rope's checks behind the meta's; *go is false where there is nothing to do.
+kvarn_status check_rope(const void* q, const void* k, const void* v, const kvarn_rope* rope, const void* q_weight,
+                        const void* k_weight, const float* inv_freq, const int32_t* positions, int64_t n_tokens,
+                        const uint16_t* q_out, const uint16_t* k_out, const uint16_t* v_out, const kvarn_meta* meta,
+                        bool* go) {
+  *go = false;
+  if (rope == nullptr) return fail(KVARN_EINVAL, "rope is NULL");
+  if (rope->dtype != KVARN_F16 && rope->dtype != KVARN_BF16 && rope->dtype != KVARN_F32)
+    return fail(KVARN_EUNSUPPORTED, "dtype must be KVARN_F16, KVARN_BF16 or KVARN_F32 (got %lld)", (long long)rope->dtype);
+  if (rope->rotary_dim != 16 && rope->rotary_dim != 32 && rope->rotary_dim != 64 && rope->rotary_dim != 128)
+    return fail(KVARN_EUNSUPPORTED, "rotary_dim must be 16, 32, 64 or 128 (got %lld)", (long long)rope->rotary_dim);
+  if (rope->interleaved != 0 && rope->interleaved != 1)
+    return fail(KVARN_EINVAL, "interleaved must be 0 or 1 (got %lld)", (long long)rope->interleaved);
+  if (!(rope->norm_eps > 0.0f) || !(rope->norm_eps < 1.0f)) return fail(KVARN_EINVAL, "norm_eps must be in (0, 1)");
+  if (n_tokens < 0 || n_tokens > INT32_MAX)
+    return fail(KVARN_EINVAL, "n_tokens must be in 0..2^31 - 1 (got %lld)", (long long)n_tokens);
+  const int64_t piece = rope->dtype == KVARN_F32 ? 4 : 8;   // elements of 16 bytes
+  const int64_t strides[3] = {rope->q_stride, rope->k_stride, rope->v_stride};
+  const int64_t widths[3] = {static_cast<int64_t>(meta->num_q_heads) * KVARN_HEAD_DIM,
+                             static_cast<int64_t>(meta->num_kv_heads) * KVARN_HEAD_DIM,
+                             static_cast<int64_t>(meta->num_kv_heads) * KVARN_HEAD_DIM};
+  for (int i = 0; i < (v != nullptr ? 3 : 2) && n_tokens > 1; ++i) {   // (a single row's stride is not used)
+    if (strides[i] < widths[i])
+      return fail(KVARN_EINVAL, "the row stride of %c is smaller than a row (%lld)", "qkv"[i], (long long)strides[i]);
+    if (strides[i] % piece != 0)
+      return fail(KVARN_EALIGN, "the row stride of %c must be a multiple of 16 bytes (%lld elements)", "qkv"[i],
+                  (long long)strides[i]);
+  }
+  if (n_tokens == 0) return KVARN_OK;
+  *go = true;
+  KV_TRY(need_ptr(q, "q"));
+  KV_TRY(need_ptr(k, "k"));
+  KV_TRY(need_ptr(q_out, "q_out"));
+  KV_TRY(need_ptr(k_out, "k_out"));
+  if (v != nullptr) {
+    KV_TRY(need_ptr(v, "v"));
+    KV_TRY(need_ptr(v_out, "v_out"));
+  }
+  if (q_weight != nullptr) KV_TRY(need_ptr(q_weight, "q_weight"));
+  if (k_weight != nullptr) KV_TRY(need_ptr(k_weight, "k_weight"));
+  if (inv_freq != nullptr) {
+    KV_TRY(need_ptr(inv_freq, "inv_freq"));
+    KV_TRY(need_ptr(positions, "positions"));
+  }
+  return KVARN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -194,6 +241,77 @@ kvarn_status kvarn_decode_attention(const uint16_t* q, const uint8_t* cache, con
                      "kvarn_decode_attention");
 }
 
+size_t kvarn_decode_weights_scratch_bytes(const kvarn_meta* meta, int32_t n_seqs) {
+  if (check_meta(meta) != KVARN_OK || n_seqs < 0 || n_seqs > 65535) return 0;
+  return kvarn::decode_weights_scratch_bytes(n_seqs, meta->num_kv_heads, meta->max_blocks_per_seq);
+}
+
+kvarn_status kvarn_decode_attention_weights(const uint16_t* q, const uint8_t* cache, const uint16_t* workspace,
+                                            const int32_t* block_tables, const int32_t* seq_lens, int32_t n_seqs,
+                                            float decay, float* weights, uint16_t* out, float* lse, void* scratch,
+                                            size_t scratch_bytes, const kvarn_meta* meta, void* stream) {
+  g_err[0] = 0;
+  KV_TRY(check_meta(meta));
+  if (n_seqs < 0 || n_seqs > 65535) return fail(KVARN_EINVAL, "n_seqs must be in 0..65535 (got %lld)", (long long)n_seqs);
+  if (!(decay >= 0.0f) || !(decay <= 1.0f)) return fail(KVARN_EINVAL, "decay must be in [0, 1]");
+  // (the kernels' arithmetic may flush subnormal numbers to 0, which reads as "replace")
+  if (subnormal(decay)) return fail(KVARN_EINVAL, "decay must not be subnormal");
+  if (n_seqs == 0) return KVARN_OK;
+  KV_TRY(need_ptr(q, "q"));
+  KV_TRY(need_ptr(seq_lens, "seq_lens"));
+  KV_TRY(need_ptr(out, "out"));
+  if (meta->max_blocks_per_seq > 0) {
+    KV_TRY(need_ptr(cache, "cache"));
+    KV_TRY(need_ptr(block_tables, "block_tables"));
+    KV_TRY(need_ptr(weights, "weights"));
+  }
+  if (workspace != nullptr) KV_TRY(need_ptr(workspace, "workspace"));
+  if (lse != nullptr) KV_TRY(need_ptr(lse, "lse"));
+  const size_t need = kvarn::decode_weights_scratch_bytes(n_seqs, meta->num_kv_heads, meta->max_blocks_per_seq);
+  KV_TRY(need_ptr(scratch, "scratch"));
+  if (scratch_bytes < need)
+    return fail(KVARN_ESCRATCH, "scratch too small: need %lld bytes", static_cast<long long>(need));
+  unsigned* fl = nullptr;
+  KV_TRY(flags_ptr(&fl));
+  return cuda_status(kvarn::launch_decode_weights(q, cache, workspace, block_tables, seq_lens, n_seqs, meta->num_kv_heads,
+                                                  meta->num_q_heads / meta->num_kv_heads, meta->max_blocks_per_seq,
+                                                  meta->num_blocks, meta->k_bits, meta->v_bits,
+                                                  meta->layout == KVARN_LAYOUT_LEAN, decay, weights, out, lse, scratch,
+                                                  fl, static_cast<cudaStream_t>(stream)),
+                     "kvarn_decode_attention_weights");
+}
+
+kvarn_status kvarn_evict_tiles(const float* weights, float* weights_out, const int32_t* seq_lens, int32_t* seq_lens_out,
+                               const int32_t* block_tables, const int32_t* budgets, int32_t n_seqs, int32_t keep_first,
+                               int32_t keep_last, int32_t* kept, uint8_t* cache, const kvarn_meta* meta, void* stream) {
+  g_err[0] = 0;
+  KV_TRY(check_meta(meta));
+  if (n_seqs < 0 || n_seqs > 65535) return fail(KVARN_EINVAL, "n_seqs must be in 0..65535 (got %lld)", (long long)n_seqs);
+  if (static_cast<int64_t>(n_seqs) * meta->num_kv_heads > INT32_MAX / (2 * KVARN_BLOCK_SIZE))
+    return fail(KVARN_EINVAL, "n_seqs * num_kv_heads must be below 2^23 (got %lld)",
+                (long long)n_seqs * meta->num_kv_heads);
+  if (keep_first < 0) return fail(KVARN_EINVAL, "keep_first must be >= 0 (got %lld)", (long long)keep_first);
+  if (keep_last < 0) return fail(KVARN_EINVAL, "keep_last must be >= 0 (got %lld)", (long long)keep_last);
+  if (meta->max_blocks_per_seq < 1) return fail(KVARN_EINVAL, "max_blocks_per_seq must be >= 1");
+  if (n_seqs == 0) return KVARN_OK;
+  KV_TRY(need_ptr(weights, "weights"));
+  KV_TRY(need_ptr(weights_out, "weights_out"));
+  KV_TRY(need_ptr(seq_lens, "seq_lens"));
+  KV_TRY(need_ptr(seq_lens_out, "seq_lens_out"));
+  if (seq_lens_out == seq_lens) return fail(KVARN_EINVAL, "seq_lens_out must not alias seq_lens");
+  KV_TRY(need_ptr(block_tables, "block_tables"));
+  KV_TRY(need_ptr(budgets, "budgets"));
+  KV_TRY(need_ptr(kept, "kept"));
+  KV_TRY(need_ptr(cache, "cache"));
+  unsigned* fl = nullptr;
+  KV_TRY(flags_ptr(&fl));
+  return cuda_status(kvarn::launch_evict(weights, weights_out, seq_lens, seq_lens_out, block_tables, budgets, n_seqs,
+                                         meta->num_kv_heads, meta->max_blocks_per_seq, meta->num_blocks, keep_first,
+                                         keep_last, kept, cache, static_cast<int>(kvarn_meta_record_bytes(meta)), fl,
+                                         static_cast<cudaStream_t>(stream)),
+                     "kvarn_evict_tiles");
+}
+
 kvarn_status kvarn_serve_step(const uint16_t* q, const uint16_t* k_new, const uint16_t* v_new,
                               const int32_t* seq_lens, int32_t* seq_lens_out, const int32_t* block_tables,
                               int32_t n_seqs, uint16_t* workspace, uint8_t* cache, uint16_t* out, void* scratch,
@@ -266,47 +384,39 @@ kvarn_status kvarn_qk_norm_rope(const void* q, const void* k, const void* v, con
                                 uint16_t* v_out, const kvarn_meta* meta, void* stream) {
   g_err[0] = 0;
   KV_TRY(check_meta(meta));
-  if (rope == nullptr) return fail(KVARN_EINVAL, "rope is NULL");
-  if (rope->dtype != KVARN_F16 && rope->dtype != KVARN_BF16 && rope->dtype != KVARN_F32)
-    return fail(KVARN_EUNSUPPORTED, "dtype must be KVARN_F16, KVARN_BF16 or KVARN_F32 (got %lld)", (long long)rope->dtype);
-  if (rope->rotary_dim != 16 && rope->rotary_dim != 32 && rope->rotary_dim != 64 && rope->rotary_dim != 128)
-    return fail(KVARN_EUNSUPPORTED, "rotary_dim must be 16, 32, 64 or 128 (got %lld)", (long long)rope->rotary_dim);
-  if (rope->interleaved != 0 && rope->interleaved != 1)
-    return fail(KVARN_EINVAL, "interleaved must be 0 or 1 (got %lld)", (long long)rope->interleaved);
-  if (!(rope->norm_eps > 0.0f) || !(rope->norm_eps < 1.0f)) return fail(KVARN_EINVAL, "norm_eps must be in (0, 1)");
-  if (n_tokens < 0 || n_tokens > INT32_MAX)
-    return fail(KVARN_EINVAL, "n_tokens must be in 0..2^31 - 1 (got %lld)", (long long)n_tokens);
-  const int64_t piece = rope->dtype == KVARN_F32 ? 4 : 8;   // elements of 16 bytes
-  const int64_t strides[3] = {rope->q_stride, rope->k_stride, rope->v_stride};
-  const int64_t widths[3] = {static_cast<int64_t>(meta->num_q_heads) * KVARN_HEAD_DIM,
-                             static_cast<int64_t>(meta->num_kv_heads) * KVARN_HEAD_DIM,
-                             static_cast<int64_t>(meta->num_kv_heads) * KVARN_HEAD_DIM};
-  for (int i = 0; i < (v != nullptr ? 3 : 2) && n_tokens > 1; ++i) {   // (a single row's stride is not used)
-    if (strides[i] < widths[i])
-      return fail(KVARN_EINVAL, "the row stride of %c is smaller than a row (%lld)", "qkv"[i], (long long)strides[i]);
-    if (strides[i] % piece != 0)
-      return fail(KVARN_EALIGN, "the row stride of %c must be a multiple of 16 bytes (%lld elements)", "qkv"[i],
-                  (long long)strides[i]);
-  }
-  if (n_tokens == 0) return KVARN_OK;
-  KV_TRY(need_ptr(q, "q"));
-  KV_TRY(need_ptr(k, "k"));
-  KV_TRY(need_ptr(q_out, "q_out"));
-  KV_TRY(need_ptr(k_out, "k_out"));
-  if (v != nullptr) {
-    KV_TRY(need_ptr(v, "v"));
-    KV_TRY(need_ptr(v_out, "v_out"));
-  }
-  if (q_weight != nullptr) KV_TRY(need_ptr(q_weight, "q_weight"));
-  if (k_weight != nullptr) KV_TRY(need_ptr(k_weight, "k_weight"));
-  if (inv_freq != nullptr) {
-    KV_TRY(need_ptr(inv_freq, "inv_freq"));
-    KV_TRY(need_ptr(positions, "positions"));
-  }
+  bool go = false;
+  KV_TRY(check_rope(q, k, v, rope, q_weight, k_weight, inv_freq, positions, n_tokens, q_out, k_out, v_out, meta, &go));
+  if (!go) return KVARN_OK;
   return cuda_status(kvarn::launch_rope(q, k, v, rope, q_weight, k_weight, inv_freq, positions, n_tokens,
                                         meta->num_q_heads, meta->num_kv_heads, q_out, k_out, v_out,
                                         static_cast<cudaStream_t>(stream)),
                      "kvarn_qk_norm_rope");
+}
+
+kvarn_status kvarn_qk_norm_rope_axes(const void* q, const void* k, const void* v, const kvarn_rope* rope,
+                                     const kvarn_axes* axes, const void* q_weight, const void* k_weight,
+                                     const float* inv_freq, const int32_t* positions, int64_t n_tokens, uint16_t* q_out,
+                                     uint16_t* k_out, uint16_t* v_out, const kvarn_meta* meta, void* stream) {
+  g_err[0] = 0;
+  KV_TRY(check_meta(meta));
+  if (axes == nullptr) return fail(KVARN_EINVAL, "axes is NULL");
+  if (axes->n_axes < 1 || axes->n_axes > KVARN_MAX_AXES)
+    return fail(KVARN_EINVAL, "n_axes must be in 1..%d (got %lld)", KVARN_MAX_AXES, (long long)axes->n_axes);
+  if (axes->reserved != 0) return fail(KVARN_EINVAL, "axes reserved must be 0");
+  bool go = false;
+  KV_TRY(check_rope(q, k, v, rope, q_weight, k_weight, inv_freq, positions, n_tokens, q_out, k_out, v_out, meta, &go));
+  if (inv_freq == nullptr) return fail(KVARN_EINVAL, "inv_freq is NULL");
+  for (int i = 0; i < rope->rotary_dim / 2; ++i)
+    if (axes->axis[i] >= axes->n_axes)
+      return fail(KVARN_EINVAL, "axis[%d] must be below n_axes (got %d)", i, static_cast<int>(axes->axis[i]));
+  if (axes->n_axes > 1 && axes->position_stride != 0 && axes->position_stride < n_tokens)
+    return fail(KVARN_EINVAL, "position_stride must be 0 or at least n_tokens (got %lld)",
+                (long long)axes->position_stride);
+  if (!go) return KVARN_OK;
+  return cuda_status(kvarn::launch_rope_axes(q, k, v, rope, axes, q_weight, k_weight, inv_freq, positions, n_tokens,
+                                             meta->num_q_heads, meta->num_kv_heads, q_out, k_out, v_out,
+                                             static_cast<cudaStream_t>(stream)),
+                     "kvarn_qk_norm_rope_axes");
 }
 
 size_t kvarn_tree_scratch_bytes(const kvarn_meta* meta, int32_t n_seqs, int32_t max_tree) {

@@ -45,6 +45,18 @@ cudaError_t launch_decode(const uint16_t* q, const uint8_t* cache, const uint16_
                           int k_bits, int v_bits, bool lean, uint16_t* out, void* scratch, unsigned* flags,
                           cudaStream_t stream);
 
+// Decode that weighs its tiles; `scratch` of decode_weights_scratch_bytes.
+cudaError_t launch_decode_weights(const uint16_t* q, const uint8_t* cache, const uint16_t* ws, const int32_t* block_tables,
+                                  const int32_t* seq_lens, int n_seqs, int hkv, int group, int max_blocks,
+                                  int64_t num_blocks, int k_bits, int v_bits, bool lean, float decay, float* weights,
+                                  uint16_t* out, float* lse, void* scratch, unsigned* flags, cudaStream_t stream);
+size_t decode_weights_scratch_bytes(int n_seqs, int hkv, int max_blocks);
+
+cudaError_t launch_evict(const float* weights, float* weights_out, const int32_t* seq_lens, int32_t* seq_lens_out,
+                         const int32_t* block_tables, const int32_t* budgets, int n_seqs, int hkv, int max_blocks,
+                         int64_t num_blocks, int keep_first, int keep_last, int32_t* kept, uint8_t* cache,
+                         int record_bytes, unsigned* flags, cudaStream_t stream);
+
 cudaError_t launch_prefill(const uint16_t* q, const uint16_t* k_new, const uint16_t* v_new, const int32_t* cu_tokens,
                            const int32_t* seq_lens, const int32_t* block_tables, const uint8_t* cache,
                            const uint16_t* ws, int n_seqs, int max_chunk, int hkv, int group, int max_blocks,
@@ -71,6 +83,10 @@ cudaError_t launch_read(const uint8_t* cache, const uint16_t* ws, const int32_t*
 cudaError_t launch_rope(const void* q, const void* k, const void* v, const kvarn_rope* r, const void* qw,
                         const void* kw, const float* inv_freq, const int32_t* positions, int64_t n, int hq, int hkv,
                         uint16_t* qo, uint16_t* ko, uint16_t* vo, cudaStream_t stream);
+// The same with the axis of each pair (positions: [axes][positions_stride]).
+cudaError_t launch_rope_axes(const void* q, const void* k, const void* v, const kvarn_rope* r, const kvarn_axes* axes,
+                             const void* qw, const void* kw, const float* inv_freq, const int32_t* positions, int64_t n,
+                             int hq, int hkv, uint16_t* qo, uint16_t* ko, uint16_t* vo, cudaStream_t stream);
 
 cudaError_t launch_tree(const uint16_t* q, const uint16_t* k_new, const uint16_t* v_new, const uint64_t* tree_mask,
                         const int32_t* positions, const int32_t* cu_tokens, const int32_t* seq_lens, int n_seqs,

@@ -215,8 +215,20 @@ __device__ __forceinline__ void rope_copy(const T* src, uint16_t* dst, int heads
   }
 }
 
-template <class T, bool kInter>
-__global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const RopeArgs a) {
+// Positions along several axes (images and video: time, height, width): pair i turns by the
+// token's position on axis[i]. Positions are [axes][stride]; a warp's lanes read theirs for pairs
+// lane and lane + 32, from at most as many lines as there are axes.
+struct RopeAxes {
+  int64_t stride;
+  uint8_t axis[64];
+};
+struct OneAxis {};
+
+__device__ __forceinline__ int64_t axis_offset(const OneAxis&, int) { return 0; }
+__device__ __forceinline__ int64_t axis_offset(const RopeAxes& x, int pair) { return x.axis[pair] * x.stride; }
+
+template <class T, bool kInter, class Axes = OneAxis>
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const RopeArgs a, const __grid_constant__ Axes axes) {
   __shared__ unsigned long long turn[64];                      // inv_freq / (2 pi), 2^64 to a turn
   __shared__ float off[64];                                    // 0; NaN where inv_freq is not finite: so are its angles, at any position
   __shared__ __align__(16) float2 cs[kRopeWarps][64];          // (cos, sin) of a warp's token
@@ -243,6 +255,9 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const RopeArgs a)
   const int ch1 = kInter || !rotate ? 64 + 8 * l : mine ? 8 * l + half : ch0 + 8;
   const bool rot0 = kInter ? rotate && ch0 < a.rotary : mine, rot1 = kInter ? rotate && ch1 < a.rotary : mine;
 
+  constexpr bool kAxes = sizeof(Axes) == sizeof(RopeAxes);
+  const int64_t axis0 = axis_offset(axes, lane), axis1 = axis_offset(axes, lane + 32);   // (behind half: not used)
+
   const int passes = a.passes[0] + a.passes[1] + a.passes[2];
   const int64_t items = a.n * a.split;
   for (int64_t it = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp; it < items; it += static_cast<int64_t>(gridDim.x) * kRopeWarps) {
@@ -256,11 +271,13 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const RopeArgs a)
     }
     float2 c[8];
     if (rotate) {
-      const long long pos = a.positions[t];
+      long long pos = 0;
+      if (!kAxes) pos = a.positions[t];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int f = lane + 32 * e;
         if (f < half) {
+          if (kAxes) pos = a.positions[(e == 0 ? axis0 : axis1) + t];
           const unsigned long long p = static_cast<unsigned long long>(pos) * turn[f];
           float sn, cn;
           sincospif(static_cast<float>(static_cast<int>(p >> 32)) * 4.656612873077393e-10f, &sn, &cn);   // 2^-31: half turns
@@ -287,20 +304,19 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const RopeArgs a)
   }
 }
 
-template <class T>
-cudaError_t launch_rope_type(const RopeArgs& a, bool interleaved, int64_t grid, cudaStream_t stream) {
+template <class T, class Axes>
+cudaError_t launch_rope_type(const RopeArgs& a, const Axes& axes, bool interleaved, int64_t grid, cudaStream_t stream) {
   if (interleaved)
-    rope_kernel<T, true><<<static_cast<unsigned>(grid), kRopeThreads, 0, stream>>>(a);
+    rope_kernel<T, true, Axes><<<static_cast<unsigned>(grid), kRopeThreads, 0, stream>>>(a, axes);
   else
-    rope_kernel<T, false><<<static_cast<unsigned>(grid), kRopeThreads, 0, stream>>>(a);
+    rope_kernel<T, false, Axes><<<static_cast<unsigned>(grid), kRopeThreads, 0, stream>>>(a, axes);
   return cudaGetLastError();
 }
 
-}  // namespace
-
-cudaError_t launch_rope(const void* q, const void* k, const void* v, const kvarn_rope* r, const void* qw,
-                        const void* kw, const float* inv_freq, const int32_t* positions, int64_t n, int hq, int hkv,
-                        uint16_t* qo, uint16_t* ko, uint16_t* vo, cudaStream_t stream) {
+template <class Axes>
+cudaError_t launch_rope_any(const void* q, const void* k, const void* v, const kvarn_rope* r, const Axes& axes,
+                            const void* qw, const void* kw, const float* inv_freq, const int32_t* positions, int64_t n,
+                            int hq, int hkv, uint16_t* qo, uint16_t* ko, uint16_t* vo, cudaStream_t stream) {
   RopeArgs a{};
   a.q = q; a.k = k; a.v = v; a.qw = qw; a.kw = kw;
   a.inv_freq = inv_freq;
@@ -325,9 +341,26 @@ cudaError_t launch_rope(const void* q, const void* k, const void* v, const kvarn
   a.split = static_cast<int>(split < passes ? split : passes);
   int64_t grid = (n * a.split + kRopeWarps - 1) / kRopeWarps;
   if (grid > 2 * static_cast<int64_t>(sms)) grid = 2 * static_cast<int64_t>(sms);
-  return r->dtype == KVARN_F16    ? launch_rope_type<__half>(a, r->interleaved != 0, grid, stream)
-         : r->dtype == KVARN_BF16 ? launch_rope_type<__nv_bfloat16>(a, r->interleaved != 0, grid, stream)
-                                  : launch_rope_type<float>(a, r->interleaved != 0, grid, stream);
+  return r->dtype == KVARN_F16    ? launch_rope_type<__half>(a, axes, r->interleaved != 0, grid, stream)
+         : r->dtype == KVARN_BF16 ? launch_rope_type<__nv_bfloat16>(a, axes, r->interleaved != 0, grid, stream)
+                                  : launch_rope_type<float>(a, axes, r->interleaved != 0, grid, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const void* q, const void* k, const void* v, const kvarn_rope* r, const void* qw,
+                        const void* kw, const float* inv_freq, const int32_t* positions, int64_t n, int hq, int hkv,
+                        uint16_t* qo, uint16_t* ko, uint16_t* vo, cudaStream_t stream) {
+  return launch_rope_any(q, k, v, r, OneAxis(), qw, kw, inv_freq, positions, n, hq, hkv, qo, ko, vo, stream);
+}
+
+cudaError_t launch_rope_axes(const void* q, const void* k, const void* v, const kvarn_rope* r, const kvarn_axes* axes,
+                             const void* qw, const void* kw, const float* inv_freq, const int32_t* positions, int64_t n,
+                             int hq, int hkv, uint16_t* qo, uint16_t* ko, uint16_t* vo, cudaStream_t stream) {
+  RopeAxes x{};
+  x.stride = axes->position_stride;
+  for (int i = 0; i < r->rotary_dim / 2; ++i) x.axis[i] = axes->axis[i];
+  return launch_rope_any(q, k, v, r, x, qw, kw, inv_freq, positions, n, hq, hkv, qo, ko, vo, stream);
 }
 
 }  // namespace kvarn
