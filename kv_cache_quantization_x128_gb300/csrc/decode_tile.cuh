@@ -70,20 +70,6 @@ struct DecodeArgs {
   int warps;            // warps per CTA of the split kernel
 };
 
-// What a decode that weighs its tiles carries besides (decode_weights.cu). The device
-// code below runs it where its argument type is this one.
-struct WeighArgs : DecodeArgs {
-  float2* stats;        // [n_seqs][hkv][max_blocks][8]: (m, l) of a tile and q-head: the running max
-                        // behind the tile and the tile's sum of 2^(score - m); m = -inf: not attended
-  float* weights;       // [n_seqs][hkv][max_blocks], updated
-  float* lse;           // [n_seqs][hkv * group] or NULL
-  float decay;
-};
-template <class Args>
-struct Weighs { static constexpr bool value = false; };
-template <>
-struct Weighs<WeighArgs> { static constexpr bool value = true; };
-
 __device__ __forceinline__ int full_tiles(const DecodeArgs& a, int s) {
   const int L = max(a.seq_lens[s], 0);
   return min(L / kB, a.max_blocks);
@@ -206,41 +192,12 @@ __device__ __forceinline__ void load_q(const DecodeArgs& a, int s, int h, int g,
     for (int t = 0; t < 4; ++t) qv[ks][t] *= kLog2e / 128.0f;
 }
 
-// Powers of two (up, down = 1 / up) that bring `top` >= 0 into [2^14, 2^15): fp16 pairs of
-// numbers up to top then keep 22 bits down to 2^-17 of it, whatever its size. Exponents stay
-// clear of subnormal and infinite factors (top below 2^-112 or not finite).
-__device__ __forceinline__ void range_scale(float top, float& up, float& down) {
-  const uint32_t e = min(max(__float_as_uint(top) >> 23, 15u), 253u);
-  up = __uint_as_float((268u - e) << 23);
-  down = __uint_as_float((e - 14u) << 23);
-}
-
-__device__ __forceinline__ float abs_max(float m, float2 x) { return fmax3f(m, fabsf(x.x), fabsf(x.y)); }
-
-// The fp32 numbers in a thread's operand registers (pairs in [0], [1] and [2], [3]) scaled by
-// a power of two for `top` and split into their fp16 hi and lo parts; f takes the factor back.
-__device__ __forceinline__ void scale_split(uint32_t (&A)[8][4], float top, float& f) {
-  float up, down;
-  range_scale(top, up, down);
-  f *= down;
-#pragma unroll
-  for (int ks = 0; ks < 8; ++ks) {
-    const float2 up2 = make_float2(up, up);
-    const float2 a = __fmul2_rn(make_float2(__uint_as_float(A[ks][0]), __uint_as_float(A[ks][1])), up2);
-    const float2 b = __fmul2_rn(make_float2(__uint_as_float(A[ks][2]), __uint_as_float(A[ks][3])), up2);
-    split2p(a, A[ks][0], A[ks][1]);
-    split2p(b, A[ks][2], A[ks][3]);
-  }
-}
-
 // One packed tile: update the running (max, sum, acc) of head g.
 // q_r comes from qv, or from shared memory (qsm[32 ks], this thread's float4 of k-step
-// ks) when kQSmem. With kWeigh, q' and p' are scaled per head by powers of two before they
-// become fp16 pairs (range_scale), and the tile's (m, l) of each head go to stat[0..7].
-template <int KB, int VB, bool kLean, bool kQSmem, bool kWeigh = false>
+// ks) when kQSmem.
+template <int KB, int VB, bool kLean, bool kQSmem>
 __device__ __forceinline__ void attend_tile(const uint8_t* rec, const float (&qv)[8][4], const float4* qsm, int g,
-                                            int c, float& m_run, float& l_run, float (&acc)[16][2],
-                                            float2* stat = nullptr) {
+                                            int c, float& m_run, float& l_run, float (&acc)[16][2]) {
   using L = RecordLayout<KB, VB, kLean>;
   const uint16_t* km = reinterpret_cast<const uint16_t*>(rec + L::kKMetaOff);
   const uint16_t* vm = reinterpret_cast<const uint16_t*>(rec + L::kVMetaOff);
@@ -248,7 +205,6 @@ __device__ __forceinline__ void attend_tile(const uint8_t* rec, const float (&qv
   // q' fragments (hi rows g, lo rows g + 8) and beta (fp32 pairs)
   uint32_t A[8][4];
   float2 beta2 = make_float2(0.f, 0.f);
-  float qtop = 0.f, kf = KB == 4 ? 8.f : 2.f;   // codes are converted to c / 8 or c / 2
 #pragma unroll
   for (int ks = 0; ks < 8; ++ks) {
     const int ch0 = 16 * ks + 2 * c;
@@ -261,24 +217,14 @@ __device__ __forceinline__ void attend_tile(const uint8_t* rec, const float (&qv
     const float2 rz0 = mul_h2(r0, z0), rz1 = mul_h2(r1, z1);
     const float4 qq = kQSmem ? qsm[32 * ks] : make_float4(qv[ks][0], qv[ks][1], qv[ks][2], qv[ks][3]);
     const float2 qa = make_float2(qq.x, qq.y), qb = make_float2(qq.z, qq.w);
-    const float2 pa = __fmul2_rn(qa, rs0), pb = __fmul2_rn(qb, rs1);
-    if (kWeigh) {
-      A[ks][0] = __float_as_uint(pa.x);
-      A[ks][1] = __float_as_uint(pa.y);
-      A[ks][2] = __float_as_uint(pb.x);
-      A[ks][3] = __float_as_uint(pb.y);
-      qtop = abs_max(abs_max(qtop, pa), pb);
-    } else {
-      split2p(pa, A[ks][0], A[ks][1]);
-      split2p(pb, A[ks][2], A[ks][3]);
-    }
+    split2p(__fmul2_rn(qa, rs0), A[ks][0], A[ks][1]);
+    split2p(__fmul2_rn(qb, rs1), A[ks][2], A[ks][3]);
     beta2 = __ffma2_rn(qa, rz0, beta2);
     beta2 = __ffma2_rn(qb, rz1, beta2);
   }
   const float beta = quad_sum(beta2.x + beta2.y);
   const float2 beta_2 = make_float2(beta, beta);
-  if (kWeigh) scale_split(A, quad_max(qtop), kf);
-  const float2 kf2 = make_float2(kf, kf);
+  const float2 kf2 = make_float2(KB == 4 ? 8.f : 2.f, KB == 4 ? 8.f : 2.f);   // codes were converted to c / 8 or c / 2
 
   // scores of tokens 8nt + 2c + {0, 1}, four n-tiles at a time (independent chains)
   float2 sc[16];
@@ -351,13 +297,7 @@ __device__ __forceinline__ void attend_tile(const uint8_t* rec, const float (&qv
     sc[nt] = make_float2(ex2(e.x), ex2(e.y));
     lsum2 = __fadd2_rn(lsum2, sc[nt]);
   }
-  if (kWeigh) {
-    const float lt = quad_sum(lsum2.x + lsum2.y);   // (l_run is the whole quad's here)
-    l_run = fmaf(l_run, corr, lt);
-    if (c == 0) stat[g] = make_float2(m_new, lt);
-  } else {
-    l_run = fmaf(l_run, corr, lsum2.x + lsum2.y);
-  }
+  l_run = fmaf(l_run, corr, lsum2.x + lsum2.y);
   const float2 corr2 = make_float2(corr, corr);
 #pragma unroll
   for (int n = 0; n < 16; ++n) {
@@ -368,7 +308,6 @@ __device__ __forceinline__ void attend_tile(const uint8_t* rec, const float (&qv
 
   // p' fragments and gamma; tokens 16ks + 2c + {0,1} (nt = 2ks) and + {8,9} (nt = 2ks+1)
   float2 gamma2 = make_float2(0.f, 0.f);
-  float ptop = 0.f, vf = VB == 4 ? 8.f : 2.f;
 #pragma unroll
   for (int ks = 0; ks < 8; ++ks) {
     const int t0 = 16 * ks + 2 * c;
@@ -379,24 +318,14 @@ __device__ __forceinline__ void attend_tile(const uint8_t* rec, const float (&qv
     const uint32_t c1 = kLean ? kH_One : h2raw(vm + L::kVc + t0 + 8);
     const float2 cs0 = mul_h2(c0, s0), cs1 = mul_h2(c1, s1);
     const float2 cz0 = mul_h2(c0, z0), cz1 = mul_h2(c1, z1);
-    const float2 pa = __fmul2_rn(sc[2 * ks], cs0), pb = __fmul2_rn(sc[2 * ks + 1], cs1);
-    if (kWeigh) {
-      A[ks][0] = __float_as_uint(pa.x);
-      A[ks][1] = __float_as_uint(pa.y);
-      A[ks][2] = __float_as_uint(pb.x);
-      A[ks][3] = __float_as_uint(pb.y);
-      ptop = abs_max(abs_max(ptop, pa), pb);
-    } else {
-      split2p(pa, A[ks][0], A[ks][1]);
-      split2p(pb, A[ks][2], A[ks][3]);
-    }
+    split2p(__fmul2_rn(sc[2 * ks], cs0), A[ks][0], A[ks][1]);
+    split2p(__fmul2_rn(sc[2 * ks + 1], cs1), A[ks][2], A[ks][3]);
     gamma2 = __ffma2_rn(sc[2 * ks], cz0, gamma2);
     gamma2 = __ffma2_rn(sc[2 * ks + 1], cz1, gamma2);
   }
   const float gamma = quad_sum(gamma2.x + gamma2.y);
   const float2 gamma_2 = make_float2(gamma, gamma);
-  if (kWeigh) scale_split(A, quad_max(ptop), vf);
-  const float2 vf2 = make_float2(vf, vf);
+  const float2 vf2 = make_float2(VB == 4 ? 8.f : 2.f, VB == 4 ? 8.f : 2.f);
 
   if (VB == 2) {
     // PV with 2-bit values: channel n-tile nt2 = 2np + which; cell (g, c) of panel np serves both `which`;
@@ -475,10 +404,9 @@ __device__ __forceinline__ void attend_tile(const uint8_t* rec, const float (&qv
 }
 
 // Partial record of one (sequence, kv-head) over the tiles this warp attended.
-template <bool kWeigh = false>
 __device__ __forceinline__ void flush_record(const DecodeArgs& a, int64_t rec_idx, int g, int c, float m_run,
                                              float l_run, const float (&acc)[16][2]) {
-  const float l = kWeigh ? l_run : quad_sum(l_run);
+  const float l = quad_sum(l_run);
   if (g >= a.group) return;
   float* out = a.part + rec_idx * kRecFloats + g * kPartStride;
 #pragma unroll
@@ -489,9 +417,8 @@ __device__ __forceinline__ void flush_record(const DecodeArgs& a, int64_t rec_id
 // The split phase of CTA `cta` in shape Cfg: warp w < kWarps attends its range of
 // tiles (warps beyond kWarps, in a larger block, have none); `smem` holds the stages
 // (and q_r when Cfg::kQSmem).
-template <int KB, int VB, bool kLean, class Cfg = SplitCfg<KB, VB, kLean>, class Args = DecodeArgs>
-__device__ __forceinline__ void split_body(const Args& a, uint8_t* smem, int cta) {
-  constexpr bool kWeigh = Weighs<Args>::value;
+template <int KB, int VB, bool kLean, class Cfg = SplitCfg<KB, VB, kLean>>
+__device__ __forceinline__ void split_body(const DecodeArgs& a, uint8_t* smem, int cta) {
   constexpr int kWarps = Cfg::kWarps, kStages = Cfg::kStages;
   constexpr int kRecBytes = RecordLayout<KB, VB, kLean>::kBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -542,7 +469,7 @@ __device__ __forceinline__ void split_body(const Args& a, uint8_t* smem, int cta
     const int stg = static_cast<int>(k % kStages);
     const int64_t u = static_cast<int64_t>(cc.s) * a.hkv + cc.h;
     if (u != unit) {
-      if (unit >= 0) flush_record<kWeigh>(a, wg + unit, g, c, m_run, l_run, acc);
+      if (unit >= 0) flush_record(a, wg + unit, g, c, m_run, l_run, acc);
       unit = u;
       if (lane == 0 && cc.ti == 0) a.cover[2 * u] = static_cast<int32_t>(wg);   // the unit's first split warp
       load_q(a, cc.s, cc.h, g, c, qv);
@@ -562,12 +489,8 @@ __device__ __forceinline__ void split_body(const Args& a, uint8_t* smem, int cta
       break;
     }
     if (lane == 0 && cc.ti == cc.nf - 1) a.cover[2 * u + 1] = static_cast<int32_t>(wg);   // and its last
-    float2* stat = nullptr;
-    if constexpr (kWeigh) stat = a.stats + (u * a.max_blocks + cc.ti) * 8;
     if ((valid >> stg) & 1u)
-      attend_tile<KB, VB, kLean, Cfg::kQSmem, kWeigh>(stages + stg * kRecBytes, qv, qsm, g, c, m_run, l_run, acc, stat);
-    else if (kWeigh && c == 0)
-      stat[g] = make_float2(-INFINITY, 0.f);
+      attend_tile<KB, VB, kLean, Cfg::kQSmem>(stages + stg * kRecBytes, qv, qsm, g, c, m_run, l_run, acc);
     __syncwarp();
     if (gb + k + kStages < ge) {     // refill this stage with the tile kStages ahead
       advance(a, lc);
@@ -581,7 +504,7 @@ __device__ __forceinline__ void split_body(const Args& a, uint8_t* smem, int cta
     }
     advance(a, cc);
   }
-  if (unit >= 0) flush_record<kWeigh>(a, wg + unit, g, c, m_run, l_run, acc);
+  if (unit >= 0) flush_record(a, wg + unit, g, c, m_run, l_run, acc);
   __syncwarp();
   if (lane == 0 && clean)   // the stages' shared memory may be reused after this phase
     for (int k = 0; k < kStages; ++k) mbar_inval(&bars[k]);
@@ -618,11 +541,11 @@ __device__ __forceinline__ int ws_tokens(const DecodeArgs& a, const uint16_t* ws
 // K index = the warp's 16 tokens in the S accumulators' order; B = the V rows, n-tile
 // j's column g being channel 16g + j, so each thread loads 32 contiguous bytes of
 // each of its four tokens.
-// kWeigh: p is scaled to 2^15 for its fp16 pairs, so that weights down to 2^-28 keep their bits.
-template <bool kWeigh = false>
+// kScaled: p is scaled to 2^15 for its fp16 pairs, so that weights down to 2^-28 keep their bits.
+template <bool kScaled = false>
 __device__ __forceinline__ void merge_ws_part(const DecodeArgs& a, const uint16_t* __restrict__ ws, int h, int s,
                                               int n_ws, int w, WsPart& sm) {
-  constexpr float kUp = kWeigh ? 32768.f : 1.f, kDown = 1.f / kUp;
+  constexpr float kUp = kScaled ? 32768.f : 1.f, kDown = 1.f / kUp;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int t0 = 16 * w;
   if (t0 >= n_ws) return;
@@ -706,16 +629,16 @@ __device__ __forceinline__ void merge_ws_part(const DecodeArgs& a, const uint16_
       o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
       mma16816(o[j], pa, b0, b1);
     }
-    // column 2c of n-tile j is channel 16(2c) + 8hf + j, column 2c + 1 channel 16(2c+1) + 8hf + j;
-    // rows g (hi) and g + 8 (lo) add up to head g
-    float4* o0 = reinterpret_cast<float4*>(orow + 32 * c + 8 * hf);
-    float4* o1 = reinterpret_cast<float4*>(orow + 32 * c + 16 + 8 * hf);
-    if (kWeigh) {
+    if (kScaled) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[j][e] *= kDown;
     }
+    // column 2c of n-tile j is channel 16(2c) + 8hf + j, column 2c + 1 channel 16(2c+1) + 8hf + j;
+    // rows g (hi) and g + 8 (lo) add up to head g
+    float4* o0 = reinterpret_cast<float4*>(orow + 32 * c + 8 * hf);
+    float4* o1 = reinterpret_cast<float4*>(orow + 32 * c + 16 + 8 * hf);
     o0[0] = make_float4(o[0][0] + o[0][2], o[1][0] + o[1][2], o[2][0] + o[2][2], o[3][0] + o[3][2]);
     o0[1] = make_float4(o[4][0] + o[4][2], o[5][0] + o[5][2], o[6][0] + o[6][2], o[7][0] + o[7][2]);
     o1[0] = make_float4(o[0][1] + o[0][3], o[1][1] + o[1][3], o[2][1] + o[2][3], o[3][1] + o[3][3]);
@@ -803,11 +726,10 @@ struct RecShares {
 // lane l owns channels 4l..4l+3, rotated domain) is combined with the other shares'
 // (`shares` of them in rs) and with the workspace warps' outputs (sm), un-rotated by
 // a 128-point FWHT, normalised and stored as fp16.
-// Returns (max, sum) over all that was attended.
 template <int kParts>
-__device__ __forceinline__ float2 merge_finish(const DecodeArgs& a, uint16_t* __restrict__ out, int h, int s, int gg,
-                                               int n_ws, const WsPart& sm, const RecShares<kParts>* rs, float M,
-                                               float l, float (&acc)[4]) {
+__device__ __forceinline__ void merge_finish(const DecodeArgs& a, uint16_t* __restrict__ out, int h, int s, int gg,
+                                             int n_ws, const WsPart& sm, const RecShares<kParts>* rs, float M,
+                                             float l, float (&acc)[4]) {
   const int lane = threadIdx.x & 31;
   const int64_t qrow = (static_cast<int64_t>(s) * a.hkv * a.group + static_cast<int64_t>(h) * a.group + gg) * kD;
   // the other shares of the records, then the workspace warps, against the common max
@@ -866,38 +788,6 @@ __device__ __forceinline__ float2 merge_finish(const DecodeArgs& a, uint16_t* __
   for (int k = 0; k < 4; ++k) res[k] = f2h_bits(fmaf(acc[k], kInvSqrt128, wacc[k]) * inv_l);
   *reinterpret_cast<uint2*>(out + qrow + 4 * lane) =
       make_uint2(res[0] | (static_cast<uint32_t>(res[1]) << 16), res[2] | (static_cast<uint32_t>(res[3]) << 16));
-  return make_float2(Mt, l);
-}
-
-// A unit's (max, 1 / sum) per q-head, and the weight that each head gave the workspace tokens.
-struct WeighPart {
-  float2 head[8];
-  float tail[8];
-};
-
-// Thread t of the block: the weights of tiles t, t + blockDim.x, ... of the unit, in the order of its
-// heads (the same sums at every call), then that of the workspace tokens.
-__device__ __forceinline__ void weigh_tiles(const WeighArgs& a, int64_t u, int s, int n_ws, const WeighPart& wp) {
-  const int n = full_tiles(a, s);
-  float* row = a.weights + u * a.max_blocks;
-  for (int t = threadIdx.x; t < n; t += blockDim.x) {
-    const float4* st = reinterpret_cast<const float4*>(a.stats + (u * a.max_blocks + t) * 8);
-    float w = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 v = st[j];
-      // (a sum of 0: not attended, or too little to count; its maximum is not looked at)
-      if (2 * j < a.group && v.y != 0.f) w = fmaf(v.y * exp2f(v.x - wp.head[2 * j].x), wp.head[2 * j].y, w);
-      if (2 * j + 1 < a.group && v.w != 0.f) w = fmaf(v.w * exp2f(v.z - wp.head[2 * j + 1].x), wp.head[2 * j + 1].y, w);
-    }
-    row[t] = a.decay == 0.f ? w : fmaf(a.decay, row[t], w);
-  }
-  const int last = max(a.seq_lens[s], 0) / kB;
-  if (threadIdx.x == 0 && n_ws > 0 && last < a.max_blocks) {
-    float w = 0.f;
-    for (int g = 0; g < a.group; ++g) w += wp.tail[g];
-    row[last] = a.decay == 0.f ? w : fmaf(a.decay, row[last], w);
-  }
 }
 
 // The split phase's outputs (marks, ranges, records) are ready when merge_body starts.
@@ -913,19 +803,17 @@ struct SplitDone {
 // rs are the block's shared memory (rs unused when kParts is 1). The workspace part
 // reads only the call's inputs; unless Wait::kReady, wait() runs after it, before
 // anything the split phase wrote is read.
-template <int kBatch = 8, int kParts = 1, class Wait = SplitDone, class Args = DecodeArgs>
-__device__ __forceinline__ void merge_body(const Args& a, const uint16_t* __restrict__ ws,
+template <int kBatch = 8, int kParts = 1, class Wait = SplitDone>
+__device__ __forceinline__ void merge_body(const DecodeArgs& a, const uint16_t* __restrict__ ws,
                                            uint16_t* __restrict__ out, int h, int s, WsPart& sm,
-                                           RecShares<kParts>* rs, const int64_t* rg, const Wait& wait = Wait(),
-                                           WeighPart* wp = nullptr) {
-  constexpr bool kWeigh = Weighs<Args>::value;
+                                           RecShares<kParts>* rs, const int64_t* rg, const Wait& wait = Wait()) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gg = warp & 7, share = warp >> 3;
   const int64_t u = static_cast<int64_t>(s) * a.hkv + h;
   int2 cv = make_int2(-1, -1);
   if (Wait::kReady) cv = *reinterpret_cast<const int2*>(a.cover + 2 * u);   // in flight with the length
   const int n_ws = ws_tokens(a, ws, s, threadIdx.x == 0);
-  if (warp < 8) merge_ws_part<kWeigh>(a, ws, h, s, n_ws, warp, sm);
+  if (warp < 8) merge_ws_part(a, ws, h, s, n_ws, warp, sm);
   if (!Wait::kReady) {
     wait();
     cv = *reinterpret_cast<const int2*>(a.cover + 2 * u);
@@ -942,23 +830,7 @@ __device__ __forceinline__ void merge_body(const Args& a, const uint16_t* __rest
     }
   }
   __syncthreads();
-  if constexpr (kWeigh) {
-    if (share == 0 && gg < a.group) {
-      const float2 ml = merge_finish<kParts>(a, out, h, s, gg, n_ws, sm, rs, M, l, acc);
-      if (lane == 0) {
-        const float inv = ml.y > 0.f ? 1.f / ml.y : 0.f;
-        float tail = 0.f;
-        for (int w = 0; w < (n_ws + 15) >> 4; ++w) tail = fmaf(sm.l[w][gg], exp2f(sm.m[w][gg] - ml.x), tail);
-        wp->head[gg] = make_float2(ml.x, inv);
-        wp->tail[gg] = tail * inv;
-        if (a.lse != nullptr) a.lse[u * a.group + gg] = (ml.x + log2f(ml.y)) * 0.693147180559945309f;
-      }
-    }
-    __syncthreads();
-    weigh_tiles(a, u, s, n_ws, *wp);
-  } else {
-    if (share == 0 && gg < a.group) merge_finish<kParts>(a, out, h, s, gg, n_ws, sm, rs, M, l, acc);
-  }
+  if (share == 0 && gg < a.group) merge_finish<kParts>(a, out, h, s, gg, n_ws, sm, rs, M, l, acc);
 }
 
 size_t prefix_bytes(int n_seqs) { return ((static_cast<size_t>(n_seqs) + 1) * sizeof(int64_t) + 255) & ~size_t(255); }

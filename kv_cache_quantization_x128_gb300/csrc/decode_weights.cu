@@ -3,56 +3,416 @@
 //   out_g = sum_j p_gj v_j,  p_gj = exp(x_gj - lse_g),  lse_g = ln sum_j exp(x_gj)
 //   w_t <- decay w_t + sum over the group's heads g and the tile's tokens j of p_gj
 // in one pass over the records. The weights need lse, which is known when the pass is over,
-// so the split phase leaves (m, l) of each tile and q-head: the running maximum behind the tile and the
+// so the pass leaves (m, l) of each tile and q-head: the running maximum behind the tile and the
 // tile's sum of 2^(score - m), 64 bytes beside the record's 10 to 18 KB; the merge, which has
 // the unit's maximum and sum, turns them into weights, a thread a tile.
 // The tile is the unit of weight because it is that of the record: its per-channel scales
 // bind 128 tokens, which cannot leave one record for another without being quantized again.
 //
-// Launches and shapes are those of kvarn_decode_attention (decode.cu: scan, split, merge; the
-// device code is shared, decode_tile.cuh). q' and p' are scaled by powers of two, per head
-// and tile, before they become fp16 pairs, so keys and values of any scales keep 22 bits.
-#include "decode_launch.cuh"
+// Two launches, the second a programmatic dependent of the first:
+//   weigh_split_kernel - persistent, a CTA an SM. The packed tiles of all units (a unit is a sequence and
+//     kv-head) lie in one row, and each warp takes an equal part of it (a block finds its
+//     warps' parts with a scan over the lengths of its own). A warp copies its next tile into its stage while
+//     other warps of its scheduler compute, with the tile after that on its way into L2, and writes
+//     a partial record (output, maximum, sum) for each unit that it leaves;
+//   weigh_merge_kernel - a block a unit: attends the workspace tokens, joins the records,
+//     un-rotates, normalises, and writes the weights.
 #include "decode_tile.cuh"
 #include "kvarn_common.cuh"
 #include "kvarn_launch.h"
+#include "kvarn_pdl.cuh"
+#include "weigh_tile.cuh"
 
 namespace kvarn {
 namespace {
 
-template <int KB, int VB, bool kLean, class Cfg>
-__global__ void __launch_bounds__(Cfg::kWarps * 32, 1) weigh_split_kernel(WeighArgs a) {
+struct WeighArgs : DecodeArgs {
+  const uint16_t* ws;
+  float2* stats;        // [n_seqs][hkv][max_blocks][8]: (m, l) of a tile and q-head
+  float* weights;       // [n_seqs][hkv][max_blocks], updated
+  float* lse;           // [n_seqs][hkv * group] or NULL
+  float decay;
+};
+
+// Warps with a record stage and q_r each: 12 (10 for k4v4's 18 KB records), at 168 registers.
+template <int KB, int VB, bool kLean>
+struct WeighCfg {
+  using L = RecordLayout<KB, VB, kLean>;
+  static constexpr int kWarps = SplitCfg<KB, VB, kLean>::kWarps;
+  static constexpr int kQOff = kWarps * L::kBytes;                  // q_r: [warp][group][lane] float4
+  static constexpr int kBarOff = kQOff + kWarps * 4096;
+  static constexpr int kSmem = kBarOff + kWarps * 8;
+};
+
+// ------------------------------------------------------------------ parts
+__device__ __forceinline__ int seq_len(const WeighArgs& a, int s) { return max(a.seq_lens[s], 0); }
+__device__ __forceinline__ int tiles_of(const WeighArgs& a, int len) { return min(len / kB, a.max_blocks); }
+
+struct Tile {
+  int s, h, it, tiles;  // tile `it` of the `tiles` of unit (s, h)
+};
+
+// The first tile of the next unit that has any (s = n_seqs: none).
+__device__ __forceinline__ void next_unit(const WeighArgs& a, Tile& c) {
+  c.it = 0;
+  if (++c.h < a.hkv) return;
+  c.h = 0;
+  do {
+    if (++c.s >= a.n_seqs) return;
+    c.tiles = tiles_of(a, seq_len(a, c.s));
+  } while (c.tiles == 0);
+}
+
+// A warp's part of the row of tiles.
+struct Part {
+  Tile first;
+  int64_t count;
+  int id;               // of the warp among those with parts; -1: no part
+};
+
+// The row in equal parts, one at least a tile; consecutive parts go to different SMs, so that few of them spread
+// out. The block scans the sequences' lengths, then each warp looks its own up. (64-bit divisions
+// are few: twelve for every warp had cost the largest batches 16 us.)
+template <int kWarps>
+__device__ __forceinline__ Part find_part(const WeighArgs& a) {
+  constexpr int kThreads = kWarps * 32;
+  __shared__ int64_t before[kThreads];              // tiles before a thread's sequences, of one kv-head
+  __shared__ int64_t sums[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.n_seqs + kThreads - 1) / kThreads;
+  const int s0 = min(tid * per, a.n_seqs), s1 = min(s0 + per, a.n_seqs);
+  int64_t own = 0;
+  bool cut = false;
+  for (int s = s0; s < s1; ++s) {
+    const int len = seq_len(a, s);
+    own += tiles_of(a, len);
+    cut |= len / kB > a.max_blocks;
+  }
+  if (cut && blockIdx.x == 0) raise_flag(a.flags, KVARN_FLAG_BAD_LENGTH);
+  int64_t upto = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  int64_t total = 0, mine = upto - own;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) mine += sums[w];
+    total += sums[w];
+  }
+  before[tid] = mine;
+  __syncthreads();
+  total *= a.hkv;
+  Part p;
+  p.id = warp * gridDim.x + blockIdx.x;
+  const unsigned n = static_cast<unsigned>(min(static_cast<int64_t>(gridDim.x) * kWarps, total));
+  if (static_cast<unsigned>(p.id) >= n) {
+    p.id = -1;
+    return p;
+  }
+  const int64_t whole = total / n;
+  const unsigned rest = static_cast<unsigned>(total - whole * n);    // below n <= 2^14
+  const int64_t begin = whole * p.id + rest * p.id / n;
+  p.count = whole * (p.id + 1) + rest * (p.id + 1) / n - begin;
+  // the last thread whose sequences begin at or before the part
+  int lo = 0;
+#pragma unroll
+  for (int step = 256; step > 0; step >>= 1)
+    if (lo + step < kThreads && before[lo + step] * a.hkv <= begin) lo += step;
+  int64_t off = begin - before[lo] * a.hkv;
+  Tile c;
+  for (c.s = min(lo * per, a.n_seqs - 1);; ++c.s) { // (a sequence at or behind c.s holds it)
+    c.tiles = tiles_of(a, seq_len(a, c.s));
+    const int64_t here = static_cast<int64_t>(c.tiles) * a.hkv;
+    if (off < here || c.s + 1 >= a.n_seqs) break;
+    off -= here;
+  }
+  c.h = off >> 32 ? static_cast<int>(off / c.tiles) : static_cast<int>(static_cast<unsigned>(off) / static_cast<unsigned>(c.tiles));
+  c.it = static_cast<int>(off - static_cast<int64_t>(c.h) * c.tiles);
+  p.first = c;
+  return p;
+}
+
+// Lane 0: the record of a tile; NULL (flag raised) where its block is not there.
+template <int kRecBytes>
+__device__ __forceinline__ const uint8_t* record_of(const WeighArgs& a, const Tile& c) {
+  const int64_t blk = a.block_tables[static_cast<int64_t>(c.s) * a.max_blocks + c.it];
+  if (blk < 0 || blk >= a.num_blocks) {
+    raise_flag(a.flags, KVARN_FLAG_BAD_BLOCK);
+    return nullptr;
+  }
+  return a.cache + (blk * a.hkv + c.h) * static_cast<int64_t>(kRecBytes);
+}
+
+// Lane 0: its copy into the stage (NULL: the barrier's phase completes without one).
+template <int kRecBytes>
+__device__ __forceinline__ void issue_record(uint8_t* stage, const uint8_t* src, uint64_t* bar) {
+  if (src == nullptr) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+    return;
+  }
+  mbar_arrive_expect_tx(bar, kRecBytes);
+  bulk_g2s(stage, src, kRecBytes, bar);
+}
+
+// Lane 0: the workspace tokens of a unit on their way into L2, for the merge kernel.
+__device__ __forceinline__ void prefetch_tail(const WeighArgs& a, int s, int64_t u) {
+  const int bytes = a.ws != nullptr ? seq_len(a, s) % kB * (kD * 2) : 0;
+  if (bytes == 0) return;
+  const uint16_t* k = a.ws + u * (2 * kB * kD);
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(k), "r"(bytes) : "memory");
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(k + kB * kD), "r"(bytes) : "memory");
+}
+
+// ------------------------------------------------------------------ split
+template <int KB, int VB, bool kLean>
+__global__ void __launch_bounds__(WeighCfg<KB, VB, kLean>::kWarps * 32, 1) weigh_split_kernel(const __grid_constant__ WeighArgs a) {
+  using Cfg = WeighCfg<KB, VB, kLean>;
+  constexpr int kRecBytes = RecordLayout<KB, VB, kLean>::kBytes;
   extern __shared__ __align__(1024) uint8_t smem[];
   griddep_launch_dependents();          // the merge kernel waits for this grid itself
-  griddep_wait();                       // the scan's prefix
-  split_body<KB, VB, kLean, Cfg, WeighArgs>(a, smem, blockIdx.x);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + Cfg::kBarOff) + warp;
+  if (lane == 0) {
+    mbar_init(bar, 1);
+    fence_mbar_init();
+  }
+  const Part part = find_part<Cfg::kWarps>(a);
+  const int id = part.id;
+  if (id < 0) return;                   // warps are independent: no block-wide barrier below
+  float4* qsm = reinterpret_cast<float4*>(smem + Cfg::kQOff) + warp * 256 + lane;
+  uint8_t* stage = smem + warp * kRecBytes;
+  Tile cur = part.first, next = cur;    // the tile in the stage, and the one on its way into L2
+  int64_t left = part.count;            // tiles from `cur` on
+  const uint8_t *src = nullptr, *ahead = nullptr;   // lane 0: their records
+  auto look_ahead = [&] {               // `next` moves on, and into L2
+    if (++next.it >= next.tiles) next_unit(a, next);
+    if (lane == 0) {
+      ahead = record_of<kRecBytes>(a, next);
+      if (ahead != nullptr)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(ahead), "r"(kRecBytes) : "memory");
+    }
+  };
+  if (lane == 0) {
+    src = record_of<kRecBytes>(a, cur);
+    issue_record<kRecBytes>(stage, src, bar);
+  }
+  if (left > 1) look_ahead();
+
+  float acc[16][2], m_run = -INFINITY, l_run = 0.f;
+#pragma unroll
+  for (int n = 0; n < 16; ++n) acc[n][0] = acc[n][1] = 0.f;
+  int first = -1;                       // the warp's first tile of the unit
+  for (uint32_t phase = 0;; phase ^= 1u) {
+    const int64_t u = static_cast<int64_t>(cur.s) * a.hkv + cur.h;
+    if (first < 0) {
+      first = cur.it;
+      float qv[8][4];
+      load_q(a, cur.s, cur.h, g, c, qv);
+      store_q<KB>(qsm, qv);
+    }
+    float2* stat = a.stats + (u * a.max_blocks + cur.it) * 8;
+    // (a copy that never arrives raises its flag and ends the warp)
+    if (!__all_sync(0xffffffffu, mbar_wait(bar, phase, a.flags))) return;
+    if (__shfl_sync(0xffffffffu, src != nullptr, 0)) {
+      float2 sc[16];
+      weigh_keys<KB, VB, kLean>(stage, qsm, g, c, sc);
+      weigh_values<KB, VB, kLean>(stage, sc, g, c, m_run, l_run, acc, stat);
+    } else if (c == 0) {
+      stat[g] = make_float2(-INFINITY, 0.f);
+    }
+    __syncwarp();
+    const bool more = --left > 0, same = ++cur.it < cur.tiles;
+    if (lane == 0 && more) issue_record<kRecBytes>(stage, ahead, bar);
+    if (!more || !same) {               // the warp's last tile of the unit
+      if (g < a.group) {
+        float* rec = a.part + (id + u) * kRecFloats + g * kPartStride;
+#pragma unroll
+        for (int n = 0; n < 16; ++n) *reinterpret_cast<float2*>(rec + 8 * n + 2 * c) = make_float2(acc[n][0], acc[n][1]);
+        if (c == 0) *reinterpret_cast<float2*>(rec + 128) = make_float2(m_run, l_run);
+      }
+      if (lane == 0) {                  // the unit's first and last warp
+        if (first == 0) a.cover[2 * u] = id;
+        if (!same) a.cover[2 * u + 1] = id;
+        if (!same) prefetch_tail(a, cur.s, u);
+      }
+      if (!more) return;
+      first = -1;
+      m_run = -INFINITY;
+      l_run = 0.f;
+#pragma unroll
+      for (int n = 0; n < 16; ++n) acc[n][0] = acc[n][1] = 0.f;
+      cur = next;
+    }
+    src = ahead;
+    if (left > 1) look_ahead();
+  }
 }
 
-template <int kMinBlocks, int kParts>
-__global__ void __launch_bounds__(256 * kParts, kMinBlocks) weigh_merge_kernel(WeighArgs a, const uint16_t* __restrict__ ws,
+// ------------------------------------------------------------------ merge
+// State of a share of a unit's records for q-head g: [share - 1][g] = acc[128], max, sum.
+template <int kParts>
+struct Shares {
+  float v[kParts > 1 ? kParts - 1 : 1][8][kPartStride];
+};
+
+// Block of 8 kParts warps. Warps 0-7 attend the workspace tokens, which are the call's inputs, before the
+// wait for the split kernel; then warp w takes every kParts-th record for q-head w % 8, share w / 8.
+template <int kParts, int kMinBlocks>
+__global__ void __launch_bounds__(256 * kParts, kMinBlocks) weigh_merge_kernel(const __grid_constant__ WeighArgs a,
                                                                               uint16_t* __restrict__ out) {
-  __shared__ WsPart sm;
-  __shared__ RecShares<kParts> rs;
-  __shared__ WeighPart wp;
-  merge_body<8, kParts, SplitWait, WeighArgs>(a, ws, out, blockIdx.x, blockIdx.y, sm, &rs, a.ranges, SplitWait(), &wp);
-}
-
-template <int KB, int VB, bool kLean, class C>
-cudaError_t launch_weigh_cfg(WeighArgs& a, cudaStream_t stream) {
-  static std::atomic<unsigned long long> smem_set{0};
-  cudaError_t err = set_smem_once(weigh_split_kernel<KB, VB, kLean, C>, C::kSmem, smem_set);
-  if (err != cudaSuccess) return err;
-  return launch_after(weigh_split_kernel<KB, VB, kLean, C>, dim3(a.n_ctas), dim3(C::kWarps * 32), C::kSmem, stream, a);
+  constexpr int kBatch = kParts > 1 ? 8 : 4;
+  __shared__ WsPart ws;
+  __shared__ Shares<kParts> shares;
+  __shared__ float2 heads[8];           // maximum, 1 / sum
+  __shared__ float tails[8];            // the weight of the workspace tokens
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gg = warp & 7, share = warp >> 3;
+  const int h = blockIdx.x, s = blockIdx.y;
+  const int64_t u = static_cast<int64_t>(s) * a.hkv + h;
+  const int len = seq_len(a, s), tiles = tiles_of(a, len);
+  const int n_ws = ws_tokens(a, a.ws, s, threadIdx.x == 0), n_wsw = (n_ws + 15) >> 4;
+  if (warp < 8) merge_ws_part<true>(a, a.ws, h, s, n_ws, warp, ws);
+  griddep_wait();
+  float M = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};   // channels 4 lane .. 4 lane + 3, rotated
+  if (gg < a.group && tiles > 0) {
+    const int2 cv = *reinterpret_cast<const int2*>(a.cover + 2 * u);
+    // (marks that a warp which gave up did not write may hold anything: nothing outside the records is read)
+    const bool sound = cv.x >= 0 && cv.y >= cv.x && cv.y < a.n_ctas * a.warps;
+    const int w1 = sound ? cv.y : -1;
+    for (int w0 = sound ? cv.x + share : 0; w0 <= w1; w0 += kBatch * kParts) {
+      float4 v[kBatch];
+      float2 ml[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const float* p = a.part + (min(w0 + j * kParts, w1) + u) * kRecFloats + gg * kPartStride;
+        ml[j] = *reinterpret_cast<const float2*>(p + 128);
+        v[j] = *reinterpret_cast<const float4*>(p + 4 * lane);
+        if (w0 + j * kParts > w1) ml[j] = make_float2(-INFINITY, 0.f);
+      }
+      float mb = M;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) mb = fmaxf(mb, ml[j].x);
+      if (mb > M) {
+        const float sc = exp2f(M - mb);           // 0 while M is -inf (nothing summed yet)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] *= sc;
+        l *= sc;
+        M = mb;
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {          // (a sum of 0: nothing was attended)
+        const bool use = ml[j].y != 0.f;
+        const float f = use ? exp2f(ml[j].x - M) : 0.f;
+        acc[0] = fmaf(use ? v[j].x : 0.f, f, acc[0]);
+        acc[1] = fmaf(use ? v[j].y : 0.f, f, acc[1]);
+        acc[2] = fmaf(use ? v[j].z : 0.f, f, acc[2]);
+        acc[3] = fmaf(use ? v[j].w : 0.f, f, acc[3]);
+        l = fmaf(use ? ml[j].y : 0.f, f, l);
+      }
+    }
+    if (kParts > 1 && share > 0) {
+      float* dst = shares.v[share - 1][gg];
+      *reinterpret_cast<float4*>(dst + 4 * lane) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (lane == 0) *reinterpret_cast<float2*>(dst + 128) = make_float2(M, l);
+    }
+  }
+  __syncthreads();
+  if (share == 0 && gg < a.group) {
+    float Mt = M;
+    if (kParts > 1 && tiles > 0)
+      for (int p = 0; p < kParts - 1; ++p) Mt = fmaxf(Mt, shares.v[p][gg][128]);
+    for (int w = 0; w < n_wsw; ++w) Mt = fmaxf(Mt, ws.m[w][gg]);
+    const float sc = l == 0.f ? 0.f : exp2f(M - Mt);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = l == 0.f ? 0.f : acc[k] * sc;
+    l *= sc;
+    if (kParts > 1 && tiles > 0)
+      for (int p = 0; p < kParts - 1; ++p) {
+        if (shares.v[p][gg][129] == 0.f) continue;
+        const float f = exp2f(shares.v[p][gg][128] - Mt);
+        const float4 v = *reinterpret_cast<const float4*>(&shares.v[p][gg][4 * lane]);
+        acc[0] = fmaf(v.x, f, acc[0]);
+        acc[1] = fmaf(v.y, f, acc[1]);
+        acc[2] = fmaf(v.z, f, acc[2]);
+        acc[3] = fmaf(v.w, f, acc[3]);
+        l = fmaf(shares.v[p][gg][129], f, l);
+      }
+    // un-rotate: H over the 128 channels
+    float a0 = acc[0] + acc[1], a1 = acc[0] - acc[1], a2 = acc[2] + acc[3], a3 = acc[2] - acc[3];
+    acc[0] = a0 + a2;
+    acc[1] = a1 + a3;
+    acc[2] = a0 - a2;
+    acc[3] = a1 - a3;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const bool upper = (lane & o) != 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float other = __shfl_xor_sync(0xffffffffu, acc[k], o);
+        acc[k] = upper ? other - acc[k] : acc[k] + other;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] *= kInvSqrt128;
+    float tail = 0.f;
+    for (int w = 0; w < n_wsw; ++w) {
+      const float f = exp2f(ws.m[w][gg] - Mt);
+      const float4 v = *reinterpret_cast<const float4*>(&ws.o[w][gg][4 * lane]);
+      acc[0] = fmaf(v.x, f, acc[0]);
+      acc[1] = fmaf(v.y, f, acc[1]);
+      acc[2] = fmaf(v.z, f, acc[2]);
+      acc[3] = fmaf(v.w, f, acc[3]);
+      tail = fmaf(ws.l[w][gg], f, tail);
+    }
+    l += tail;
+    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;       // (a sum that is not a number stays one)
+    uint16_t r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = f2h_bits(acc[k] * inv);
+    *reinterpret_cast<uint2*>(out + (u * a.group + gg) * kD + 4 * lane) =
+        make_uint2(r[0] | static_cast<uint32_t>(r[1]) << 16, r[2] | static_cast<uint32_t>(r[3]) << 16);
+    if (lane == 0) {
+      heads[gg] = make_float2(Mt, inv);
+      tails[gg] = tail * inv;
+      if (a.lse != nullptr) a.lse[u * a.group + gg] = (Mt + log2f(l)) * 0.693147180559945309f;
+    }
+  }
+  if (tiles + n_ws == 0) return;
+  __syncthreads();
+  // The weights, summed in the order of the heads: the same numbers at every call.
+  float* row = a.weights + u * a.max_blocks;
+  for (int t = threadIdx.x; t < tiles; t += blockDim.x) {
+    const float4* stat = reinterpret_cast<const float4*>(a.stats + (u * a.max_blocks + t) * 8);
+    float w = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 v = stat[j];
+      // (a sum of 0: not attended, or too little to count; its maximum is not looked at)
+      if (2 * j < a.group && v.y != 0.f) w = fmaf(v.y * exp2f(v.x - heads[2 * j].x), heads[2 * j].y, w);
+      if (2 * j + 1 < a.group && v.w != 0.f) w = fmaf(v.w * exp2f(v.z - heads[2 * j + 1].x), heads[2 * j + 1].y, w);
+    }
+    row[t] = a.decay == 0.f ? w : fmaf(a.decay, row[t], w);
+  }
+  const int last = len / kB;
+  if (threadIdx.x == 0 && n_ws > 0 && last < a.max_blocks) {
+    float w = 0.f;
+    for (int g = 0; g < a.group; ++g) w += tails[g];
+    row[last] = a.decay == 0.f ? w : fmaf(a.decay, row[last], w);
+  }
 }
 
 template <int KB, int VB, bool kLean>
-cudaError_t launch_weigh(WeighArgs& a, bool few_units, cudaStream_t stream) {
-  a.warps = few_units ? SplitCfg2<KB, VB, kLean>::kWarps : SplitCfg<KB, VB, kLean>::kWarps;
-  decode_scan_kernel<<<1, 1024, 0, stream>>>(a);
-  const cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess || a.max_blocks == 0) return err;
-  return few_units ? launch_weigh_cfg<KB, VB, kLean, SplitCfg2<KB, VB, kLean>>(a, stream)
-                   : launch_weigh_cfg<KB, VB, kLean, SplitCfg<KB, VB, kLean>>(a, stream);
+cudaError_t launch_weigh(WeighArgs& a, cudaStream_t stream) {
+  using C = WeighCfg<KB, VB, kLean>;
+  static std::atomic<unsigned long long> smem_set{0};
+  const cudaError_t err = set_smem_once(weigh_split_kernel<KB, VB, kLean>, C::kSmem, smem_set);
+  if (err != cudaSuccess) return err;
+  a.warps = C::kWarps;
+  weigh_split_kernel<KB, VB, kLean><<<a.n_ctas, C::kWarps * 32, C::kSmem, stream>>>(a);
+  return cudaGetLastError();
 }
 
 size_t stats_offset(int n_seqs, int hkv, int max_blocks) {
@@ -62,7 +422,8 @@ size_t stats_offset(int n_seqs, int hkv, int max_blocks) {
 }  // namespace
 
 size_t decode_weights_scratch_bytes(int n_seqs, int hkv, int max_blocks) {
-  return stats_offset(n_seqs, hkv, max_blocks) + static_cast<size_t>(n_seqs) * hkv * max_blocks * 8 * sizeof(float2);
+  return stats_offset(n_seqs, hkv, max_blocks) +
+         static_cast<size_t>(n_seqs) * hkv * max_blocks * 8 * sizeof(float2);
 }
 
 cudaError_t launch_decode_weights(const uint16_t* q, const uint8_t* cache, const uint16_t* ws, const int32_t* block_tables,
@@ -75,9 +436,6 @@ cudaError_t launch_decode_weights(const uint16_t* q, const uint8_t* cache, const
   a.cache = cache;
   a.block_tables = block_tables;
   a.seq_lens = seq_lens;
-  a.prefix = reinterpret_cast<int64_t*>(at);
-  a.ranges = reinterpret_cast<int64_t*>(at + prefix_bytes(n_seqs));
-  a.part = reinterpret_cast<float*>(at + prefix_bytes(n_seqs) + kRangeBytes);
   a.flags = flags;
   a.num_blocks = num_blocks;
   a.n_seqs = n_seqs;
@@ -85,22 +443,23 @@ cudaError_t launch_decode_weights(const uint16_t* q, const uint8_t* cache, const
   a.group = group;
   a.max_blocks = max_blocks;
   a.n_ctas = decode_num_ctas();
+  a.part = reinterpret_cast<float*>(at);
   a.cover = cover_ptr(a.part, n_seqs, hkv, a.n_ctas);
+  a.ws = ws;
   a.stats = reinterpret_cast<float2*>(at + stats_offset(n_seqs, hkv, max_blocks));
   a.weights = weights;
   a.lse = lse;
   a.decay = decay;
-  // (the shapes are chosen as in launch_decode)
-  const int64_t units = static_cast<int64_t>(n_seqs) * hkv;
-  const bool few = units <= a.n_ctas;
-  const cudaError_t err = k_bits == 2   ? launch_weigh<2, 2, false>(a, few, stream)
-                          : v_bits == 4 ? launch_weigh<4, 4, false>(a, few, stream)
-                          : lean        ? launch_weigh<4, 2, true>(a, few, stream)
-                                        : launch_weigh<4, 2, false>(a, few, stream);
+  const cudaError_t err = k_bits == 2   ? launch_weigh<2, 2, false>(a, stream)
+                          : v_bits == 4 ? launch_weigh<4, 4, false>(a, stream)
+                          : lean        ? launch_weigh<4, 2, true>(a, stream)
+                                        : launch_weigh<4, 2, false>(a, stream);
   if (err != cudaSuccess) return err;
+  // units with 8 or more partial records on average: the records of a q-head split 4 ways
+  const int64_t units = static_cast<int64_t>(n_seqs) * hkv;
   const bool long_units = static_cast<int64_t>(a.n_ctas) * a.warps >= 8 * units && max_blocks >= 8;
-  return long_units ? launch_after(weigh_merge_kernel<1, 4>, dim3(hkv, n_seqs), dim3(1024), 0, stream, a, ws, out)
-                    : launch_after(weigh_merge_kernel<4, 1>, dim3(hkv, n_seqs), dim3(256), 0, stream, a, ws, out);
+  return long_units ? launch_after(weigh_merge_kernel<4, 1>, dim3(hkv, n_seqs), dim3(1024), 0, stream, a, out)
+                    : launch_after(weigh_merge_kernel<1, 4>, dim3(hkv, n_seqs), dim3(256), 0, stream, a, out);
 }
 
 }  // namespace kvarn
