@@ -541,11 +541,8 @@ __device__ __forceinline__ int ws_tokens(const DecodeArgs& a, const uint16_t* ws
 // K index = the warp's 16 tokens in the S accumulators' order; B = the V rows, n-tile
 // j's column g being channel 16g + j, so each thread loads 32 contiguous bytes of
 // each of its four tokens.
-// kScaled: p is scaled to 2^15 for its fp16 pairs, so that weights down to 2^-28 keep their bits.
-template <bool kScaled = false>
 __device__ __forceinline__ void merge_ws_part(const DecodeArgs& a, const uint16_t* __restrict__ ws, int h, int s,
                                               int n_ws, int w, WsPart& sm) {
-  constexpr float kUp = kScaled ? 32768.f : 1.f, kDown = 1.f / kUp;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int t0 = 16 * w;
   if (t0 >= n_ws) return;
@@ -606,8 +603,8 @@ __device__ __forceinline__ void merge_ws_part(const DecodeArgs& a, const uint16_
     }
   lsum = quad_sum(lsum);
   uint32_t pa[4];
-  split2p(make_float2(sc[0][0] * kUp, sc[0][1] * kUp), pa[0], pa[1]);
-  split2p(make_float2(sc[1][0] * kUp, sc[1][1] * kUp), pa[2], pa[3]);
+  split2p(make_float2(sc[0][0], sc[0][1]), pa[0], pa[1]);
+  split2p(make_float2(sc[1][0], sc[1][1]), pa[2], pa[3]);
 
   // PV in two halves of eight n-tiles (channels 16g + 8hf .. 16g + 8hf + 7)
   const int tk[4] = {t0 + 2 * c, t0 + 2 * c + 1, t0 + 2 * c + 8, t0 + 2 * c + 9};
@@ -628,12 +625,6 @@ __device__ __forceinline__ void merge_ws_part(const DecodeArgs& a, const uint16_
       const uint32_t b0 = __byte_perm(w01, w1, sel), b1 = __byte_perm(w8, w9, sel);
       o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
       mma16816(o[j], pa, b0, b1);
-    }
-    if (kScaled) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] *= kDown;
     }
     // column 2c of n-tile j is channel 16(2c) + 8hf + j, column 2c + 1 channel 16(2c+1) + 8hf + j;
     // rows g (hi) and g + 8 (lo) add up to head g

@@ -158,15 +158,6 @@ __device__ __forceinline__ void issue_record(uint8_t* stage, const uint8_t* src,
   bulk_g2s(stage, src, kRecBytes, bar);
 }
 
-// Lane 0: the workspace tokens of a unit on their way into L2, for the merge kernel.
-__device__ __forceinline__ void prefetch_tail(const WeighArgs& a, int s, int64_t u) {
-  const int bytes = a.ws != nullptr ? seq_len(a, s) % kB * (kD * 2) : 0;
-  if (bytes == 0) return;
-  const uint16_t* k = a.ws + u * (2 * kB * kD);
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(k), "r"(bytes) : "memory");
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(k + kB * kD), "r"(bytes) : "memory");
-}
-
 // ------------------------------------------------------------------ split
 template <int KB, int VB, bool kLean>
 __global__ void __launch_bounds__(WeighCfg<KB, VB, kLean>::kWarps * 32, 1) weigh_split_kernel(const __grid_constant__ WeighArgs a) {
@@ -237,7 +228,6 @@ __global__ void __launch_bounds__(WeighCfg<KB, VB, kLean>::kWarps * 32, 1) weigh
       if (lane == 0) {                  // the unit's first and last warp
         if (first == 0) a.cover[2 * u] = id;
         if (!same) a.cover[2 * u + 1] = id;
-        if (!same) prefetch_tail(a, cur.s, u);
       }
       if (!more) return;
       first = -1;
@@ -253,6 +243,100 @@ __global__ void __launch_bounds__(WeighCfg<KB, VB, kLean>::kWarps * 32, 1) weigh
 }
 
 // ------------------------------------------------------------------ merge
+// The workspace tokens of a unit (exact, unrotated rows of its partial last tile), 16 a warp: per
+// warp and q-head the maximum, sum and output (a row padded against bank conflicts).
+constexpr int kWsRow = kD + 4;
+struct WeighWs {
+  float o[8][8][kWsRow];
+  float m[8][8], l[8][8];
+};
+
+// Warp w's tokens 16 w .. of the n_ws, all q-heads of the group at once. The products' K index is permuted alike in
+// both operands, so that the loads are 16 bytes and neighbouring lanes' adjacent: for
+// q k, k-steps 2 j and 2 j + 1 of thread (g, c) carry channels 32 j + 8 c + 0..7 of token 16 w + 8 nt + g; for p v, n-tile i's column g is channel 64 half + 8 g + i. Rows 0-7 of q are
+// the heads, 8-15 zero; p enters as hi and lo rows, scaled to 2^15, so that weights down to 2^-28 keep their bits.
+__device__ __forceinline__ void weigh_ws(const WeighArgs& a, int64_t u, int n_ws, int w, WeighWs& sm) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, t0 = 16 * w;
+  if (t0 >= n_ws) return;
+  const uint16_t* wk = a.ws + u * (2 * kB * kD) + t0 * kD;
+  const uint16_t* wv = wk + kB * kD;
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(wv + lane * 64));    // the 16 rows of V, 128 bytes a lane
+  float d[2][4];
+  {
+    const uint4* qr = reinterpret_cast<const uint4*>(a.q + (u * a.group + min(g, a.group - 1)) * kD + 8 * c);
+    const uint4* kr = reinterpret_cast<const uint4*>(wk + g * kD + 8 * c);
+    uint4 qv[4], k0[4], k1[4];                     // (rows past n_ws, still inside the unit's, are read and masked out)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      k0[j] = kr[4 * j];
+      k1[j] = kr[8 * kD / 8 + 4 * j];
+      qv[j] = g < a.group ? qr[4 * j] : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t a0[4] = {qv[j].x, 0u, qv[j].y, 0u}, a1[4] = {qv[j].z, 0u, qv[j].w, 0u};
+      if (j == 0) {
+        mma16816_first(d[0], a0, k0[j].x, k0[j].y);
+        mma16816_first(d[1], a0, k1[j].x, k1[j].y);
+      } else {
+        mma16816(d[0], a0, k0[j].x, k0[j].y);
+        mma16816(d[1], a0, k1[j].x, k1[j].y);
+      }
+      mma16816(d[0], a1, k0[j].z, k0[j].w);
+      mma16816(d[1], a1, k1[j].z, k1[j].w);
+    }
+  }
+  constexpr float kScale = kLog2e * kInvSqrt128, kUp = 32768.f;
+  float p[2][2], mx = -INFINITY, sum = 0.f;        // tokens t0 + 8 nt + 2 c + {0, 1} of head g
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      p[nt][e] = t0 + 8 * nt + 2 * c + e < n_ws ? d[nt][e] * kScale : -INFINITY;
+      mx = fmaxf(mx, p[nt][e]);
+    }
+  mx = quad_max(mx);
+#pragma unroll
+  for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      p[nt][e] = exp2f(p[nt][e] - mx);
+      sum += p[nt][e];
+    }
+  sum = quad_sum(sum);
+  uint32_t pa[4];
+  split2p(make_float2(p[0][0] * kUp, p[0][1] * kUp), pa[0], pa[1]);
+  split2p(make_float2(p[1][0] * kUp, p[1][1] * kUp), pa[2], pa[3]);
+  const int tk[4] = {2 * c, 2 * c + 1, 2 * c + 8, 2 * c + 9};
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint4 vr[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)                    // (rows behind the last token may hold anything: not multiplied)
+      vr[i] = t0 + tk[i] < n_ws ? *reinterpret_cast<const uint4*>(wv + tk[i] * kD + 64 * half + 8 * g)
+                                : make_uint4(0u, 0u, 0u, 0u);
+    float o[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t sel = (i & 1) ? 0x7632u : 0x5410u;   // high or low halves of two words
+      mma16816_first(o[i], pa, __byte_perm((&vr[0].x)[i >> 1], (&vr[1].x)[i >> 1], sel),
+                     __byte_perm((&vr[2].x)[i >> 1], (&vr[3].x)[i >> 1], sel));
+    }
+    // columns 2 c and 2 c + 1 of n-tile i: channels 64 half + 16 c + i and + 8 + i; rows g and g + 8 add up to head g
+    float4* dst = reinterpret_cast<float4*>(&sm.o[w][g][64 * half + 16 * c]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int i = 0; i < 8; i += 4)
+        dst[2 * e + i / 4] = make_float4((o[i][e] + o[i][e + 2]) / kUp, (o[i + 1][e] + o[i + 1][e + 2]) / kUp,
+                                         (o[i + 2][e] + o[i + 2][e + 2]) / kUp, (o[i + 3][e] + o[i + 3][e + 2]) / kUp);
+  }
+  if (c == 0) {
+    sm.m[w][g] = mx;
+    sm.l[w][g] = sum;
+  }
+}
+
 // State of a share of a unit's records for q-head g: [share - 1][g] = acc[128], max, sum.
 template <int kParts>
 struct Shares {
@@ -265,16 +349,16 @@ template <int kParts, int kMinBlocks>
 __global__ void __launch_bounds__(256 * kParts, kMinBlocks) weigh_merge_kernel(const __grid_constant__ WeighArgs a,
                                                                               uint16_t* __restrict__ out) {
   constexpr int kBatch = kParts > 1 ? 8 : 4;
-  __shared__ WsPart ws;
+  __shared__ WeighWs ws;
   __shared__ Shares<kParts> shares;
   __shared__ float2 heads[8];           // maximum, 1 / sum
   __shared__ float tails[8];            // the weight of the workspace tokens
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gg = warp & 7, share = warp >> 3;
-  const int h = blockIdx.x, s = blockIdx.y;
-  const int64_t u = static_cast<int64_t>(s) * a.hkv + h;
+  const int s = blockIdx.y;
+  const int64_t u = static_cast<int64_t>(s) * a.hkv + blockIdx.x;
   const int len = seq_len(a, s), tiles = tiles_of(a, len);
   const int n_ws = ws_tokens(a, a.ws, s, threadIdx.x == 0), n_wsw = (n_ws + 15) >> 4;
-  if (warp < 8) merge_ws_part<true>(a, a.ws, h, s, n_ws, warp, ws);
+  if (warp < 8) weigh_ws(a, u, n_ws, warp, ws);
   griddep_wait();
   float M = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};   // channels 4 lane .. 4 lane + 3, rotated
   if (gg < a.group && tiles > 0) {
