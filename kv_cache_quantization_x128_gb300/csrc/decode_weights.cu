@@ -31,6 +31,7 @@ struct WeighArgs : DecodeArgs {
   float2* stats;        // [n_seqs][hkv][max_blocks][8]: (m, l) of a tile and q-head
   float* weights;       // [n_seqs][hkv][max_blocks], updated
   float* lse;           // [n_seqs][hkv * group] or NULL
+  float4* ends;         // [n_seqs][hkv][8]: HeadEnd of each q-head (few units)
   float decay;
 };
 
@@ -246,16 +247,19 @@ __global__ void __launch_bounds__(WeighCfg<KB, VB, kLean>::kWarps * 32, 1) weigh
 // The workspace tokens of a unit (exact, unrotated rows of its partial last tile), 16 a warp: per
 // warp and q-head the maximum, sum and output (a row padded against bank conflicts).
 constexpr int kWsRow = kD + 4;
+template <int kHeads>
 struct WeighWs {
-  float o[8][8][kWsRow];
-  float m[8][8], l[8][8];
+  float o[8][kHeads][kWsRow];
+  float m[8][kHeads], l[8][kHeads];
 };
 
 // Warp w's tokens 16 w .. of the n_ws, all q-heads of the group at once. The products' K index is permuted alike in
 // both operands, so that the loads are 16 bytes and neighbouring lanes' adjacent: for
 // q k, k-steps 2 j and 2 j + 1 of thread (g, c) carry channels 32 j + 8 c + 0..7 of token 16 w + 8 nt + g; for p v, n-tile i's column g is channel 64 half + 8 g + i. Rows 0-7 of q are
 // the heads, 8-15 zero; p enters as hi and lo rows, scaled to 2^15, so that weights down to 2^-28 keep their bits.
-__device__ __forceinline__ void weigh_ws(const WeighArgs& a, int64_t u, int n_ws, int w, WeighWs& sm) {
+// kHeads 1: head `only` alone is kept.
+template <int kHeads>
+__device__ __forceinline__ void weigh_ws(const WeighArgs& a, int64_t u, int n_ws, int w, int only, WeighWs<kHeads>& sm) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, t0 = 16 * w;
   if (t0 >= n_ws) return;
   const uint16_t* wk = a.ws + u * (2 * kB * kD) + t0 * kD;
@@ -323,7 +327,8 @@ __device__ __forceinline__ void weigh_ws(const WeighArgs& a, int64_t u, int n_ws
                      __byte_perm((&vr[2].x)[i >> 1], (&vr[3].x)[i >> 1], sel));
     }
     // columns 2 c and 2 c + 1 of n-tile i: channels 64 half + 16 c + i and + 8 + i; rows g and g + 8 add up to head g
-    float4* dst = reinterpret_cast<float4*>(&sm.o[w][g][64 * half + 16 * c]);
+    if (kHeads == 1 && g != only) continue;
+    float4* dst = reinterpret_cast<float4*>(&sm.o[w][kHeads == 1 ? 0 : g][64 * half + 16 * c]);
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -331,34 +336,65 @@ __device__ __forceinline__ void weigh_ws(const WeighArgs& a, int64_t u, int n_ws
         dst[2 * e + i / 4] = make_float4((o[i][e] + o[i][e + 2]) / kUp, (o[i + 1][e] + o[i + 1][e + 2]) / kUp,
                                          (o[i + 2][e] + o[i + 2][e + 2]) / kUp, (o[i + 3][e] + o[i + 3][e + 2]) / kUp);
   }
-  if (c == 0) {
-    sm.m[w][g] = mx;
-    sm.l[w][g] = sum;
+  if (c == 0 && (kHeads > 1 || g == only)) {
+    sm.m[w][kHeads == 1 ? 0 : g] = mx;
+    sm.l[w][kHeads == 1 ? 0 : g] = sum;
   }
 }
 
-// State of a share of a unit's records for q-head g: [share - 1][g] = acc[128], max, sum.
-template <int kParts>
-struct Shares {
-  float v[kParts > 1 ? kParts - 1 : 1][8][kPartStride];
+// What the weights of a unit's tiles need of q-head g: its maximum, 1 / sum, and the weight of the workspace tokens.
+struct HeadEnd {
+  float top, inv, tail, pad;
 };
 
-// Block of 8 kParts warps. Warps 0-7 attend the workspace tokens, which are the call's inputs, before the
-// wait for the split kernel; then warp w takes every kParts-th record for q-head w % 8, share w / 8.
-template <int kParts, int kMinBlocks>
-__global__ void __launch_bounds__(256 * kParts, kMinBlocks) weigh_merge_kernel(const __grid_constant__ WeighArgs a,
-                                                                              uint16_t* __restrict__ out) {
-  constexpr int kBatch = kParts > 1 ? 8 : 4;
-  __shared__ WeighWs ws;
-  __shared__ Shares<kParts> shares;
-  __shared__ float2 heads[8];           // maximum, 1 / sum
-  __shared__ float tails[8];            // the weight of the workspace tokens
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gg = warp & 7, share = warp >> 3;
-  const int s = blockIdx.y;
-  const int64_t u = static_cast<int64_t>(s) * a.hkv + blockIdx.x;
+// The weight of the tile whose (m, l) are at `stat`, summed in the order of the heads: the same number at every call.
+__device__ __forceinline__ float tile_weight(const WeighArgs& a, const float2* stat, const HeadEnd* heads) {
+  float w = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 v = reinterpret_cast<const float4*>(stat)[j];
+    // (a sum of 0: not attended, or too little to count; its maximum is not looked at)
+    if (2 * j < a.group && v.y != 0.f) w = fmaf(v.y * exp2f(v.x - heads[2 * j].top), heads[2 * j].inv, w);
+    if (2 * j + 1 < a.group && v.w != 0.f) w = fmaf(v.w * exp2f(v.z - heads[2 * j + 1].top), heads[2 * j + 1].inv, w);
+  }
+  return w;
+}
+__device__ __forceinline__ void add_weight(const WeighArgs& a, float* at, float w) {
+  *at = a.decay == 0.f ? w : fmaf(a.decay, *at, w);
+}
+
+// Tiles first, first + stride, ... of the unit, and (first == 0) its workspace tokens.
+__device__ __forceinline__ void weigh_unit(const WeighArgs& a, int64_t u, int len, int n_ws, const HeadEnd* heads, int first,
+                                           int stride) {
+  const int tiles = tiles_of(a, len), last = len / kB;
+  float* row = a.weights + u * a.max_blocks;
+  for (int t = first; t < tiles; t += stride) add_weight(a, row + t, tile_weight(a, a.stats + (u * a.max_blocks + t) * 8, heads));
+  if (first == 0 && n_ws > 0 && last < a.max_blocks) {
+    float w = 0.f;
+    for (int g = 0; g < a.group; ++g) w += heads[g].tail;
+    add_weight(a, row + last, w);
+  }
+}
+
+// kHeads 8: a block a unit, kShares warps a q-head with every kShares-th record each, then the unit's weights. kHeads 1
+// (few units with very many records): a block a q-head; the weights are weigh_tiles_kernel's. Warps 0-7 attend the workspace tokens, which are the call's
+// inputs, before the wait for the split kernel.
+template <int kHeads, int kShares>
+__global__ void __launch_bounds__(32 * kHeads * kShares, kHeads * kShares > 8 ? 1 : 4)
+    weigh_merge_kernel(const __grid_constant__ WeighArgs a, uint16_t* __restrict__ out) {
+  static_assert(kHeads * kShares >= 8 && (kHeads == 8 || kHeads == 1), "8 warps for the workspace tokens");
+  constexpr int kBatch = 4;             // records in flight (8 spill: 1 x 1000 tokens 13.1 us, 12.1 so)
+  __shared__ WeighWs<kHeads> ws;
+  __shared__ float shares[kShares > 1 ? kShares - 1 : 1][kHeads][kPartStride];
+  __shared__ HeadEnd heads[8];
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s = blockIdx.y;
+  const int gg = kHeads == 8 ? warp & 7 : static_cast<int>(blockIdx.x) % a.group, share = warp / kHeads;
+  const int wg = kHeads == 8 ? gg : 0;  // the head's row in shared memory
+  const int64_t u = static_cast<int64_t>(s) * a.hkv + (kHeads == 8 ? blockIdx.x : blockIdx.x / a.group);
   const int len = seq_len(a, s), tiles = tiles_of(a, len);
   const int n_ws = ws_tokens(a, a.ws, s, threadIdx.x == 0), n_wsw = (n_ws + 15) >> 4;
-  if (warp < 8) weigh_ws(a, u, n_ws, warp, ws);
+  if (warp < 8) weigh_ws<kHeads>(a, u, n_ws, warp, gg, ws);
   griddep_wait();
   float M = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};   // channels 4 lane .. 4 lane + 3, rotated
   if (gg < a.group && tiles > 0) {
@@ -366,15 +402,15 @@ __global__ void __launch_bounds__(256 * kParts, kMinBlocks) weigh_merge_kernel(c
     // (marks that a warp which gave up did not write may hold anything: nothing outside the records is read)
     const bool sound = cv.x >= 0 && cv.y >= cv.x && cv.y < a.n_ctas * a.warps;
     const int w1 = sound ? cv.y : -1;
-    for (int w0 = sound ? cv.x + share : 0; w0 <= w1; w0 += kBatch * kParts) {
+    for (int w0 = sound ? cv.x + share : 0; w0 <= w1; w0 += kBatch * kShares) {
       float4 v[kBatch];
       float2 ml[kBatch];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const float* p = a.part + (min(w0 + j * kParts, w1) + u) * kRecFloats + gg * kPartStride;
+        const float* p = a.part + (min(w0 + j * kShares, w1) + u) * kRecFloats + gg * kPartStride;
         ml[j] = *reinterpret_cast<const float2*>(p + 128);
         v[j] = *reinterpret_cast<const float4*>(p + 4 * lane);
-        if (w0 + j * kParts > w1) ml[j] = make_float2(-INFINITY, 0.f);
+        if (w0 + j * kShares > w1) ml[j] = make_float2(-INFINITY, 0.f);
       }
       float mb = M;
 #pragma unroll
@@ -397,35 +433,34 @@ __global__ void __launch_bounds__(256 * kParts, kMinBlocks) weigh_merge_kernel(c
         l = fmaf(use ? ml[j].y : 0.f, f, l);
       }
     }
-    if (kParts > 1 && share > 0) {
-      float* dst = shares.v[share - 1][gg];
-      *reinterpret_cast<float4*>(dst + 4 * lane) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      if (lane == 0) *reinterpret_cast<float2*>(dst + 128) = make_float2(M, l);
-    }
+  }
+  if (kShares > 1 && share > 0) {
+    *reinterpret_cast<float4*>(&shares[share - 1][wg][4 * lane]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    if (lane == 0) *reinterpret_cast<float2*>(&shares[share - 1][wg][128]) = make_float2(M, l);
   }
   __syncthreads();
   if (share == 0 && gg < a.group) {
     float Mt = M;
-    if (kParts > 1 && tiles > 0)
-      for (int p = 0; p < kParts - 1; ++p) Mt = fmaxf(Mt, shares.v[p][gg][128]);
-    for (int w = 0; w < n_wsw; ++w) Mt = fmaxf(Mt, ws.m[w][gg]);
+    if (kShares > 1)
+      for (int p = 0; p < kShares - 1; ++p) Mt = fmaxf(Mt, shares[p][wg][128]);
+    for (int w = 0; w < n_wsw; ++w) Mt = fmaxf(Mt, ws.m[w][wg]);
     const float sc = l == 0.f ? 0.f : exp2f(M - Mt);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = l == 0.f ? 0.f : acc[k] * sc;
+    for (int k = 0; k < 4; ++k) acc[k] *= sc;
     l *= sc;
-    if (kParts > 1 && tiles > 0)
-      for (int p = 0; p < kParts - 1; ++p) {
-        if (shares.v[p][gg][129] == 0.f) continue;
-        const float f = exp2f(shares.v[p][gg][128] - Mt);
-        const float4 v = *reinterpret_cast<const float4*>(&shares.v[p][gg][4 * lane]);
+    if (kShares > 1)
+      for (int p = 0; p < kShares - 1; ++p) {
+        if (shares[p][wg][129] == 0.f) continue;
+        const float f = exp2f(shares[p][wg][128] - Mt);
+        const float4 v = *reinterpret_cast<const float4*>(&shares[p][wg][4 * lane]);
         acc[0] = fmaf(v.x, f, acc[0]);
         acc[1] = fmaf(v.y, f, acc[1]);
         acc[2] = fmaf(v.z, f, acc[2]);
         acc[3] = fmaf(v.w, f, acc[3]);
-        l = fmaf(shares.v[p][gg][129], f, l);
+        l = fmaf(shares[p][wg][129], f, l);
       }
     // un-rotate: H over the 128 channels
-    float a0 = acc[0] + acc[1], a1 = acc[0] - acc[1], a2 = acc[2] + acc[3], a3 = acc[2] - acc[3];
+    const float a0 = acc[0] + acc[1], a1 = acc[0] - acc[1], a2 = acc[2] + acc[3], a3 = acc[2] - acc[3];
     acc[0] = a0 + a2;
     acc[1] = a1 + a3;
     acc[2] = a0 - a2;
@@ -443,13 +478,13 @@ __global__ void __launch_bounds__(256 * kParts, kMinBlocks) weigh_merge_kernel(c
     for (int k = 0; k < 4; ++k) acc[k] *= kInvSqrt128;
     float tail = 0.f;
     for (int w = 0; w < n_wsw; ++w) {
-      const float f = exp2f(ws.m[w][gg] - Mt);
-      const float4 v = *reinterpret_cast<const float4*>(&ws.o[w][gg][4 * lane]);
+      const float f = exp2f(ws.m[w][wg] - Mt);
+      const float4 v = *reinterpret_cast<const float4*>(&ws.o[w][wg][4 * lane]);
       acc[0] = fmaf(v.x, f, acc[0]);
       acc[1] = fmaf(v.y, f, acc[1]);
       acc[2] = fmaf(v.z, f, acc[2]);
       acc[3] = fmaf(v.w, f, acc[3]);
-      tail = fmaf(ws.l[w][gg], f, tail);
+      tail = fmaf(ws.l[w][wg], f, tail);
     }
     l += tail;
     const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;       // (a sum that is not a number stays one)
@@ -459,33 +494,27 @@ __global__ void __launch_bounds__(256 * kParts, kMinBlocks) weigh_merge_kernel(c
     *reinterpret_cast<uint2*>(out + (u * a.group + gg) * kD + 4 * lane) =
         make_uint2(r[0] | static_cast<uint32_t>(r[1]) << 16, r[2] | static_cast<uint32_t>(r[3]) << 16);
     if (lane == 0) {
-      heads[gg] = make_float2(Mt, inv);
-      tails[gg] = tail * inv;
+      const HeadEnd e{Mt, inv, tail * inv, 0.f};
+      if (kHeads == 8) heads[gg] = e;
+      else reinterpret_cast<HeadEnd*>(a.ends)[u * 8 + gg] = e;
       if (a.lse != nullptr) a.lse[u * a.group + gg] = (Mt + log2f(l)) * 0.693147180559945309f;
     }
   }
-  if (tiles + n_ws == 0) return;
+  if (kHeads == 8) {
+    __syncthreads();
+    weigh_unit(a, u, len, n_ws, heads, threadIdx.x, blockDim.x);
+  }
+}
+
+// The weights of few units, gridDim.z blocks each.
+__global__ void __launch_bounds__(256) weigh_tiles_kernel(const __grid_constant__ WeighArgs a) {
+  __shared__ HeadEnd heads[8];
+  const int s = blockIdx.y, len = seq_len(a, s);
+  const int64_t u = static_cast<int64_t>(s) * a.hkv + blockIdx.x;
+  griddep_wait();
+  if (threadIdx.x < a.group) heads[threadIdx.x] = reinterpret_cast<const HeadEnd*>(a.ends)[u * 8 + threadIdx.x];
   __syncthreads();
-  // The weights, summed in the order of the heads: the same numbers at every call.
-  float* row = a.weights + u * a.max_blocks;
-  for (int t = threadIdx.x; t < tiles; t += blockDim.x) {
-    const float4* stat = reinterpret_cast<const float4*>(a.stats + (u * a.max_blocks + t) * 8);
-    float w = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 v = stat[j];
-      // (a sum of 0: not attended, or too little to count; its maximum is not looked at)
-      if (2 * j < a.group && v.y != 0.f) w = fmaf(v.y * exp2f(v.x - heads[2 * j].x), heads[2 * j].y, w);
-      if (2 * j + 1 < a.group && v.w != 0.f) w = fmaf(v.w * exp2f(v.z - heads[2 * j + 1].x), heads[2 * j + 1].y, w);
-    }
-    row[t] = a.decay == 0.f ? w : fmaf(a.decay, row[t], w);
-  }
-  const int last = len / kB;
-  if (threadIdx.x == 0 && n_ws > 0 && last < a.max_blocks) {
-    float w = 0.f;
-    for (int g = 0; g < a.group; ++g) w += tails[g];
-    row[last] = a.decay == 0.f ? w : fmaf(a.decay, row[last], w);
-  }
+  weigh_unit(a, u, len, a.ws != nullptr ? len % kB : 0, heads, blockIdx.z * 256 + threadIdx.x, gridDim.z * 256);
 }
 
 template <int KB, int VB, bool kLean>
@@ -499,15 +528,16 @@ cudaError_t launch_weigh(WeighArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-size_t stats_offset(int n_seqs, int hkv, int max_blocks) {
+// Scratch: the partial records and marks (within the decode's), HeadEnds, (m, l) of the tiles.
+size_t ends_offset(int n_seqs, int hkv, int max_blocks) {
   return (decode_part_bytes(n_seqs, hkv, max_blocks) + 255) & ~size_t(255);
 }
 
 }  // namespace
 
 size_t decode_weights_scratch_bytes(int n_seqs, int hkv, int max_blocks) {
-  return stats_offset(n_seqs, hkv, max_blocks) +
-         static_cast<size_t>(n_seqs) * hkv * max_blocks * 8 * sizeof(float2);
+  return ends_offset(n_seqs, hkv, max_blocks) +
+         static_cast<size_t>(n_seqs) * hkv * (sizeof(HeadEnd) + static_cast<size_t>(max_blocks) * sizeof(float2)) * 8;
 }
 
 cudaError_t launch_decode_weights(const uint16_t* q, const uint8_t* cache, const uint16_t* ws, const int32_t* block_tables,
@@ -530,20 +560,28 @@ cudaError_t launch_decode_weights(const uint16_t* q, const uint8_t* cache, const
   a.part = reinterpret_cast<float*>(at);
   a.cover = cover_ptr(a.part, n_seqs, hkv, a.n_ctas);
   a.ws = ws;
-  a.stats = reinterpret_cast<float2*>(at + stats_offset(n_seqs, hkv, max_blocks));
+  a.ends = reinterpret_cast<float4*>(at + ends_offset(n_seqs, hkv, max_blocks));
+  a.stats = reinterpret_cast<float2*>(a.ends + static_cast<size_t>(n_seqs) * hkv * 8);
   a.weights = weights;
   a.lse = lse;
   a.decay = decay;
-  const cudaError_t err = k_bits == 2   ? launch_weigh<2, 2, false>(a, stream)
-                          : v_bits == 4 ? launch_weigh<4, 4, false>(a, stream)
-                          : lean        ? launch_weigh<4, 2, true>(a, stream)
-                                        : launch_weigh<4, 2, false>(a, stream);
+  cudaError_t err = k_bits == 2   ? launch_weigh<2, 2, false>(a, stream)
+                    : v_bits == 4 ? launch_weigh<4, 4, false>(a, stream)
+                    : lean        ? launch_weigh<4, 2, true>(a, stream)
+                                  : launch_weigh<4, 2, false>(a, stream);
   if (err != cudaSuccess) return err;
-  // units with 8 or more partial records on average: the records of a q-head split 4 ways
-  const int64_t units = static_cast<int64_t>(n_seqs) * hkv;
-  const bool long_units = static_cast<int64_t>(a.n_ctas) * a.warps >= 8 * units && max_blocks >= 8;
-  return long_units ? launch_after(weigh_merge_kernel<4, 1>, dim3(hkv, n_seqs), dim3(1024), 0, stream, a, out)
-                    : launch_after(weigh_merge_kernel<1, 4>, dim3(hkv, n_seqs), dim3(256), 0, stream, a, out);
+  // By the partial records of a unit, on average (as many as parts, or tiles). 64 heads over 8, k4v2:
+  // from 8 records on 4 warps a q-head (16 x 1000 tokens: 15.6 us, 20.1 with one), from 96 on a block a q-head
+  // (1 x 131072: 46 us against 64; 3 x 16389, 76 records: 30 against 28).
+  const int64_t units = static_cast<int64_t>(n_seqs) * hkv, parts = static_cast<int64_t>(a.n_ctas) * a.warps;
+  const int64_t records = parts / units < max_blocks ? parts / units : max_blocks;
+  if (records < 8) return launch_after(weigh_merge_kernel<8, 1>, dim3(hkv, n_seqs), dim3(256), 0, stream, a, out);
+  if (records < 96) return launch_after(weigh_merge_kernel<8, 4>, dim3(hkv, n_seqs), dim3(1024), 0, stream, a, out);
+  err = launch_after(weigh_merge_kernel<1, 32>, dim3(hkv * group, n_seqs), dim3(1024), 0, stream, a, out);
+  if (err != cudaSuccess) return err;
+  int64_t z = (max_blocks + 255) / 256;
+  if (z > 64) z = 64;
+  return launch_after(weigh_tiles_kernel, dim3(hkv, n_seqs, static_cast<unsigned>(z)), dim3(256), 0, stream, a);
 }
 
 }  // namespace kvarn

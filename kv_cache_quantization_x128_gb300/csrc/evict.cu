@@ -7,9 +7,8 @@
 // slide down in order. A random choice of b of n tiles then moves about b (n - b) / n records a
 // kv-head instead of nearly b, and a sequence one tile above its budget keep_last + 1.
 //
-// evict_select_kernel - a block per (sequence, kv-head), about eight tiles a thread. The
-//   smallest weight that stays is found bit by bit from the top (a count over the block for
-//   each bit, until one leaves exactly as many tiles as may stay); ranks by ballots give
+// evict_select_kernel - a block per (sequence, kv-head), about two tiles a thread. The
+//   smallest weight that stays is found two bits at a time from the top (search_warp); ranks by ballots give
 //   the slots. No atomics: the same slots at every call.
 // evict_move_kernel - the copies, bound by memory. An evicted slot below b starts a path: it takes
 //   the record of slot kept[.], whose place, where it is below b itself, takes the next. Paths
@@ -35,13 +34,19 @@ struct EvictArgs {
   int64_t num_blocks;
   int n_seqs, hkv, max_blocks;
   int first, last;
-  int key_slots;                // keys held in shared memory
+  int key_slots;                // keys held in shared memory, and behind them
+  int list_slots;               // max_blocks where the slots' list is held there too, 0 where `kept` is the list
   int per_unit;                 // blocks of the move kernel a (sequence, kv-head)
   int record_bytes;
 };
 
 constexpr int kEvictMaxThreads = 1024;
-constexpr int kKeySlots = 10240;      // 40 KB; weights of further tiles are read again for every bit
+constexpr int kKeySlots = 10240;      // 40 KB; weights of further tiles are read again for every two bits
+constexpr int kListSlots = 5120;      // the most blocks of a row whose list is held beside the keys
+// Up to so many tiles to choose from are one warp's: every warp of a block with tiles of its own and barriers between
+// the counts took 2048 blocks of 256 tiles 22 us, bound by instructions, where the warp takes 11.
+constexpr int kWarpTiles = 512;
+static_assert(kWarpTiles <= kKeySlots, "its keys are held");
 constexpr int kMoveThreads = 128;
 
 // Whole numbers in the order of the weights: -0 as 0, NaN below everything.
@@ -50,14 +55,113 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return w != w ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// Sum over the block; `sums` holds a number a warp, and is free again after the next barrier.
-__device__ __forceinline__ int block_sum(int x, int* sums) {
-  x = __reduce_add_sync(0xffffffffu, x);
-  if (blockDim.x == 32) return x;
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = x;
-  __syncthreads();
-  const int lane = threadIdx.x & 31;
-  return __reduce_add_sync(0xffffffffu, lane < static_cast<int>(blockDim.x >> 5) ? sums[lane] : 0);
+// Of the keys of tiles lo .. hi - 1, the smallest that stays where `quota` (0 < quota < hi - lo) stay: it is above `cut`, or is `cut` for
+// the first `ties` tiles that have it. One warp, with KPL keys a lane in registers.
+//   Few tiles to evict (a sequence at its budget has one): the smallest key, then the next one, ...
+//   until enough are counted.
+//   Else two bits at a time from the top: three counts each, until one leaves exactly the quota.
+template <int KPL>
+__device__ __forceinline__ void search_warp(const uint32_t* keys, int lo, int hi, int quota, uint32_t& cut, int& ties) {
+  constexpr uint32_t kAll = 0xffffffffu;           // above every key: what is behind hi
+  uint32_t k[KPL];
+#pragma unroll
+  for (int j = 0; j < KPL; ++j) {
+    const int i = lo + static_cast<int>(threadIdx.x & 31) + 32 * j;
+    k[j] = i < hi ? keys[i] : kAll;
+  }
+  const int evict = hi - lo - quota;
+  if (evict <= 4) {
+    bool any = false;
+    int below = 0;                                 // keys up to `cut`
+    do {
+      uint32_t least = kAll;
+#pragma unroll
+      for (int j = 0; j < KPL; ++j)
+        if (!any || k[j] > cut) least = min(least, k[j]);
+      cut = __reduce_min_sync(kAll, least);
+      any = true;
+      int c = 0;
+#pragma unroll
+      for (int j = 0; j < KPL; ++j) c += k[j] <= cut;
+      below = __reduce_add_sync(kAll, c);
+    } while (below < evict);
+    ties = below - evict;
+    return;
+  }
+  const int want = quota + KPL * 32 - (hi - lo);   // (what is behind hi is counted too)
+  cut = 0;
+  ties = 0;
+#pragma unroll 1
+  for (int bit = 30; bit >= 0; bit -= 2) {
+    const uint32_t k0 = cut | 1u << bit, k1 = cut | 2u << bit, k2 = cut | 3u << bit;
+    int c0 = 0, c1 = 0, c2 = 0;
+#pragma unroll
+    for (int j = 0; j < KPL; ++j) {
+      c0 += k[j] >= k0;
+      c1 += k[j] >= k1;
+      c2 += k[j] >= k2;
+    }
+    c0 = __reduce_add_sync(kAll, c0);
+    c1 = __reduce_add_sync(kAll, c1);
+    c2 = __reduce_add_sync(kAll, c2);
+    const int c = c2 >= want ? c2 : c1 >= want ? c1 : c0;
+    cut = c2 >= want ? k2 : c1 >= want ? k1 : c0 >= want ? k0 : cut;
+    if (c == want) {
+      --cut;                                       // (a bit was just set)
+      return;
+    }
+  }
+  int c = 0;
+#pragma unroll
+  for (int j = 0; j < KPL; ++j) c += k[j] > cut;
+  ties = want - __reduce_add_sync(kAll, c);
+}
+
+// The same for any number of tiles, by the whole block; keys from `slots` on come from the weights.
+__device__ __forceinline__ void search_block(const uint32_t* keys, int slots, const float* w, int lo, int hi, int quota, uint32_t& cut,
+                                             int& ties) {
+  __shared__ int sums[2][3][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  // a thread's first two keys stay in registers (0 where there is none: below every threshold)
+  const int i0 = lo + static_cast<int>(threadIdx.x), i1 = i0 + static_cast<int>(blockDim.x);
+  const uint32_t key0 = i0 < min(hi, slots) ? keys[i0] : i0 < hi ? weight_key(w[i0]) : 0u;
+  const uint32_t key1 = i1 < min(hi, slots) ? keys[i1] : i1 < hi ? weight_key(w[i1]) : 0u;
+  auto count = [&](int (&c)[3], uint32_t k0, uint32_t k1, uint32_t k2, int (*sm)[32]) {
+    c[0] = (key0 >= k0) + (key1 >= k0);
+    c[1] = (key0 >= k1) + (key1 >= k1);
+    c[2] = (key0 >= k2) + (key1 >= k2);
+    for (int i = i1 + static_cast<int>(blockDim.x); i < hi; i += static_cast<int>(blockDim.x)) {
+      const uint32_t k = i < slots ? keys[i] : weight_key(w[i]);
+      c[0] += k >= k0;
+      c[1] += k >= k1;
+      c[2] += k >= k2;
+    }
+#pragma unroll
+    for (int j = 0; j < 3; ++j) c[j] = __reduce_add_sync(0xffffffffu, c[j]);
+    if (lane == 0)
+#pragma unroll
+      for (int j = 0; j < 3; ++j) sm[j][warp] = c[j];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 3; ++j) c[j] = __reduce_add_sync(0xffffffffu, lane < warps ? sm[j][lane] : 0);
+  };
+  cut = 0;
+  ties = 0;
+  int c[3];
+#pragma unroll 1
+  for (int bit = 30; bit >= 0; bit -= 2) {         // (sums alternate: a barrier lies between their uses)
+    const uint32_t k0 = cut | 1u << bit, k1 = cut | 2u << bit, k2 = cut | 3u << bit;
+    count(c, k0, k1, k2, sums[bit >> 1 & 1]);
+    const int most = c[2] >= quota ? c[2] : c[1] >= quota ? c[1] : c[0];
+    cut = c[2] >= quota ? k2 : c[1] >= quota ? k1 : c[0] >= quota ? k0 : cut;
+    if (most == quota) {
+      --cut;
+      return;
+    }
+  }
+  // (no key has all bits set, so cut + 1 does not wrap: that would be a NaN's)
+  count(c, cut + 1u, cut + 1u, cut + 1u, sums[1]);
+  ties = quota - c[0];
 }
 
 // The thread's rank among those with `p`, counted from `base`, which moves on by their number.
@@ -81,22 +185,28 @@ __device__ __forceinline__ int block_rank(bool p, int& base, int* sums) {
 __global__ void __launch_bounds__(kEvictMaxThreads) evict_select_kernel(const EvictArgs a) {
   griddep_launch_dependents();          // the move kernel waits for this grid itself
   extern __shared__ uint32_t keys[];
-  __shared__ int sums[2][32];
+  __shared__ int ranks[3][32];
+  __shared__ uint32_t found[2];
   const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, threads = blockDim.x;
   const int64_t u = static_cast<int64_t>(s) * a.hkv + h;
   const float* w = a.weights + u * a.max_blocks;
   float* wo = a.weights_out + u * a.max_blocks;
   int32_t* kept = a.kept + u * a.max_blocks;
-  const int length = a.seq_lens[s], tiles = max(length, 0) / kB, n = min(tiles, a.max_blocks);
-  const int budget = a.budgets[s];
-  int b = budget < 0 ? n : min(n, budget);
+  int32_t* list = a.list_slots > 0 ? reinterpret_cast<int32_t*>(keys + a.key_slots) : kept;
+  const int length = a.seq_lens[s], budget = a.budgets[s];
+  const int tiles = max(length, 0) / kB, n = min(tiles, a.max_blocks), b = budget < 0 ? n : min(n, budget);
+  const int first = min(a.first, b), last = min(a.last, b - first);
+  const int lo = first, hi = n - last, quota = b - first - last, edge = b - last;
   bool sound = tiles <= a.max_blocks;
   if (!sound && tid == 0) raise_flag(a.flags, KVARN_FLAG_BAD_LENGTH);
-  if (b < n && sound) {                 // every block that could be read or written
+  if (b < n && sound) {                 // every block that could be read or written, and the keys
     bool ok = true;
+#pragma unroll 2
     for (int t = tid; t < n; t += threads) {
       const int64_t blk = a.block_tables[static_cast<int64_t>(s) * a.max_blocks + t];
+      const float x = w[t];
       ok &= blk >= 0 && blk < a.num_blocks;
+      if (t < a.key_slots) keys[t] = weight_key(x);
     }
     sound = __syncthreads_and(ok);
     if (!sound && tid == 0) raise_flag(a.flags, KVARN_FLAG_BAD_BLOCK);
@@ -111,69 +221,62 @@ __global__ void __launch_bounds__(kEvictMaxThreads) evict_select_kernel(const Ev
     return;
   }
 
-  const int first = min(a.first, b), last = min(a.last, b - first);
-  const int lo = first, hi = n - last, quota = b - first - last, edge = b - last;
-  // the smallest key that stays is above `cut`, or is `cut` for the first `ties` tiles that have it
   uint32_t cut = 0;
   int ties = 0;
   const bool choose = quota > 0 && quota < hi - lo;
-  if (choose) {
-    const int held = min(hi, lo + a.key_slots);
-    for (int i = lo + tid; i < held; i += threads) keys[i - lo] = weight_key(w[i]);   // (each thread reads its own)
-    auto count_from = [&](uint32_t least, int* sm) {
-      int c = 0;
-      for (int i = lo + tid; i < hi; i += threads) c += (i < held ? keys[i - lo] : weight_key(w[i])) >= least;
-      return block_sum(c, sm);
-    };
-    bool exact = false;
-    for (int bit = 31; bit >= 0 && !exact; --bit) {
-      const uint32_t least = cut | 1u << bit;
-      const int c = count_from(least, sums[bit & 1]);
-      if (c >= quota) cut = least;
-      exact = c == quota;
+  if (choose && hi - lo <= kWarpTiles) {
+    if (tid < 32) {
+      if (hi - lo <= 64) search_warp<2>(keys, lo, hi, quota, cut, ties);
+      else if (hi - lo <= 128) search_warp<4>(keys, lo, hi, quota, cut, ties);
+      else if (hi - lo <= 256) search_warp<8>(keys, lo, hi, quota, cut, ties);
+      else search_warp<16>(keys, lo, hi, quota, cut, ties);
+      if (tid == 0) {
+        found[0] = cut;
+        found[1] = static_cast<uint32_t>(ties);
+      }
     }
-    if (exact) {
-      --cut;                            // cut > 0: a bit was just set
-    } else {
-      __syncthreads();
-      // (no key has all bits set, so cut + 1 does not wrap: that would be a NaN's)
-      ties = quota - count_from(cut + 1u, sums[0]);
-    }
+    __syncthreads();
+    cut = found[0];
+    ties = static_cast<int>(found[1]);
+  } else if (choose) {
+    search_block(keys, a.key_slots, w, lo, hi, quota, cut, ties);
   }
   int eq = 0, gone = 0, late = 0;       // ties, evicted tiles and moved tiles so far
   for (int i0 = lo; i0 < hi; i0 += threads) {
     const int i = i0 + tid;
     const bool live = i < hi;
-    bool stays = live && (!choose ? quota > 0 : false);
+    bool stays = live && !choose && quota > 0;
     if (choose) {
-      const uint32_t k = live ? (i - lo < a.key_slots ? keys[i - lo] : weight_key(w[i])) : 0u;
-      const bool tie = live && ties > 0 && k == cut;
+      const uint32_t k = !live ? 0u : i < a.key_slots ? keys[i] : weight_key(w[i]);
+      stays = live && k > cut;
       if (ties > 0) {
-        const int r = block_rank(tie, eq, sums[0]);
-        stays = live && (k > cut || (tie && r < ties));
-      } else {
-        stays = live && k > cut;
+        const bool tie = live && k == cut;
+        const int r = block_rank(tie, eq, ranks[0]);
+        stays |= tie && r < ties;
       }
     }
-    const int g = block_rank(live && !stays, gone, sums[0]);
     const bool moves = stays && i >= edge;
-    const int m = block_rank(moves, late, sums[1]);
-    if (live && !stays) kept[b + g] = i;
-    if (stays && !moves) kept[i] = i;
+    const int g = block_rank(live && !stays, gone, ranks[1]);
+    const int m = block_rank(moves, late, ranks[2]);
+    if (live && !stays) list[b + g] = i;
+    if (stays && !moves) list[i] = i;
     __syncthreads();                    // the evicted slots so far are listed; the m-th is the moved tile's place
-    if (moves) kept[kept[b + m]] = i;
+    if (moves) list[list[b + m]] = i;
   }
-  for (int i = tid; i < first; i += threads) kept[i] = i;
-  for (int i = tid; i < last; i += threads) kept[edge + i] = hi + i;
-  for (int i = n + tid; i < a.max_blocks; i += threads) kept[i] = -1;
+  for (int i = tid; i < first; i += threads) list[i] = i;
+  for (int i = tid; i < last; i += threads) list[edge + i] = hi + i;
+  for (int i = n + tid; i < a.max_blocks; i += threads) list[i] = -1;
   __syncthreads();
-  // Weights follow their tiles, the partial tile's the last of them (kept[i] >= i: where weights_out
+  // Weights follow their tiles, the partial tile's the last of them (list[i] >= i: where weights_out
   // is weights, what a round reads no earlier round has written).
   for (int i0 = 0; i0 < a.max_blocks; i0 += threads) {
     const int i = i0 + tid;
-    const bool take = i < b || (i == b && n < a.max_blocks);
     float x = 0.f;
-    if (i < a.max_blocks && take) x = w[i < b ? kept[i] : n];
+    if (i < a.max_blocks) {
+      const int from = list[i];
+      if (i < b || (i == b && n < a.max_blocks)) x = w[i < b ? from : n];
+      if (a.list_slots > 0) kept[i] = from;
+    }
     __syncthreads();
     if (i < a.max_blocks) wo[i] = x;
   }
@@ -239,9 +342,11 @@ cudaError_t launch_evict(const float* weights, float* weights_out, const int32_t
   a.last = keep_last;
   a.record_bytes = record_bytes;
   a.key_slots = max_blocks < kKeySlots ? max_blocks : kKeySlots;
-  int threads = (max_blocks / 8 + 31) / 32 * 32;
+  a.list_slots = max_blocks <= kListSlots ? max_blocks : 0;
+  // about two tiles a thread (eight: 16 x 16384 tokens, 128 tiles, 15.5 us of choosing)
+  int threads = max_blocks / 2 / 32 * 32;
   threads = threads < 32 ? 32 : threads > kEvictMaxThreads ? kEvictMaxThreads : threads;
-  evict_select_kernel<<<dim3(hkv, n_seqs), threads, a.key_slots * sizeof(uint32_t), stream>>>(a);
+  evict_select_kernel<<<dim3(hkv, n_seqs), threads, (a.key_slots + a.list_slots) * sizeof(uint32_t), stream>>>(a);
   const cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   // as many blocks a unit as fill the GPU, at most one for each of a unit's paths (no more than half its tiles)
