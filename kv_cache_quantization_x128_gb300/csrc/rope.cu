@@ -16,8 +16,8 @@
 // channels as two 16-byte accesses, chosen so that both members of a pair are its own and
 // a rotation needs no exchange; the norm's sum takes three shuffles for the four rows of a warp.
 // 65536 tokens of 64 q-heads over 8 kv-heads, fp16, normed: 456 us, 5.9 TB/s of 2.68 GB (87 % of a
-// plain copy's rate); two blocks an SM at 128 registers, three at 80 spill (599 us). fp32 rows: 715 us of 4.03 GB, 83 %,
-// with 104 to 128 bytes of spill stores (the 16-bit types have none).
+// plain copy's rate); two blocks an SM at 128 registers, three at 80 spill (599 us). fp32 rows: 661 us of 4.03 GB, 91 %.
+// With positions along three axes: 463 us in bf16, 87 %; fp32 674 us, 89 %.
 #include <cuda_bf16.h>
 
 #include "kvarn_common.cuh"
@@ -101,7 +101,9 @@ __device__ __forceinline__ void rope_store(uint16_t* dst, const float (&x)[8]) {
 template <class T, bool kInter>
 __device__ __forceinline__ void rope_rows(const T* src, uint16_t* dst, int heads, int p0, int p1, const float* w, float eps,
                                           bool turn, const float2* c, int ch0, int ch1, bool rot0, bool rot1) {
-  constexpr int kBatch = 2;   // passes in flight: 456 us for 65536 tokens of 64 + 8 + 8 rows; 1 548, 4 478 (spills)
+  // passes in flight: 456 us for 65536 tokens of 64 + 8 + 8 rows, fp16; 1 548, 4 478 (spills). Two of
+  // fp32 rows spill: 30000 tokens 341 us, one 312.
+  constexpr int kBatch = sizeof(T) == 4 ? 1 : 2;
   const int row = (threadIdx.x & 31) >> 3;
   // a pair is (xa, xb): channels i of the two groups, or two neighbours of one
   float ca[8], sa[8], cb[8], sb[8];                // w cos, w sin of a pair's members
@@ -335,10 +337,18 @@ cudaError_t launch_rope_any(const void* q, const void* k, const void* v, const k
   a.passes[1] = (hkv + 3) / 4;
   a.passes[2] = v != nullptr ? a.passes[1] : 0;
   // An item is a token and a warp's. Few tokens: their passes are split over several warps, so
-  // that a call of one token keeps more than one SM's loads in flight.
+  // that a call of one token keeps more than one SM's loads in flight. The split whose rounds over the
+  // GPU's warps take the fewest passes, an item's sines and cosines counted as three (split until there are as
+  // many items as warps instead: 1073 tokens of 40 + 8 + 8 rows 8.6 us, 7.4 so; 3000 of 64 + 8 + 8 33.5 and 29.8).
   const int64_t warps = 2 * static_cast<int64_t>(sms) * kRopeWarps, passes = a.passes[0] + a.passes[1] + a.passes[2];
-  const int64_t split = (warps + n - 1) / n;
-  a.split = static_cast<int>(split < passes ? split : passes);
+  int64_t least = INT64_MAX;
+  for (int64_t split = 1; split <= passes && (split == 1 || n * split <= 8 * warps); ++split) {
+    const int64_t cost = (n * split + warps - 1) / warps * ((passes + split - 1) / split + 3);
+    if (cost < least) {
+      least = cost;
+      a.split = static_cast<int>(split);
+    }
+  }
   int64_t grid = (n * a.split + kRopeWarps - 1) / kRopeWarps;
   if (grid > 2 * static_cast<int64_t>(sms)) grid = 2 * static_cast<int64_t>(sms);
   return r->dtype == KVARN_F16    ? launch_rope_type<__half>(a, axes, r->interleaved != 0, grid, stream)
