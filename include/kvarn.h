@@ -281,8 +281,9 @@ KVARN_API kvarn_status kvarn_decode_attention(const uint16_t* q, const uint8_t* 
                                     void* scratch, size_t scratch_bytes,
                                     const kvarn_meta* meta, void* stream);
 
-/* Bytes of device scratch kvarn_decode_attention_weights needs: the decode's, and 64 bytes for
- * each entry of weights (n_seqs * num_kv_heads * max_blocks_per_seq). 0 if an argument is invalid. */
+/* Bytes of device scratch kvarn_decode_attention_weights needs: the decode's, 64 bytes for each
+ * entry of weights (n_seqs * num_kv_heads * max_blocks_per_seq) and 128 for each of its rows.
+ * 0 if an argument is invalid. */
 KVARN_API size_t kvarn_decode_weights_scratch_bytes(const kvarn_meta* meta, int32_t n_seqs);
 
 /*
@@ -304,9 +305,10 @@ KVARN_API size_t kvarn_decode_weights_scratch_bytes(const kvarn_meta* meta, int3
  *                 overlap on the GPU must not share it (nor weights).
  * A tile that is not attended (its block outside [0, num_blocks)) gets weight 0 from the step; the
  * workspace tokens' weight is dropped where floor(L/128) is not below max_blocks_per_seq. Other
- * arguments, flags and launches are kvarn_decode_attention's; its limits of range do not
- * hold here (q_r r s and p c s are scaled per head and tile before they become fp16 pairs),
- * and KVARN_DECODE_SPLIT is not looked at.
+ * arguments and flags are kvarn_decode_attention's; its limits of range do not hold here
+ * (q_r r s and p c s are scaled per head and tile before they become fp16 pairs), and
+ * KVARN_DECODE_SPLIT is not looked at. Two or three launches, each a programmatic
+ * dependent of the one before. Groups of up to four q-heads take a form of their own, a quarter faster.
  */
 KVARN_API kvarn_status kvarn_decode_attention_weights(const uint16_t* q, const uint8_t* cache,
                                                       const uint16_t* workspace, const int32_t* block_tables,

@@ -9,14 +9,21 @@
 // The tile is the unit of weight because it is that of the record: its per-channel scales
 // bind 128 tokens, which cannot leave one record for another without being quantized again.
 //
-// Two launches, the second a programmatic dependent of the first:
+// Two launches (three for few units with many records), each a programmatic dependent of the one before:
 //   weigh_split_kernel - persistent, a CTA an SM. The packed tiles of all units (a unit is a sequence and
 //     kv-head) lie in one row, and each warp takes an equal part of it (a block finds its
 //     warps' parts with a scan over the lengths of its own). A warp copies its next tile into its stage while
 //     other warps of its scheduler compute, with the tile after that on its way into L2, and writes
 //     a partial record (output, maximum, sum) for each unit that it leaves;
 //   weigh_merge_kernel - a block a unit: attends the workspace tokens, joins the records,
-//     un-rotates, normalises, and writes the weights.
+//     un-rotates, normalises, and writes the weights (for few units a block a q-head, and
+//     weigh_tiles_kernel writes the weights).
+//
+// Bound by arithmetic: a tile and kv-head is 256 m16n8k16 products (2048 cycles of a scheduler's tensor pipe; the
+// legacy products are what small N needs, decode_tc.cuh has the tcgen05 form), 890 instructions of the ALU
+// pipe, two cycles each, and about 850 cycles of the fp32 pipe, which hardly overlap: measured 4110
+// cycles, ncu 50, 43 and 22 % of them. 64 x 16384 tokens, 64 heads over 8, k4v2: 236 us, 4.0 TB/s of records
+// (60 % of the copy rate; the plain decode 239), with groups of four 176 us, 80 %.
 #include "decode_tile.cuh"
 #include "kvarn_common.cuh"
 #include "kvarn_launch.h"
@@ -84,6 +91,7 @@ __device__ __forceinline__ Part find_part(const WeighArgs& a) {
   const int s0 = min(tid * per, a.n_seqs), s1 = min(s0 + per, a.n_seqs);
   int64_t own = 0;
   bool cut = false;
+#pragma unroll 4
   for (int s = s0; s < s1; ++s) {
     const int len = seq_len(a, s);
     own += tiles_of(a, len);
@@ -160,7 +168,7 @@ __device__ __forceinline__ void issue_record(uint8_t* stage, const uint8_t* src,
 }
 
 // ------------------------------------------------------------------ split
-template <int KB, int VB, bool kLean>
+template <int KB, int VB, bool kLean, bool kNarrow>
 __global__ void __launch_bounds__(WeighCfg<KB, VB, kLean>::kWarps * 32, 1) weigh_split_kernel(const __grid_constant__ WeighArgs a) {
   using Cfg = WeighCfg<KB, VB, kLean>;
   constexpr int kRecBytes = RecordLayout<KB, VB, kLean>::kBytes;
@@ -194,25 +202,22 @@ __global__ void __launch_bounds__(WeighCfg<KB, VB, kLean>::kWarps * 32, 1) weigh
   }
   if (left > 1) look_ahead();
 
-  float acc[16][2], m_run = -INFINITY, l_run = 0.f;
-#pragma unroll
-  for (int n = 0; n < 16; ++n) acc[n][0] = acc[n][1] = 0.f;
+  UnitState<kNarrow> state;
+  state.reset();
   int first = -1;                       // the warp's first tile of the unit
   for (uint32_t phase = 0;; phase ^= 1u) {
     const int64_t u = static_cast<int64_t>(cur.s) * a.hkv + cur.h;
     if (first < 0) {
       first = cur.it;
       float qv[8][4];
-      load_q(a, cur.s, cur.h, g, c, qv);
+      load_q(a, cur.s, cur.h, state.head(g), c, qv);
       store_q<KB>(qsm, qv);
     }
     float2* stat = a.stats + (u * a.max_blocks + cur.it) * 8;
     // (a copy that never arrives raises its flag and ends the warp)
     if (!__all_sync(0xffffffffu, mbar_wait(bar, phase, a.flags))) return;
     if (__shfl_sync(0xffffffffu, src != nullptr, 0)) {
-      float2 sc[16];
-      weigh_keys<KB, VB, kLean>(stage, qsm, g, c, sc);
-      weigh_values<KB, VB, kLean>(stage, sc, g, c, m_run, l_run, acc, stat);
+      state.template attend<KB, VB, kLean>(stage, qsm, g, c, stat);
     } else if (c == 0) {
       stat[g] = make_float2(-INFINITY, 0.f);
     }
@@ -220,22 +225,14 @@ __global__ void __launch_bounds__(WeighCfg<KB, VB, kLean>::kWarps * 32, 1) weigh
     const bool more = --left > 0, same = ++cur.it < cur.tiles;
     if (lane == 0 && more) issue_record<kRecBytes>(stage, ahead, bar);
     if (!more || !same) {               // the warp's last tile of the unit
-      if (g < a.group) {
-        float* rec = a.part + (id + u) * kRecFloats + g * kPartStride;
-#pragma unroll
-        for (int n = 0; n < 16; ++n) *reinterpret_cast<float2*>(rec + 8 * n + 2 * c) = make_float2(acc[n][0], acc[n][1]);
-        if (c == 0) *reinterpret_cast<float2*>(rec + 128) = make_float2(m_run, l_run);
-      }
+      state.write(a.part + (id + u) * kRecFloats, kPartStride, a.group, g, c);
       if (lane == 0) {                  // the unit's first and last warp
         if (first == 0) a.cover[2 * u] = id;
         if (!same) a.cover[2 * u + 1] = id;
       }
       if (!more) return;
       first = -1;
-      m_run = -INFINITY;
-      l_run = 0.f;
-#pragma unroll
-      for (int n = 0; n < 16; ++n) acc[n][0] = acc[n][1] = 0.f;
+      state.reset();
       cur = next;
     }
     src = ahead;
@@ -517,15 +514,20 @@ __global__ void __launch_bounds__(256) weigh_tiles_kernel(const __grid_constant_
   weigh_unit(a, u, len, a.ws != nullptr ? len % kB : 0, heads, blockIdx.z * 256 + threadIdx.x, gridDim.z * 256);
 }
 
-template <int KB, int VB, bool kLean>
-cudaError_t launch_weigh(WeighArgs& a, cudaStream_t stream) {
+template <int KB, int VB, bool kLean, bool kNarrow>
+cudaError_t launch_split(const WeighArgs& a, cudaStream_t stream) {
   using C = WeighCfg<KB, VB, kLean>;
   static std::atomic<unsigned long long> smem_set{0};
-  const cudaError_t err = set_smem_once(weigh_split_kernel<KB, VB, kLean>, C::kSmem, smem_set);
+  const cudaError_t err = set_smem_once(weigh_split_kernel<KB, VB, kLean, kNarrow>, C::kSmem, smem_set);
   if (err != cudaSuccess) return err;
-  a.warps = C::kWarps;
-  weigh_split_kernel<KB, VB, kLean><<<a.n_ctas, C::kWarps * 32, C::kSmem, stream>>>(a);
+  weigh_split_kernel<KB, VB, kLean, kNarrow><<<a.n_ctas, C::kWarps * 32, C::kSmem, stream>>>(a);
   return cudaGetLastError();
+}
+
+template <int KB, int VB, bool kLean>
+cudaError_t launch_weigh(WeighArgs& a, cudaStream_t stream) {
+  a.warps = WeighCfg<KB, VB, kLean>::kWarps;
+  return a.group <= 4 ? launch_split<KB, VB, kLean, true>(a, stream) : launch_split<KB, VB, kLean, false>(a, stream);
 }
 
 // Scratch: the partial records and marks (within the decode's), HeadEnds, (m, l) of the tiles.

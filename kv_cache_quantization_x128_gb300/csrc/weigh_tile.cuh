@@ -150,18 +150,9 @@ __device__ __forceinline__ void store_q(float4* qsm, const float (&qv)[8][4]) {
                                     : make_float4(qv[q][0], qv[q][1], qv[q][2], qv[q][3]);
 }
 
-// One packed tile, rotated domain, in two halves (the keys' part of the stage is free again behind the first): as
-// attend_tile (decode_tile.cuh), but q' and p' on grids (make_operand). The scores, log2 domain, of
-// head g and tokens 8 nt + 2 c + {0, 1}; qsm[32 q]: q_r of the thread's operand group q (store_q).
-template <int KB, int VB, bool kLean>
-__device__ __forceinline__ void weigh_keys(const uint8_t* rec, const float4* qsm, int g, int c, float2 (&sc)[16]) {
-  using L = RecordLayout<KB, VB, kLean>;
-  const uint16_t* km = reinterpret_cast<const uint16_t*>(rec + L::kKMetaOff);
-
-  float2 E[8][2];
-  uint32_t A[8][4];
-  float2 sum2 = make_float2(0.f, 0.f);
-  float top = 0.f, f;
+// q' = q_r r s of a head's operand groups, the largest of them, and beta's terms.
+template <int KB, class L, bool kLean>
+__device__ __forceinline__ void fold_keys(const uint16_t* km, const float4* qsm, int c, float2 (&E)[8][2], float& top, float2& sum2) {
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
     const int ca = 16 * q + 2 * c, cb = ca + 8;
@@ -178,6 +169,21 @@ __device__ __forceinline__ void weigh_keys(const uint8_t* rec, const float4* qsm
       sum2 = __ffma2_rn(q2[odd], rz[odd], sum2);
     }
   }
+}
+
+// One packed tile, rotated domain, in two halves: as
+// attend_tile (decode_tile.cuh), but q' and p' on grids (make_operand). The scores, log2 domain, of
+// head g and tokens 8 nt + 2 c + {0, 1}; qsm[32 q]: q_r of the thread's operand group q (store_q).
+template <int KB, int VB, bool kLean>
+__device__ __forceinline__ void weigh_keys(const uint8_t* rec, const float4* qsm, int g, int c, float2 (&sc)[16]) {
+  using L = RecordLayout<KB, VB, kLean>;
+  const uint16_t* km = reinterpret_cast<const uint16_t*>(rec + L::kKMetaOff);
+
+  float2 E[8][2];
+  uint32_t A[8][4];
+  float2 sum2 = make_float2(0.f, 0.f);
+  float top = 0.f, f;
+  fold_keys<KB, L, kLean>(km, qsm, c, E, top, sum2);
   make_operand<KB>(E, quad_max(top), f, A);
   const float beta = quad_sum(sum2.x + sum2.y);
   const float2 beta_2 = make_float2(beta, beta), kf2 = make_float2(f, f);
@@ -291,6 +297,286 @@ __device__ __forceinline__ void weigh_values(const uint8_t* rec, float2 (&sc)[16
     }
   }
 }
+
+// ------------------------------------------------------------------ groups of up to four q-heads
+// With four heads, hi and lo parts fill the eight columns of the other operand of the m16n8k16 products:
+// codes are A (16 tokens, then 16 channels, a product), columns 0-3 the heads' hi, 4-7 their lo
+// parts; half the products of the wide form above. Thread (g, c) folds head g % 4 (as its hi part
+// for g < 4, its lo part else), and holds, of heads 2 (c % 2) + {0, 1}: the scores of tokens 16 b + g + 8 (c / 2);
+// maximum and sum; and acc[2 n + e] = the part of channel 16 n + 8 e + g that came through hi columns
+// (c < 2) or lo columns, added up when the record is written.
+// 64 x 16384 tokens, 32 heads over 8: k4v2 176 us (the wide form 234), k4v4 224 (274), k2v2 173 (231).
+
+// x of head g % 4, the same in a quad, for the thread's two heads.
+__device__ __forceinline__ float2 two_heads(float x, int c) {
+  return make_float2(__shfl_sync(0xffffffffu, x, 8 * (c & 1)), __shfl_sync(0xffffffffu, x, 8 * (c & 1) + 4));
+}
+// Over the lanes that hold tokens of the thread's heads.
+__device__ __forceinline__ float2 token_max(float2 x) {
+#pragma unroll
+  for (int o = 2; o < 32; o <<= 1)
+    x = make_float2(fmaxf(x.x, __shfl_xor_sync(0xffffffffu, x.x, o)), fmaxf(x.y, __shfl_xor_sync(0xffffffffu, x.y, o)));
+  return x;
+}
+__device__ __forceinline__ float2 token_sum(float2 x) {
+#pragma unroll
+  for (int o = 2; o < 32; o <<= 1)
+    x = __fadd2_rn(x, make_float2(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o)));
+  return x;
+}
+// Product of two fp16 numbers in fp32 (exact).
+__device__ __forceinline__ float mul_h(uint16_t a, uint16_t b) {
+  float r;
+  asm("fma.rn.f32.f16 %0, %1, %2, 0f00000000;" : "=f"(r) : "h"(a), "h"(b));
+  return r;
+}
+
+// A operands of one word of each of two rows of codes (r: row g, s: row g + 8), and their products.
+template <int BITS, bool kMasked>
+__device__ __forceinline__ void mma_rows(float* d, const uint32_t (&B)[8][2], int m, uint32_t r, uint32_t s) {
+  constexpr int kSteps = 8 / BITS;
+  uint32_t a[kSteps][4];
+  const uint32_t w[2] = {r, s};
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if constexpr (kMasked) {
+      static_assert(BITS == 4, "see Masked");
+      const uint32_t h = w[e] >> 8;
+      a[0][e] = w[e] & 0x000F000Fu; a[0][e + 2] = h & 0x000F000Fu; a[1][e] = w[e] & 0x00F000F0u; a[1][e + 2] = h & 0x00F000F0u;
+    } else if constexpr (BITS == 4) {
+      cvt4(w[e] & 0x0F0F0F0Fu, a[0][e], a[0][e + 2]);
+      cvt4((w[e] >> 4) & 0x0F0F0F0Fu, a[1][e], a[1][e + 2]);
+    } else {
+      uint32_t x[4], y[4];
+      cvt2(w[e] & 0x33333333u, x);
+      cvt2((w[e] >> 2) & 0x33333333u, y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i][e] = x[i];
+        a[i][e + 2] = y[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    if (m == 0 && i == 0) mma16816_first(d, a[0], B[0][0], B[0][1]);
+    else mma16816(d, a[i], B[kSteps * m + i][0], B[kSteps * m + i][1]);
+  }
+}
+
+// The first half: sc[b] = the scores of the thread's two heads and token 16 b + g + 8 (c / 2).
+template <int KB, int VB, bool kLean>
+__device__ __forceinline__ void narrow_keys(const uint8_t* rec, const float4* qsm, int g, int c, float2 (&sc)[8]) {
+  using L = RecordLayout<KB, VB, kLean>;
+  const uint16_t* km = reinterpret_cast<const uint16_t*>(rec + L::kKMetaOff);
+  uint32_t B[8][2];
+  float2 f2, beta2;
+  {
+    float2 E[8][2], sum2 = make_float2(0.f, 0.f);
+    uint32_t A[8][4];
+    float top = 0.f, f;
+    fold_keys<KB, L, kLean>(km, qsm, c, E, top, sum2);
+    make_operand<KB>(E, quad_max(top), f, A);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      B[q][0] = g < 4 ? A[q][0] : A[q][1];
+      B[q][1] = g < 4 ? A[q][2] : A[q][3];
+    }
+    f2 = two_heads(f, c);
+    beta2 = two_heads(quad_sum(sum2.x + sum2.y), c);
+  }
+  const bool hi = c < 2;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {           // four blocks of 16 tokens at a time (independent chains)
+    float d[4][4];
+    uint32_t kw[4][2][KB];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint8_t* row = rec + L::kKCodeOff + (16 * (4 * half + i) + 8 * e + g) * (16 * KB) + c * (4 * KB);
+        if constexpr (KB == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(row);
+          kw[i][e][0] = v.x; kw[i][e][1] = v.y; kw[i][e][2] = v.z; kw[i][e][3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(row);
+          kw[i][e][0] = v.x; kw[i][e][1] = v.y;
+        }
+      }
+#pragma unroll
+    for (int m = 0; m < KB; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mma_rows<KB, Masked<KB>::value>(d[i], B, m, kw[i][0][m], kw[i][1][m]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int b = 4 * half + i;
+      // hi parts stand in lanes c < 2, lo parts two lanes on; each keeps one of the two tokens
+      const float2 keep = hi ? make_float2(d[i][0], d[i][1]) : make_float2(d[i][2], d[i][3]);
+      const float2 give = hi ? make_float2(d[i][2], d[i][3]) : make_float2(d[i][0], d[i][1]);
+      const float2 got = make_float2(__shfl_xor_sync(0xffffffffu, give.x, 2), __shfl_xor_sync(0xffffffffu, give.y, 2));
+      const float ck = h2f_bits(km[L::kKc + 16 * b + g + 8 * (c >> 1)]);
+      sc[b] = __fmul2_rn(make_float2(ck, ck), __ffma2_rn(__fadd2_rn(keep, got), f2, beta2));
+    }
+  }
+}
+
+// The second half, as weigh_values; m and l of the thread's two heads, stat as there.
+template <int KB, int VB, bool kLean>
+__device__ __forceinline__ void narrow_values(const uint8_t* rec, float2 (&sc)[8], int g, int c, float2& m_run, float2& l_run,
+                                              float (&acc)[16][2], float2* stat) {
+  using L = RecordLayout<KB, VB, kLean>;
+  const uint16_t* vm = reinterpret_cast<const uint16_t*>(rec + L::kVMetaOff);
+  float2 top = sc[0];
+#pragma unroll
+  for (int b = 1; b < 8; ++b) top = make_float2(fmaxf(top.x, sc[b].x), fmaxf(top.y, sc[b].y));
+  top = token_max(top);
+  const bool ux = top.x > m_run.x + 8.f, uy = top.y > m_run.y + 8.f;     // (raise_max's rule)
+  if (__any_sync(0xffffffffu, ux || uy)) {
+    const float2 m_new = make_float2(ux ? top.x : m_run.x, uy ? top.y : m_run.y);
+    const float2 corr = make_float2(ux ? ex2(m_run.x - m_new.x) : 1.f, uy ? ex2(m_run.y - m_new.y) : 1.f);
+    m_run = m_new;
+    l_run = __fmul2_rn(l_run, corr);
+#pragma unroll
+    for (int n = 0; n < 16; ++n) {
+      const float2 v = __fmul2_rn(make_float2(acc[n][0], acc[n][1]), corr);
+      acc[n][0] = v.x;
+      acc[n][1] = v.y;
+    }
+  }
+  float2 lt = make_float2(0.f, 0.f), sum2 = lt;
+  top = lt;
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    const int t = 16 * b + g + 8 * (c >> 1);
+    const float2 p = make_float2(ex2(sc[b].x - m_run.x), ex2(sc[b].y - m_run.y));
+    const uint16_t vc = kLean ? 0x3C00 : vm[L::kVc + t];
+    const float cs = mul_h(vc, vm[L::kVs + t]), cz = mul_h(vc, vm[L::kVz + t]);
+    lt = __fadd2_rn(lt, p);
+    sum2 = __ffma2_rn(p, make_float2(cz, cz), sum2);
+    sc[b] = __fmul2_rn(p, make_float2(cs, cs));
+    top = make_float2(fmaxf(top.x, fabsf(sc[b].x)), fmaxf(top.y, fabsf(sc[b].y)));
+  }
+  lt = token_sum(lt);
+  l_run = __fadd2_rn(l_run, lt);
+  if (g == 0 && c < 2) *reinterpret_cast<float4*>(stat + 2 * c) = make_float4(m_run.x, lt.x, m_run.y, lt.y);
+  top = token_max(top);
+  float2 up, f2;
+  range_scale(top.x, up.x, f2.x);
+  range_scale(top.y, up.y, f2.y);
+  constexpr float kf = VB == 4 ? 8.f : 2.f;        // (conversions give code / 8 and code / 2)
+  f2 = __fmul2_rn(f2, make_float2(kf, kf));
+  const bool hi = c < 2;
+  const float2 gamma = token_sum(sum2), g2 = hi ? gamma : make_float2(0.f, 0.f);   // (once: with the hi parts)
+  // p' of both heads as one fp16 pair a token; rows of 8 tokens (hi parts in lanes c < 2, lo parts two lanes on), transposed
+  uint32_t B[8][2];
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    uint32_t h, l;
+    split2p(__fmul2_rn(sc[b], up), h, l);
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? l : h, 2);
+    const uint32_t r0 = hi ? h : got, r1 = hi ? got : l;       // tokens 16 b + g and 16 b + 8 + g
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(B[b][0]) : "r"(r0));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(B[b][1]) : "r"(r1));
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {           // four blocks of 16 channels at a time
+    float d[4][4];
+    uint32_t vw[4][2][VB];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = 4 * half + i;
+      if constexpr (VB == 4) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint4 v = *reinterpret_cast<const uint4*>(rec + L::kVCodeOff + (16 * n + 8 * e + g) * 64 + c * 16);
+          vw[i][e][0] = v.x; vw[i][e][1] = v.y; vw[i][e][2] = v.z; vw[i][e][3] = v.w;
+        }
+      } else {                                     // a cell serves channel g of a 16-channel panel and its partner g + 8
+        const uint4 v = *reinterpret_cast<const uint4*>(rec + L::kVCodeOff + n * 512 + (g * 4 + c) * 16);
+        vw[i][0][0] = v.x; vw[i][0][1] = v.y; vw[i][1][0] = v.z; vw[i][1][1] = v.w;
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < VB; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mma_rows<VB, false>(d[i], B, m, vw[i][0][m], vw[i][1][m]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int n = 2 * (4 * half + i) + e;
+        const float r = h2f_bits(vm[L::kVr + 8 * n + g]);
+        const float2 v = __ffma2_rn(make_float2(r, r), __ffma2_rn(make_float2(d[i][2 * e], d[i][2 * e + 1]), f2, g2),
+                                    make_float2(acc[n][0], acc[n][1]));
+        acc[n][0] = v.x;
+        acc[n][1] = v.y;
+      }
+  }
+}
+
+// ------------------------------------------------------------------ a warp's state of a unit
+// kNarrow: groups of up to four q-heads.
+template <bool kNarrow>
+struct UnitState;
+
+template <>
+struct UnitState<false> {
+  float acc[16][2], m, l;
+  __device__ __forceinline__ void reset() {
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int n = 0; n < 16; ++n) acc[n][0] = acc[n][1] = 0.f;
+  }
+  __device__ static __forceinline__ int head(int g) { return g; }          // that the thread folds
+  template <int KB, int VB, bool kLean>
+  __device__ __forceinline__ void attend(const uint8_t* rec, const float4* qsm, int g, int c, float2* stat) {
+    float2 sc[16];
+    weigh_keys<KB, VB, kLean>(rec, qsm, g, c, sc);
+    weigh_values<KB, VB, kLean>(rec, sc, g, c, m, l, acc, stat);
+  }
+  // rec: [head][stride]: 128 channels, maximum, sum
+  __device__ __forceinline__ void write(float* rec, int stride, int group, int g, int c) {
+    if (g >= group) return;
+    float* row = rec + g * stride;
+#pragma unroll
+    for (int n = 0; n < 16; ++n) *reinterpret_cast<float2*>(row + 8 * n + 2 * c) = make_float2(acc[n][0], acc[n][1]);
+    if (c == 0) *reinterpret_cast<float2*>(row + 128) = make_float2(m, l);
+  }
+};
+
+template <>
+struct UnitState<true> {
+  float acc[16][2];
+  float2 m, l;
+  __device__ __forceinline__ void reset() {
+    m = make_float2(-INFINITY, -INFINITY);
+    l = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int n = 0; n < 16; ++n) acc[n][0] = acc[n][1] = 0.f;
+  }
+  __device__ static __forceinline__ int head(int g) { return g & 3; }
+  template <int KB, int VB, bool kLean>
+  __device__ __forceinline__ void attend(const uint8_t* rec, const float4* qsm, int g, int c, float2* stat) {
+    float2 sc[8];
+    narrow_keys<KB, VB, kLean>(rec, qsm, g, c, sc);
+    narrow_values<KB, VB, kLean>(rec, sc, g, c, m, l, acc, stat);
+  }
+  __device__ __forceinline__ void write(float* rec, int stride, int group, int g, int c) {
+#pragma unroll
+    for (int n = 0; n < 16; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) acc[n][k] += __shfl_xor_sync(0xffffffffu, acc[n][k], 2);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int h = 2 * c + k;
+      if (c >= 2 || h >= group) continue;
+#pragma unroll
+      for (int n = 0; n < 16; ++n) rec[h * stride + 8 * n + g] = acc[n][k];
+      if (g == 0) *reinterpret_cast<float2*>(rec + h * stride + 128) = k ? make_float2(m.y, l.y) : make_float2(m.x, l.x);
+    }
+  }
+};
 
 }  // namespace
 }  // namespace kvarn
