@@ -193,6 +193,16 @@ __global__ void __launch_bounds__(kEvictMaxThreads) evict_select_kernel(const Ev
   float* wo = a.weights_out + u * a.max_blocks;
   int32_t* kept = a.kept + u * a.max_blocks;
   int32_t* list = a.list_slots > 0 ? reinterpret_cast<int32_t*>(keys + a.key_slots) : kept;
+  const int32_t* table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks;
+  // a thread's first two tiles, in flight with the length
+  float w2[2] = {0.f, 0.f};
+  int32_t blk2[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (tid + j * threads < a.max_blocks) {
+      w2[j] = w[tid + j * threads];
+      blk2[j] = table[tid + j * threads];
+    }
   const int length = a.seq_lens[s], budget = a.budgets[s];
   const int tiles = max(length, 0) / kB, n = min(tiles, a.max_blocks), b = budget < 0 ? n : min(n, budget);
   const int first = min(a.first, b), last = min(a.last, b - first);
@@ -201,13 +211,14 @@ __global__ void __launch_bounds__(kEvictMaxThreads) evict_select_kernel(const Ev
   if (!sound && tid == 0) raise_flag(a.flags, KVARN_FLAG_BAD_LENGTH);
   if (b < n && sound) {                 // every block that could be read or written, and the keys
     bool ok = true;
-#pragma unroll 2
-    for (int t = tid; t < n; t += threads) {
-      const int64_t blk = a.block_tables[static_cast<int64_t>(s) * a.max_blocks + t];
-      const float x = w[t];
+    auto look = [&](int t, int64_t blk, float x) {
       ok &= blk >= 0 && blk < a.num_blocks;
       if (t < a.key_slots) keys[t] = weight_key(x);
-    }
+    };
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (tid + j * threads < n) look(tid + j * threads, blk2[j], w2[j]);
+    for (int t = tid + 2 * threads; t < n; t += threads) look(t, table[t], w[t]);
     sound = __syncthreads_and(ok);
     if (!sound && tid == 0) raise_flag(a.flags, KVARN_FLAG_BAD_BLOCK);
   }
@@ -285,14 +296,15 @@ __global__ void __launch_bounds__(kEvictMaxThreads) evict_select_kernel(const Ev
 
 template <int kPieces>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
-  griddep_wait();                       // the slots and the lengths
   const int64_t u = blockIdx.x / a.per_unit;
   const int part = blockIdx.x - static_cast<int>(u) * a.per_unit;
   const int s = static_cast<int>(u / a.hkv), h = static_cast<int>(u - static_cast<int64_t>(s) * a.hkv);
-  const int length = a.seq_lens[s], n = min(max(length, 0) / kB, a.max_blocks);
-  const int dropped = (length - a.seq_lens_out[s]) / kB, b = n - dropped;
   const int32_t* kept = a.kept + u * a.max_blocks;
   const int32_t* table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks;
+  const int length = a.seq_lens[s], budget = a.budgets[s], n = min(max(length, 0) / kB, a.max_blocks);
+  const int b = budget < 0 ? n : min(n, budget), dropped = n - b;
+  griddep_wait();                       // the slots and the lengths
+  if (dropped <= part || a.seq_lens_out[s] == length) return;       // (as it was: nothing to evict, or not sound)
   const int pieces = a.record_bytes / 16;
   for (int i = part; i < dropped; i += a.per_unit) {
     int slot = kept[b + i];
