@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvarn.so")
@@ -101,13 +102,10 @@ class KvarnRope(ctypes.Structure):
                 ("v_stride", ctypes.c_int64)]
 
 
-_Pairs = ctypes.c_uint8 * 64
-
-
 class KvarnAxes(ctypes.Structure):
     """Mirror of ``kvarn_axes``."""
     _fields_ = [("n_axes", ctypes.c_int32), ("reserved", ctypes.c_int32), ("position_stride", ctypes.c_int64),
-                ("axis", _Pairs)]
+                ("axis", ctypes.c_uint8 * 64)]
 
 
 class KvarnScore(ctypes.Structure):
@@ -159,7 +157,7 @@ def _ptr(t, name, dtype=None, numel=None):
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if numel is not None and t.numel() < numel:
         raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
@@ -282,9 +280,14 @@ def kvarn_prefill_attention(q, k_new, v_new, cu_tokens, seq_lens, max_chunk: int
                                         _ptr(out, "out", torch.float16), ctypes.byref(meta), _stream(stream)))
 
 
+_CODES = {}
+
+
 def _dtype_code(t, name):
-    import torch
-    code = {torch.float16: KVARN_F16, torch.bfloat16: KVARN_BF16, torch.float32: KVARN_F32}.get(t.dtype)
+    if not _CODES:
+        import torch
+        _CODES.update({torch.float16: KVARN_F16, torch.bfloat16: KVARN_BF16, torch.float32: KVARN_F32})
+    code = _CODES.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} must be torch.float16, torch.bfloat16 or torch.float32, got {t.dtype}")
     return code
@@ -307,7 +310,7 @@ def _device_call(lead, tensors, stream, call):
         raise ValueError(f"tensors are on {lead.device}, the stream is on {stream.device}")
     else:
         handle = stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         _check(call(handle))
     else:
         with torch.cuda.device(dev):
@@ -326,17 +329,23 @@ def _heads(t, name, n, heads, dtype):
     return row
 
 
+# kvarn_rope and kvarn_axes as bytes (a ctypes Structure costs 0.3 us a call more)
+_ROPE, _AXES = struct.Struct("=iiifqqq"), struct.Struct("=iiq64s")
+assert _ROPE.size == ctypes.sizeof(KvarnRope) and _AXES.size == ctypes.sizeof(KvarnAxes)
+
+
 def _rope_args(q, k, v, q_out, k_out, v_out, meta, q_weight, k_weight, norm_eps, inv_freq, interleaved):
     """The C arguments that the norm and rotation calls share: the rows up to their
     kvarn_rope, and those behind it."""
     import torch
     n, hq, hkv = int(q.shape[0]), meta.num_q_heads, meta.num_kv_heads
     f16 = torch.float16
-    rope = KvarnRope(_dtype_code(q, "q"), HEAD_DIM if inv_freq is None else 2 * inv_freq.numel(), int(bool(interleaved)),
-                     norm_eps, _heads(q, "q", n, hq, q.dtype), _heads(k, "k", n, hkv, q.dtype),
-                     0 if v is None else _heads(v, "v", n, hkv, q.dtype))
-    return ((q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(), ctypes.byref(rope)),
-            (_ptr(q_weight, "q_weight", q.dtype, HEAD_DIM), _ptr(k_weight, "k_weight", q.dtype, HEAD_DIM),
+    dtype = q.dtype
+    rope = _ROPE.pack(_dtype_code(q, "q"), HEAD_DIM if inv_freq is None else 2 * inv_freq.numel(), 1 if interleaved else 0,
+                      norm_eps, _heads(q, "q", n, hq, dtype), _heads(k, "k", n, hkv, dtype),
+                      0 if v is None else _heads(v, "v", n, hkv, dtype))
+    return ((q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(), rope),
+            (_ptr(q_weight, "q_weight", dtype, HEAD_DIM), _ptr(k_weight, "k_weight", dtype, HEAD_DIM),
              _ptr(inv_freq, "inv_freq", torch.float32), _ptr(q_out, "q_out", f16, n * hq * HEAD_DIM),
              _ptr(k_out, "k_out", f16, n * hkv * HEAD_DIM),
              None if v is None else _ptr(v_out, "v_out", f16, n * hkv * HEAD_DIM), ctypes.byref(meta)))
@@ -375,8 +384,8 @@ def kvarn_qk_norm_rope_axes(q, k, v, positions, axes, q_out, k_out, v_out, meta:
         raise ValueError(f"axes must have {inv_freq.numel()} entries, one for each pair, got {len(axes)}")
     of_pair = bytes(axes if isinstance(axes, (list, tuple)) else [int(x) for x in axes])
     rows, rest = _rope_args(q, k, v, q_out, k_out, v_out, meta, q_weight, k_weight, norm_eps, inv_freq, interleaved)
-    split = KvarnAxes(int(positions.shape[0]), 0, positions.stride(0), _Pairs.from_buffer_copy(of_pair[:64].ljust(64, b"\0")))
-    args = (*rows, ctypes.byref(split), *rest[:3], positions.data_ptr(), n, *rest[3:])
+    split = _AXES.pack(int(positions.shape[0]), 0, positions.stride(0), of_pair)
+    args = (*rows, split, *rest[:3], positions.data_ptr(), n, *rest[3:])
     _device_call(q, (k, v, positions, q_out, k_out, v_out, q_weight, k_weight, inv_freq), stream,
                  lambda st: _lib.kvarn_qk_norm_rope_axes(*args, st))
 
