@@ -297,6 +297,7 @@ KVARN_API size_t kvarn_decode_weights_scratch_bytes(const kvarn_meta* meta, int3
  * decay 1 the weights are plain sums; below 1 old steps fade; with 0 the entry is replaced (what it
  * held is not looked at). Sums are fp32, in the same order at every call.
  *   decay         in [0, 1], not subnormal.
+ *   out           must not overlap q (KVARN_EINVAL).
  *   weights       float [n_seqs][num_kv_heads][max_blocks_per_seq].
  *   lse           float [n_seqs][num_q_heads] or NULL: ln of the sum of exp(score) over the
  *                 attended tokens (-inf where there are none), to join the rows with

@@ -271,6 +271,10 @@ kvarn_status kvarn_decode_attention_weights(const uint16_t* q, const uint8_t* ca
   KV_TRY(need_ptr(scratch, "scratch"));
   if (scratch_bytes < need)
     return fail(KVARN_ESCRATCH, "scratch too small: need %lld bytes", static_cast<long long>(need));
+  // (the merge's blocks read the rows of q for the workspace tokens while others write out)
+  const uint64_t row_bytes = static_cast<uint64_t>(n_seqs) * meta->num_q_heads * KVARN_HEAD_DIM * sizeof(uint16_t);
+  const uintptr_t q_at = reinterpret_cast<uintptr_t>(q), out_at = reinterpret_cast<uintptr_t>(out);
+  if (q_at - out_at < row_bytes || out_at - q_at < row_bytes) return fail(KVARN_EINVAL, "out must not overlap q");
   unsigned* fl = nullptr;
   KV_TRY(flags_ptr(&fl));
   return cuda_status(kvarn::launch_decode_weights(q, cache, workspace, block_tables, seq_lens, n_seqs, meta->num_kv_heads,

@@ -136,6 +136,14 @@ def test_weights_refusals(kv):
     assert _weigh(kv, wide) == 2
 
 
+def test_weights_out_over_q(kv):
+    m, size = kv.make_meta(8, 64, 16, max_blocks_per_seq=4), 4 * 64 * 128 * 2
+    q = 1 << 32
+    for out in (q, q + 16, q - 16, q + size - 16, q - size + 16):
+        assert _weigh(kv, m, q=ctypes.c_void_p(q), out=ctypes.c_void_p(out)) == 1, out - q
+        assert b"overlap" in kv._lib.kvarn_last_error(), out - q
+
+
 def test_evict_refusals(kv):
     def call(m=kv.make_meta(8, 64, 16, max_blocks_per_seq=4), n=4, first=1, last=1, **ptr):
         p = dict(w=A, wo=A, lens=A, lo=B, bt=A, budgets=A, kept=A, cache=A) | ptr
