@@ -36,19 +36,21 @@ struct EvictArgs {
   int64_t num_blocks;
   int n_seqs, hkv, max_blocks;
   int first, last;
-  int key_slots;                // keys held in shared memory, and behind them
+  int key_slots;                // keys held in shared memory (of the first tiles to choose from), and behind them
   int list_slots;               // max_blocks where the slots' list is held there too, 0 where `kept` is the list
   int per_unit;                 // blocks of the move kernel a (sequence, kv-head)
   int record_bytes;
 };
 
 constexpr int kEvictMaxThreads = 1024;
-constexpr int kKeySlots = 10240;      // 40 KB; weights of further tiles are read again for every two bits
+// 40 KB. Keys are held by their place among the tiles to choose from, lo .. hi - 1, which may lie anywhere
+// in the row (a long keep_first); weights behind the held ones are read again for every two bits.
+constexpr int kKeySlots = 10240;
 constexpr int kListSlots = 5120;      // the most blocks of a row whose list is held beside the keys
 // Up to so many tiles to choose from are one warp's: every warp of a block with tiles of its own and barriers between
 // the counts took 2048 blocks of 256 tiles 22 us, bound by instructions, where the warp takes 11.
 constexpr int kWarpTiles = 512;
-static_assert(kWarpTiles <= kKeySlots, "its keys are held");
+static_assert(kWarpTiles <= kKeySlots, "its keys, of places 0 .. kWarpTiles - 1, are held");
 constexpr int kMoveThreads = 128;
 
 // Whole numbers in the order of the weights: -0 as 0, NaN below everything.
@@ -57,21 +59,21 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return w != w ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// Of the keys of tiles lo .. hi - 1, the smallest that stays where `quota` (0 < quota < hi - lo) stay: it is above `cut`, or is `cut` for
-// the first `ties` tiles that have it. One warp, with KPL keys a lane in registers.
+// Of the keys at places 0 .. count - 1, the smallest that stays where `quota` (0 < quota < count) stay: it is above `cut`, or is `cut` for
+// the first `ties` places that have it. One warp, with KPL keys a lane in registers (count <= 32 KPL, all held).
 //   Few tiles to evict (a sequence at its budget has one): the smallest key, then the next one, ...
 //   until enough are counted.
 //   Else two bits at a time from the top: three counts each, until one leaves exactly the quota.
 template <int KPL>
-__device__ __forceinline__ void search_warp(const uint32_t* keys, int lo, int hi, int quota, uint32_t& cut, int& ties) {
-  constexpr uint32_t kAll = 0xffffffffu;           // above every key: what is behind hi
+__device__ __forceinline__ void search_warp(const uint32_t* keys, int count, int quota, uint32_t& cut, int& ties) {
+  constexpr uint32_t kAll = 0xffffffffu;           // above every key: what is behind the last
   uint32_t k[KPL];
 #pragma unroll
   for (int j = 0; j < KPL; ++j) {
-    const int i = lo + static_cast<int>(threadIdx.x & 31) + 32 * j;
-    k[j] = i < hi ? keys[i] : kAll;
+    const int i = static_cast<int>(threadIdx.x & 31) + 32 * j;
+    k[j] = i < count ? keys[i] : kAll;
   }
-  const int evict = hi - lo - quota;
+  const int evict = count - quota;
   if (evict <= 4) {
     bool any = false;
     int below = 0;                                 // keys up to `cut`
@@ -90,7 +92,7 @@ __device__ __forceinline__ void search_warp(const uint32_t* keys, int lo, int hi
     ties = below - evict;
     return;
   }
-  const int want = quota + KPL * 32 - (hi - lo);   // (what is behind hi is counted too)
+  const int want = quota + KPL * 32 - count;       // (what is behind the last is counted too)
   cut = 0;
   ties = 0;
 #pragma unroll 1
@@ -119,20 +121,20 @@ __device__ __forceinline__ void search_warp(const uint32_t* keys, int lo, int hi
   ties = want - __reduce_add_sync(kAll, c);
 }
 
-// The same for any number of tiles, by the whole block; keys from `slots` on come from the weights.
-__device__ __forceinline__ void search_block(const uint32_t* keys, int slots, const float* w, int lo, int hi, int quota, uint32_t& cut,
+// The same for any number of tiles, by the whole block; keys from place `slots` on come from the weights w.
+__device__ __forceinline__ void search_block(const uint32_t* keys, int slots, const float* w, int count, int quota, uint32_t& cut,
                                              int& ties) {
   __shared__ int sums[2][3][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   // a thread's first two keys stay in registers (0 where there is none: below every threshold)
-  const int i0 = lo + static_cast<int>(threadIdx.x), i1 = i0 + static_cast<int>(blockDim.x);
-  const uint32_t key0 = i0 < min(hi, slots) ? keys[i0] : i0 < hi ? weight_key(w[i0]) : 0u;
-  const uint32_t key1 = i1 < min(hi, slots) ? keys[i1] : i1 < hi ? weight_key(w[i1]) : 0u;
-  auto count = [&](int (&c)[3], uint32_t k0, uint32_t k1, uint32_t k2, int (*sm)[32]) {
+  const int i0 = static_cast<int>(threadIdx.x), i1 = i0 + static_cast<int>(blockDim.x);
+  const uint32_t key0 = i0 < min(count, slots) ? keys[i0] : i0 < count ? weight_key(w[i0]) : 0u;
+  const uint32_t key1 = i1 < min(count, slots) ? keys[i1] : i1 < count ? weight_key(w[i1]) : 0u;
+  auto tally = [&](int (&c)[3], uint32_t k0, uint32_t k1, uint32_t k2, int (*sm)[32]) {
     c[0] = (key0 >= k0) + (key1 >= k0);
     c[1] = (key0 >= k1) + (key1 >= k1);
     c[2] = (key0 >= k2) + (key1 >= k2);
-    for (int i = i1 + static_cast<int>(blockDim.x); i < hi; i += static_cast<int>(blockDim.x)) {
+    for (int i = i1 + static_cast<int>(blockDim.x); i < count; i += static_cast<int>(blockDim.x)) {
       const uint32_t k = i < slots ? keys[i] : weight_key(w[i]);
       c[0] += k >= k0;
       c[1] += k >= k1;
@@ -153,7 +155,7 @@ __device__ __forceinline__ void search_block(const uint32_t* keys, int slots, co
 #pragma unroll 1
   for (int bit = 30; bit >= 0; bit -= 2) {         // (sums alternate: a barrier lies between their uses)
     const uint32_t k0 = cut | 1u << bit, k1 = cut | 2u << bit, k2 = cut | 3u << bit;
-    count(c, k0, k1, k2, sums[bit >> 1 & 1]);
+    tally(c, k0, k1, k2, sums[bit >> 1 & 1]);
     const int most = c[2] >= quota ? c[2] : c[1] >= quota ? c[1] : c[0];
     cut = c[2] >= quota ? k2 : c[1] >= quota ? k1 : c[0] >= quota ? k0 : cut;
     if (most == quota) {
@@ -162,7 +164,7 @@ __device__ __forceinline__ void search_block(const uint32_t* keys, int slots, co
     }
   }
   // (no key has all bits set, so cut + 1 does not wrap: that would be a NaN's)
-  count(c, cut + 1u, cut + 1u, cut + 1u, sums[1]);
+  tally(c, cut + 1u, cut + 1u, cut + 1u, sums[1]);
   ties = quota - c[0];
 }
 
@@ -209,13 +211,14 @@ __global__ void __launch_bounds__(kEvictMaxThreads) evict_select_kernel(const Ev
   const int tiles = max(length, 0) / kB, n = min(tiles, a.max_blocks), b = budget < 0 ? n : min(n, budget);
   const int first = min(a.first, b), last = min(a.last, b - first);
   const int lo = first, hi = n - last, quota = b - first - last, edge = b - last;
+  const unsigned held = static_cast<unsigned>(min(hi - lo, a.key_slots));    // keys in shared memory: of tiles lo ..
   bool sound = tiles <= a.max_blocks;
   if (!sound && tid == 0) raise_flag(a.flags, KVARN_FLAG_BAD_LENGTH);
   if (b < n && sound) {                 // every block that could be read or written, and the keys
     bool ok = true;
     auto look = [&](int t, int64_t blk, float x) {
       ok &= blk >= 0 && blk < a.num_blocks;
-      if (t < a.key_slots) keys[t] = weight_key(x);
+      if (static_cast<unsigned>(t - lo) < held) keys[t - lo] = weight_key(x);
     };
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -239,10 +242,10 @@ __global__ void __launch_bounds__(kEvictMaxThreads) evict_select_kernel(const Ev
   const bool choose = quota > 0 && quota < hi - lo;
   if (choose && hi - lo <= kWarpTiles) {
     if (tid < 32) {
-      if (hi - lo <= 64) search_warp<2>(keys, lo, hi, quota, cut, ties);
-      else if (hi - lo <= 128) search_warp<4>(keys, lo, hi, quota, cut, ties);
-      else if (hi - lo <= 256) search_warp<8>(keys, lo, hi, quota, cut, ties);
-      else search_warp<16>(keys, lo, hi, quota, cut, ties);
+      if (hi - lo <= 64) search_warp<2>(keys, hi - lo, quota, cut, ties);
+      else if (hi - lo <= 128) search_warp<4>(keys, hi - lo, quota, cut, ties);
+      else if (hi - lo <= 256) search_warp<8>(keys, hi - lo, quota, cut, ties);
+      else search_warp<16>(keys, hi - lo, quota, cut, ties);
       if (tid == 0) {
         found[0] = cut;
         found[1] = static_cast<uint32_t>(ties);
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(kEvictMaxThreads) evict_select_kernel(const Ev
     cut = found[0];
     ties = static_cast<int>(found[1]);
   } else if (choose) {
-    search_block(keys, a.key_slots, w, lo, hi, quota, cut, ties);
+    search_block(keys, a.key_slots, w + lo, hi - lo, quota, cut, ties);
   }
   int eq = 0, gone = 0, late = 0;       // ties, evicted tiles and moved tiles so far
   for (int i0 = lo; i0 < hi; i0 += threads) {
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(kEvictMaxThreads) evict_select_kernel(const Ev
     const bool live = i < hi;
     bool stays = live && !choose && quota > 0;
     if (choose) {
-      const uint32_t k = !live ? 0u : i < a.key_slots ? keys[i] : weight_key(w[i]);
+      const uint32_t k = !live ? 0u : i - lo < a.key_slots ? keys[i - lo] : weight_key(w[i]);
       stays = live && k > cut;
       if (ties > 0) {
         const bool tie = live && k == cut;
