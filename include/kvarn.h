@@ -304,8 +304,9 @@ KVARN_API size_t kvarn_decode_weights_scratch_bytes(const kvarn_meta* meta, int3
  *                 attention over other tokens.
  *   scratch       device buffer of >= kvarn_decode_weights_scratch_bytes(meta, n_seqs); calls that
  *                 overlap on the GPU must not share it (nor weights).
- * A tile that is not attended (its block outside [0, num_blocks)) gets weight 0 from the step; the
- * workspace tokens' weight is dropped where floor(L/128) is not below max_blocks_per_seq. Other
+ * A tile that is not attended (its block outside [0, num_blocks), or a partial one without a workspace)
+ * gets weight 0 from the step, and its old weight fades; the workspace tokens' weight is dropped where
+ * floor(L/128) is not below max_blocks_per_seq. Other
  * arguments and flags are kvarn_decode_attention's; its limits of range do not hold here
  * (q_r r s and p c s are scaled per head and tile before they become fp16 pairs), and
  * KVARN_DECODE_SPLIT is not looked at. Two or three launches, each a programmatic

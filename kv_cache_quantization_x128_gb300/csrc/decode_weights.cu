@@ -360,13 +360,13 @@ __device__ __forceinline__ void add_weight(const WeighArgs& a, float* at, float 
   *at = a.decay == 0.f ? w : fmaf(a.decay, *at, w);
 }
 
-// Tiles first, first + stride, ... of the unit, and (first == 0) its workspace tokens.
-__device__ __forceinline__ void weigh_unit(const WeighArgs& a, int64_t u, int len, int n_ws, const HeadEnd* heads, int first,
-                                           int stride) {
+// Tiles first, first + stride, ... of the unit, and (first == 0) its partial one, whose weight from the step is
+// 0 without a workspace (the old one fades all the same).
+__device__ __forceinline__ void weigh_unit(const WeighArgs& a, int64_t u, int len, const HeadEnd* heads, int first, int stride) {
   const int tiles = tiles_of(a, len), last = len / kB;
   float* row = a.weights + u * a.max_blocks;
   for (int t = first; t < tiles; t += stride) add_weight(a, row + t, tile_weight(a, a.stats + (u * a.max_blocks + t) * 8, heads));
-  if (first == 0 && n_ws > 0 && last < a.max_blocks) {
+  if (first == 0 && len % kB > 0 && last < a.max_blocks) {
     float w = 0.f;
     for (int g = 0; g < a.group; ++g) w += heads[g].tail;
     add_weight(a, row + last, w);
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(32 * kHeads * kShares, kHeads * kShares > 8 ? 
     *reinterpret_cast<uint2*>(out + (u * a.group + gg) * kD + 4 * lane) =
         make_uint2(r[0] | static_cast<uint32_t>(r[1]) << 16, r[2] | static_cast<uint32_t>(r[3]) << 16);
     if (lane == 0) {
-      const HeadEnd e{Mt, inv, tail * inv, 0.f};
+      const HeadEnd e{Mt, inv, tail == 0.f ? 0.f : tail * inv, 0.f};   // (as a tile's: a sum of 0 is none)
       if (kHeads == 8) heads[gg] = e;
       else reinterpret_cast<HeadEnd*>(a.ends)[u * 8 + gg] = e;
       if (a.lse != nullptr) a.lse[u * a.group + gg] = (Mt + log2f(l)) * 0.693147180559945309f;
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(32 * kHeads * kShares, kHeads * kShares > 8 ? 
   }
   if (kHeads == 8) {
     __syncthreads();
-    weigh_unit(a, u, len, n_ws, heads, threadIdx.x, blockDim.x);
+    weigh_unit(a, u, len, heads, threadIdx.x, blockDim.x);
   }
 }
 
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(256) weigh_tiles_kernel(const __grid_constant_
   griddep_wait();
   if (threadIdx.x < a.group) heads[threadIdx.x] = reinterpret_cast<const HeadEnd*>(a.ends)[u * 8 + threadIdx.x];
   __syncthreads();
-  weigh_unit(a, u, len, a.ws != nullptr ? len % kB : 0, heads, blockIdx.z * 256 + threadIdx.x, gridDim.z * 256);
+  weigh_unit(a, u, len, heads, blockIdx.z * 256 + threadIdx.x, gridDim.z * 256);
 }
 
 template <int KB, int VB, bool kLean, bool kNarrow>
