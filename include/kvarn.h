@@ -301,7 +301,8 @@ KVARN_API size_t kvarn_decode_weights_scratch_bytes(const kvarn_meta* meta, int3
  *   weights       float [n_seqs][num_kv_heads][max_blocks_per_seq].
  *   lse           float [n_seqs][num_q_heads] or NULL: ln of the sum of exp(score) over the
  *                 attended tokens (-inf where there are none), to join the rows with
- *                 attention over other tokens.
+ *                 attention over other tokens. Workspace keys whose score is -inf have no
+ *                 weight; a row of nothing else gets 0.
  *   scratch       device buffer of >= kvarn_decode_weights_scratch_bytes(meta, n_seqs); calls that
  *                 overlap on the GPU must not share it (nor weights).
  * A tile that is not attended (its block outside [0, num_blocks), or a partial one without a workspace)

@@ -297,11 +297,12 @@ __device__ __forceinline__ void weigh_ws(const WeighArgs& a, int64_t u, int n_ws
       mx = fmaxf(mx, p[nt][e]);
     }
   mx = quad_max(mx);
+  const float base = mx == -INFINITY ? 0.f : mx;   // (scores of minus infinity, of keys beyond fp16's end, are no weight)
 #pragma unroll
   for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      p[nt][e] = exp2f(p[nt][e] - mx);
+      p[nt][e] = exp2f(p[nt][e] - base);
       sum += p[nt][e];
     }
   sum = quad_sum(sum);
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(32 * kHeads * kShares, kHeads * kShares > 8 ? 
     for (int k = 0; k < 4; ++k) acc[k] *= kInvSqrt128;
     float tail = 0.f;
     for (int w = 0; w < n_wsw; ++w) {
-      const float f = exp2f(ws.m[w][wg] - Mt);
+      const float f = ws.l[w][wg] == 0.f ? 0.f : exp2f(ws.m[w][wg] - Mt);
       const float4 v = *reinterpret_cast<const float4*>(&ws.o[w][wg][4 * lane]);
       acc[0] = fmaf(v.x, f, acc[0]);
       acc[1] = fmaf(v.y, f, acc[1]);
