@@ -341,8 +341,9 @@ def _rope_args(q, k, v, q_out, k_out, v_out, meta, q_weight, k_weight, norm_eps,
     n, hq, hkv = int(q.shape[0]), meta.num_q_heads, meta.num_kv_heads
     f16 = torch.float16
     dtype = q.dtype
+    eps = norm_eps if 0.0 < norm_eps < 1.0 else 0.0    # (refused by the library; what is not a float would not pack)
     rope = _ROPE.pack(_dtype_code(q, "q"), HEAD_DIM if inv_freq is None else 2 * inv_freq.numel(), 1 if interleaved else 0,
-                      norm_eps, _heads(q, "q", n, hq, dtype), _heads(k, "k", n, hkv, dtype),
+                      eps, _heads(q, "q", n, hq, dtype), _heads(k, "k", n, hkv, dtype),
                       0 if v is None else _heads(v, "v", n, hkv, dtype))
     return ((q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(), rope),
             (_ptr(q_weight, "q_weight", dtype, HEAD_DIM), _ptr(k_weight, "k_weight", dtype, HEAD_DIM),
