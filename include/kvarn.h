@@ -339,11 +339,13 @@ KVARN_API kvarn_status kvarn_decode_attention_weights(const uint16_t* q, const u
  *   weights       float [n_seqs][num_kv_heads][max_blocks_per_seq].
  *   weights_out   the same, or weights itself: the weights of the tiles that stay by their new
  *                 slots, then entry n's (the partial tile's), then zeros.
- *   seq_lens_out  int32 [n_seqs]: seq_lens[s] - 128 (n - b). Must not alias seq_lens.
+ *   seq_lens_out  int32 [n_seqs]: seq_lens[s] - 128 (n - b).
  *   budgets       int32 [n_seqs].
  *   kept          int32 [n_seqs][num_kv_heads][max_blocks_per_seq], a permutation of a
  *                 row's slots: the old slots of the b tiles that stay, by new slot; the n - b
  *                 evicted slots, ascending; -1.
+ * weights_out, seq_lens_out and kept must not overlap one another, nor weights (but for
+ * weights_out being weights), seq_lens, block_tables and budgets (KVARN_EINVAL).
  * A sequence longer than its block table (KVARN_FLAG_BAD_LENGTH), or with tiles to evict and a
  * block outside [0, num_blocks) among its n (KVARN_FLAG_BAD_BLOCK), is left as it is: its
  * lengths and weights are copied and its kept is 0 .. n - 1.

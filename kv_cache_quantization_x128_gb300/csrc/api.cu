@@ -67,6 +67,18 @@ kvarn_status need_ptr(const void* p, const char* name) {
   return KVARN_OK;
 }
 
+// A device buffer of a call, by the bytes that the call may touch.
+struct Span {
+  const void* at;
+  uint64_t bytes;
+  const char* name;
+};
+
+bool overlap(const Span& x, const Span& y) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(x.at), q = reinterpret_cast<uintptr_t>(y.at);
+  return p < q ? q - p < x.bytes : p - q < y.bytes;
+}
+
 kvarn_status flags_ptr(unsigned** out) {
   const cudaError_t e = kvarn::flags_device_ptr(out);
   if (e != cudaSuccess) return fail(KVARN_ECUDA, "device flag word: %s", cudaGetErrorString(e));
@@ -273,8 +285,7 @@ kvarn_status kvarn_decode_attention_weights(const uint16_t* q, const uint8_t* ca
     return fail(KVARN_ESCRATCH, "scratch too small: need %lld bytes", static_cast<long long>(need));
   // (the merge's blocks read the rows of q for the workspace tokens while others write out)
   const uint64_t row_bytes = static_cast<uint64_t>(n_seqs) * meta->num_q_heads * KVARN_HEAD_DIM * sizeof(uint16_t);
-  const uintptr_t q_at = reinterpret_cast<uintptr_t>(q), out_at = reinterpret_cast<uintptr_t>(out);
-  if (q_at - out_at < row_bytes || out_at - q_at < row_bytes) return fail(KVARN_EINVAL, "out must not overlap q");
+  if (overlap({q, row_bytes, "q"}, {out, row_bytes, "out"})) return fail(KVARN_EINVAL, "out must not overlap q");
   unsigned* fl = nullptr;
   KV_TRY(flags_ptr(&fl));
   return cuda_status(kvarn::launch_decode_weights(q, cache, workspace, block_tables, seq_lens, n_seqs, meta->num_kv_heads,
@@ -302,11 +313,23 @@ kvarn_status kvarn_evict_tiles(const float* weights, float* weights_out, const i
   KV_TRY(need_ptr(weights_out, "weights_out"));
   KV_TRY(need_ptr(seq_lens, "seq_lens"));
   KV_TRY(need_ptr(seq_lens_out, "seq_lens_out"));
-  if (seq_lens_out == seq_lens) return fail(KVARN_EINVAL, "seq_lens_out must not alias seq_lens");
   KV_TRY(need_ptr(block_tables, "block_tables"));
   KV_TRY(need_ptr(budgets, "budgets"));
   KV_TRY(need_ptr(kept, "kept"));
   KV_TRY(need_ptr(cache, "cache"));
+  // The blocks of a sequence's kv-heads read its length, budget and table, and those that move records read them again,
+  // while others write: each output lies apart from the inputs (but weights_out may be weights) and the other outputs.
+  const uint64_t rows = static_cast<uint64_t>(n_seqs) * 4, table = rows * meta->max_blocks_per_seq,
+                 entries = table * meta->num_kv_heads;
+  const Span outs[3] = {{weights_out, entries, "weights_out"}, {kept, entries, "kept"}, {seq_lens_out, rows, "seq_lens_out"}};
+  const Span ins[4] = {{weights, entries, "weights"}, {seq_lens, rows, "seq_lens"}, {block_tables, table, "block_tables"},
+                       {budgets, rows, "budgets"}};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = i == 0 && weights_out == weights ? 1 : 0; j < 4; ++j)
+      if (overlap(outs[i], ins[j])) return fail(KVARN_EINVAL, "%s must not overlap %s", outs[i].name, ins[j].name);
+    for (int j = i + 1; j < 3; ++j)
+      if (overlap(outs[i], outs[j])) return fail(KVARN_EINVAL, "%s must not overlap %s", outs[i].name, outs[j].name);
+  }
   unsigned* fl = nullptr;
   KV_TRY(flags_ptr(&fl));
   return cuda_status(kvarn::launch_evict(weights, weights_out, seq_lens, seq_lens_out, block_tables, budgets, n_seqs,
