@@ -474,7 +474,9 @@ KVARN_API kvarn_status kvarn_qk_norm_rope(const void* q, const void* k, const vo
  * other, or dealt in turn. A token of text has the same position on every axis, and is then
  * rotated as by kvarn_qk_norm_rope, to the bit. axes is a host pointer, read before the call
  * returns; inv_freq is required; all else is kvarn_qk_norm_rope's.
- *   positions     int32 [n_axes][position_stride], n_tokens of each row used.
+ *   positions     int32 [n_axes][position_stride], n_tokens of each row used. Its start is 16-byte
+ *                 aligned like every pointer's (a chunk of longer rows starts at a multiple of four
+ *                 tokens, or is copied); the other rows lie where the stride puts them.
  */
 KVARN_API kvarn_status kvarn_qk_norm_rope_axes(const void* q, const void* k, const void* v, const kvarn_rope* rope,
                                                const kvarn_axes* axes, const void* q_weight, const void* k_weight,

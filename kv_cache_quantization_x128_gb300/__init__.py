@@ -369,8 +369,10 @@ def kvarn_qk_norm_rope(q, k, v, positions, q_out, k_out, v_out, meta: KvarnMeta,
 def kvarn_qk_norm_rope_axes(q, k, v, positions, axes, q_out, k_out, v_out, meta: KvarnMeta, q_weight=None, k_weight=None,
                             norm_eps: float = 1e-6, inv_freq=None, interleaved: bool = False, stream=None):
     """kvarn_qk_norm_rope for tokens with a position on each of several axes (time, height,
-    width): positions int32 [n_axes, n] (rows at any stride, or one row expanded); axes: for each of the
-    rotary_dim / 2 pairs its axis, a sequence of whole numbers as long as inv_freq."""
+    width): positions int32 [n_axes, n] (rows at any stride, or one row expanded; the first starts 16-byte
+    aligned, so columns [:, start:end] of longer rows can be given where start is a multiple of four, and
+    have to be copied by the caller otherwise); axes: for each of the rotary_dim / 2 pairs its axis, a
+    sequence of whole numbers as long as inv_freq."""
     import torch
     n = int(q.shape[0])
     if positions.dim() != 2 or positions.shape[1] != n:
