@@ -288,7 +288,9 @@ __device__ __forceinline__ void weigh_ws(const WeighArgs& a, int64_t u, int n_ws
     }
   }
   constexpr float kScale = kLog2e * kInvSqrt128, kUp = 32768.f;
-  float p[2][2], mx = -INFINITY, sum = 0.f;        // tokens t0 + 8 nt + 2 c + {0, 1} of head g
+  // tokens t0 + 8 nt + 2 c + {0, 1} of head g. The maximum starts finite, below every finite score (|q.k| < 2^40), so that
+  // scores of minus infinity (keys beyond fp16's end), even of all the rows, are weights of 0.
+  float p[2][2], mx = -1e30f, sum = 0.f;
 #pragma unroll
   for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -297,12 +299,11 @@ __device__ __forceinline__ void weigh_ws(const WeighArgs& a, int64_t u, int n_ws
       mx = fmaxf(mx, p[nt][e]);
     }
   mx = quad_max(mx);
-  const float base = mx == -INFINITY ? 0.f : mx;   // (scores of minus infinity, of keys beyond fp16's end, are no weight)
 #pragma unroll
   for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      p[nt][e] = exp2f(p[nt][e] - base);
+      p[nt][e] = exp2f(p[nt][e] - mx);
       sum += p[nt][e];
     }
   sum = quad_sum(sum);
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(32 * kHeads * kShares, kHeads * kShares > 8 ? 
     for (int k = 0; k < 4; ++k) acc[k] *= kInvSqrt128;
     float tail = 0.f;
     for (int w = 0; w < n_wsw; ++w) {
-      const float f = ws.l[w][wg] == 0.f ? 0.f : exp2f(ws.m[w][wg] - Mt);
+      const float f = exp2f(ws.m[w][wg] - Mt);
       const float4 v = *reinterpret_cast<const float4*>(&ws.o[w][wg][4 * lane]);
       acc[0] = fmaf(v.x, f, acc[0]);
       acc[1] = fmaf(v.y, f, acc[1]);
@@ -499,8 +500,10 @@ __global__ void __launch_bounds__(32 * kHeads * kShares, kHeads * kShares > 8 ? 
     }
   }
   if (kHeads == 8) {
+    // (the length is read again, not held: that spills, and 256 x 1000 tokens take 105 us instead of 103.3)
+    const int again = seq_len(a, s);
     __syncthreads();
-    weigh_unit(a, u, len, heads, threadIdx.x, blockDim.x);
+    weigh_unit(a, u, again, heads, threadIdx.x, blockDim.x);
   }
 }
 
