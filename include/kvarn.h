@@ -288,8 +288,11 @@ KVARN_API size_t kvarn_decode_weights_scratch_bytes(const kvarn_meta* meta, int3
 
 /*
  * Decode attention that also accumulates each tile's attention weight, for eviction
- * (kvarn_evict_tiles; a reading of this library, the pages are silent on it). out is
- * kvarn_decode_attention's; with p_gj the softmax weight that q-head g gives token j,
+ * (kvarn_evict_tiles; a reading of this library, the pages are silent on it). It is the only call that
+ * does: kvarn_prefill_attention's prompt tokens and kvarn_tree_attention's drafted ones leave no
+ * weight, so that an eviction right behind a prefill goes by whatever weights holds, and by
+ * slot where that is 0 everywhere (the lowest ones stay).
+ * out is kvarn_decode_attention's; with p_gj the softmax weight that q-head g gives token j,
  *   weights[s][h][t] <- decay * weights[s][h][t] + sum of p_gj over kv-head h's q-heads and
  *                       the tokens j of tile t (128 t .. 128 t + 127)
  * for t = 0 .. ceil(L/128) - 1; entries behind them stay as they are. The workspace's tokens

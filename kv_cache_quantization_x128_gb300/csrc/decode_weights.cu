@@ -23,7 +23,9 @@
 // legacy products are what small N needs, decode_tc.cuh has the tcgen05 form), 890 instructions of the ALU
 // pipe, two cycles each, and about 850 cycles of the fp32 pipe, which hardly overlap: measured 4110
 // cycles, ncu 50, 43 and 22 % of them. 64 x 16384 tokens, 64 heads over 8, k4v2: 236 us, 4.0 TB/s of records
-// (60 % of the copy rate; the plain decode 239), with groups of four 176 us, 80 %.
+// (60 % of the copy rate; the plain decode 239), with groups of four 178 us, 79 %. Batches of short sequences: 256 x 1000
+// tokens 103 us, of which the merge has 40 %: a chain of dependent loads a block, which hardly starts beside
+// the split, whose CTAs hold nearly all shared memory (alone, ncu: split 64 us, merge 45).
 #include "decode_tile.cuh"
 #include "kvarn_common.cuh"
 #include "kvarn_launch.h"

@@ -8,9 +8,11 @@
 // kv-head instead of nearly b, and a sequence one tile above its budget keep_last + 1.
 //
 // evict_select_kernel - a block per (sequence, kv-head), about two tiles a thread. The
-//   smallest weight that stays is found two bits at a time from the top (search_warp); ranks by ballots give
-//   the slots. No atomics: the same slots at every call. Bound by latency: a chain of two loads, the
-//   search, two barriers a count (128 tiles 5.6 us, 1024 tiles 8.2, 2048 blocks at once 8.6).
+//   smallest weight that stays is found two bits at a time from the top, by one warp without a barrier for up to 512
+//   tiles to choose from (search_warp), else by the block with a barrier a count (search_block); ranks by ballots,
+//   two barriers each, give the slots. No atomics: the same slots at every call. Bound by latency: a thread's first
+//   weights and table entries are loaded with the length and the budget, then come the search, the
+//   ranks and the lists (128 tiles 5.6 us, 1024 tiles 8.2, 2048 blocks of up to 256 at once 8.8).
 // evict_move_kernel - the copies, at the rate of a plain copy (16 x 16384 tokens to half, k4v2: 20 us of 127 MB).
 //   An evicted slot below b starts a path: it takes the record of slot kept[.], whose place, where it is
 //   below b itself, takes the next. Paths share no slot, so blocks take paths independently, and a thread
@@ -48,7 +50,8 @@ constexpr int kEvictMaxThreads = 1024;
 constexpr int kKeySlots = 10240;
 constexpr int kListSlots = 5120;      // the most blocks of a row whose list is held beside the keys
 // Up to so many tiles to choose from are one warp's: every warp of a block with tiles of its own and barriers between
-// the counts took 2048 blocks of 256 tiles 22 us, bound by instructions, where the warp takes 11.
+// the counts took 2048 blocks of 256 tiles 22 us, bound by instructions, where the warp took 11 (8.8 since the first
+// loads go out together).
 constexpr int kWarpTiles = 512;
 static_assert(kWarpTiles <= kKeySlots, "its keys, of places 0 .. kWarpTiles - 1, are held");
 constexpr int kMoveThreads = 128;

@@ -305,7 +305,10 @@ __device__ __forceinline__ void weigh_values(const uint8_t* rec, float2 (&sc)[16
 // for g < 4, its lo part else), and holds, of heads 2 (c % 2) + {0, 1}: the scores of tokens 16 b + g + 8 (c / 2);
 // maximum and sum; and acc[2 n + e] = the part of channel 16 n + 8 e + g that came through hi columns
 // (c < 2) or lo columns, added up when the record is written.
-// 64 x 16384 tokens, 32 heads over 8: k4v2 176 us (the wide form 234), k4v4 224 (274), k2v2 173 (231).
+// 64 x 16384 tokens, 32 heads over 8: k4v2 175 us (the wide form 234), k4v4 224 (274), k2v2 174 (231).
+// Nothing is at its limit: 1793 instructions a tile and kv-head with 2-bit keys, 1796 with 4-bit ones, of which 949 and
+// 920 are the ALU pipe's (ncu 61 and 59 % of it; tensor pipe 33, fp32 19 and 20, issue 58), on three warps a scheduler. The
+// fold is a part of them that is done twice: lanes g and g + 4 fold the same head, and each keeps one of its parts.
 
 // x of head g % 4, the same in a quad, for the thread's two heads.
 __device__ __forceinline__ float2 two_heads(float x, int c) {
